@@ -20,7 +20,9 @@ real-valued calls ``sc_causal_conv_fixed_f32``, ``sc_causal_conv_fixed_f32_ws``,
 ``sc_fixed_range_ok`` and :func:`causal_conv_fixed`; and for a filter shared by the batch
 ``sc_filter_spectrum_bytes``, ``sc_filter_spectrum_{f32,bf16}``, ``sc_causal_conv_spec_{f32,bf16}``,
 ``sc_causal_conv_shared_{f32,bf16}`` with :func:`filter_spectrum`, :func:`causal_conv_spec`,
-:func:`causal_conv_shared`.
+:func:`causal_conv_shared`.  The layers beside the convolution (layer norm, gated recurrence,
+causal attention, each with its backward pass) are in :mod:`fft_causal_long_amd.layers` and
+re-exported here.
 """
 from __future__ import annotations
 
@@ -748,3 +750,10 @@ def gate_conv_blc(v: torch.Tensor, s: torch.Tensor, W: torch.Tensor,
     if st != SC_OK:
         raise SpecConvError(st, "gate_conv_blc")
     return out
+
+
+# the layers beside the convolution use the handle and the helpers above
+from . import layers as _layers  # noqa: E402
+from .layers import *  # noqa: E402,F401,F403
+
+__all__ += _layers.__all__

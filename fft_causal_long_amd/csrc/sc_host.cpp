@@ -1620,6 +1620,6 @@ sc_status sc_prepare(sc_kind kind, int64_t L)
     });
 }
 
-int sc_version(void) { return 902; }
+int sc_version(void) { return 1000; }
 
 }  // extern "C"

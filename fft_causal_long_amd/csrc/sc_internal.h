@@ -261,4 +261,72 @@ hipError_t launch_transpose(int elt_bytes, const void* src0, void* dst0, const v
 hipError_t launch_gate(Store st, bool token_major, const void* s, const void* W, void* g,
                        int64_t nb, int64_t C, int64_t cw, int64_t L, int64_t gcs, hipStream_t s_);
 
+// ---- layers beside the convolution
+
+// Layer norm of `rows` rows of C values (xs, ys: row strides in elements); w, b, mean, rstd may
+// be null.  The backward pass writes dx and, where not null, dw and db (C sums over the rows),
+// through layernorm_bwd_bytes(...) bytes of ws (needed only with dw or db).
+hipError_t launch_layernorm(Store st, const void* x, const void* w, const void* b, void* y,
+                            float* mean, float* rstd, int64_t rows, int C, int64_t xs, int64_t ys,
+                            float eps, hipStream_t stream);
+size_t layernorm_bwd_bytes(Store st, int64_t rows, int C);
+hipError_t launch_layernorm_bwd(Store st, const void* dy, const void* x, const void* w,
+                                const float* mean, const float* rstd, void* dx, void* dw, void* db,
+                                int64_t rows, int C, int64_t dys, int64_t xs, int64_t dxs,
+                                void* ws, hipStream_t stream);
+
+// Gated recurrence h_t = f_t h_{t-1} + (1 - f_t) u_t, f = sigmoid(z), over token-major (B, L, C)
+// arrays whose tokens lie zs, us, ... elements apart (batch rows L tokens apart); states (B, C)
+// float32, null states are zero (inputs) or not wanted (outputs).  whole: every array's rows all
+// start 16-byte aligned.  recur_bytes(...) bytes of ws, either direction.
+struct RecurFwd {
+    const void *z, *u;
+    void* h;
+    const float* h0;
+    float* hT;
+    int64_t zs, us, hs;
+    int whole;
+};
+struct RecurBwd {
+    const void *dh, *z, *u, *h;
+    void *dz, *du;
+    const float *h0, *dhT;
+    float* dh0;
+    int64_t dhs, zs, us, hs, dzs, dus;
+    int whole;
+};
+size_t recur_bytes(int64_t B, int64_t L, int C);
+hipError_t launch_recur(Store st, const RecurFwd& r, int64_t B, int64_t L, int C, void* ws,
+                        hipStream_t stream);
+hipError_t launch_recur_bwd(Store st, const RecurBwd& r, int64_t B, int64_t L, int C, void* ws,
+                            hipStream_t stream);
+
+// Causal attention (sc_attn.hip, sc_attn_bwd.hip).  Strides in elements: batch, token, head; the
+// head's D values are contiguous, D a multiple of 8 up to 128, every row 16-byte aligned.
+struct AttnArgs {
+    const void *q, *k, *v;
+    void* o;              // the backward pass reads it
+    float* lse;           // (B, H, Lq); the backward pass reads it
+    const void* dout;
+    void *dq, *dk, *dv;
+    int64_t qs[3], ks[3], vs[3], os[3], dos[3], dqs[3], dks[3], dvs[3];
+    const float* slopes;     // (H) or null
+    const int32_t* kv_len;   // (B) or null
+    const int32_t* doc;      // (B, Lk) or null
+    int B, H, Hkv, G, D, Lq, Lk;   // G = H / Hkv
+    int window;              // INT_MAX: none
+    float scale, cap;        // cap 0: none
+    int nrow, nbh;           // packed rows Lq G and key heads B Hkv of the call
+    // set by the launchers
+    int ntile, nsplit;
+    float *part, *part_lse;  // forward: the splits' results
+    float2* rowstat;         // backward: (lse in base 2, delta) of each packed row
+    int4* strips;            // backward: per 32-row strip the lowest and the highest key seen,
+                             // the highest first key and the lowest position
+};
+size_t attn_fwd_bytes(const AttnArgs& a);
+hipError_t launch_attn(Store st, const AttnArgs& a, void* ws, hipStream_t stream);
+size_t attn_bwd_bytes(const AttnArgs& a);
+hipError_t launch_attn_bwd(Store st, const AttnArgs& a, void* ws, hipStream_t stream);
+
 }  // namespace sc

@@ -1,0 +1,537 @@
+// Layer norm, forward and backward (gfx950).
+//
+// Row x of C values (the normalisation before a mixing layer, "Caracal: Causal Architecture
+// via Spectral Mixing", key design 1):
+//
+//     mean = sum x / C,  rstd = (sum (x - mean)^2 / C + eps)^-1/2,  y = (x - mean) rstd w + b
+//
+// and for the output gradient dy, with xh = (x - mean) rstd and e = dy w:
+//
+//     dx = rstd (e - mean(e) - xh mean(e xh)),   dw = sum_rows dy xh,   db = sum_rows dy
+//
+// Both directions are bound by memory: 2 elements a value forward, 3 backward.  A row is read
+// once and kept in registers by TPR threads (16, 64 or 256, NV vectors of 16 bytes each), so
+// the variance is the two-pass sum about the mean, exact to float32 rounding, at no second
+// read.  Backward, a workgroup walks rows and keeps its share of dw and db in registers; the
+// shares go to a workspace and a second kernel adds them in a fixed order: no atomics, the
+// same bits every run.
+// Rows longer than 8192 values do not fit the registers: they are read again from cache
+// (lnl_* kernels), and dw, db come from a kernel that walks the rows column by column.
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "sc_internal.h"
+#include "sc_rows.h"
+
+namespace sc {
+
+namespace {
+
+constexpr int NT = 256;          // threads
+constexpr int LNL_STRIPS = 64;   // row strips of the column kernel (long rows)
+
+// Sum of v over the TPR threads of a row, in every one of them.  TPR = 256 goes through
+// `red` (4 floats, one buffer per call so that one barrier is enough).
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* red)
+{
+#pragma unroll
+    for (int m = 1; m < (TPR < 64 ? TPR : 64); m <<= 1) v += __shfl_xor(v, m);
+    if constexpr (TPR > 64) {
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = (red[0] + red[1]) + (red[2] + red[3]);
+    }
+    return v;
+}
+
+template <class IO, int TPR, int NV>
+__global__ __launch_bounds__(NT) void ln_fwd(const typename IO::T* __restrict__ x,
+                                             const typename IO::T* __restrict__ w,
+                                             const typename IO::T* __restrict__ b,
+                                             typename IO::T* __restrict__ y,
+                                             float* __restrict__ mean, float* __restrict__ rstd,
+                                             int64_t rows, int C, int64_t xs, int64_t ys,
+                                             float eps, int whole, int wwhole)
+{
+    constexpr int V = vec_elems<IO>, RPB = NT / TPR;
+    __shared__ float red[2][2][4];   // double-buffered over the row loop
+    const int lt = threadIdx.x % TPR;
+    const float n = (float)C;
+    int buf = 0;
+    // every thread of a workgroup makes the same number of turns (the barriers of TPR = 256)
+    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < rows; r0 += (int64_t)gridDim.x * RPB) {
+        const int64_t row = r0 + threadIdx.x / TPR;
+        const bool on = row < rows;
+        const typename IO::T* xr = x + (on ? row : 0) * xs;
+        Lanes<IO> v[NV];
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + lt) * V;
+            v[i] = widen<IO>(c < C ? load_raw<IO>(xr, c, C, whole) : make_uint4(0, 0, 0, 0));
+#pragma unroll
+            for (int e = 0; e < V; ++e) s += v[i].x[e];
+        }
+        const float mu = row_sum<TPR>(s, red[buf][0]) / n;
+        float q = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + lt) * V;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                v[i].x[e] -= mu;
+                q += c + e < C ? v[i].x[e] * v[i].x[e] : 0.f;
+            }
+        }
+        const float var = row_sum<TPR>(q, red[buf][1]) / n;
+        const float rs = 1.0f / sqrtf(var + eps);
+        buf ^= 1;
+        if (!on) continue;
+        if (lt == 0) {
+            if (mean) mean[row] = mu;
+            if (rstd) rstd[row] = rs;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + lt) * V;
+            if (c >= C) continue;
+            Lanes<IO> o;
+            Lanes<IO> wv, bv;
+            if (w) wv = widen<IO>(load_raw<IO>(w, c, C, wwhole));
+            if (b) bv = widen<IO>(load_raw<IO>(b, c, C, wwhole));
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                float t = v[i].x[e] * rs;
+                if (w) t *= wv.x[e];
+                o.x[e] = b ? t + bv.x[e] : t;
+            }
+            store_raw<IO>(y + row * ys, c, C, whole, o);
+        }
+    }
+}
+
+template <class IO, int TPR, int NV>
+__global__ __launch_bounds__(NT) void ln_bwd(const typename IO::T* __restrict__ dy,
+                                             const typename IO::T* __restrict__ x,
+                                             const typename IO::T* __restrict__ w,
+                                             const float* __restrict__ mean,
+                                             const float* __restrict__ rstd,
+                                             typename IO::T* __restrict__ dx,
+                                             float* __restrict__ part, int64_t rows, int C,
+                                             int64_t dys, int64_t xs, int64_t dxs, int whole,
+                                             int wwhole)
+{
+    constexpr int V = vec_elems<IO>, RPB = NT / TPR;
+    __shared__ float red[2][2][4];
+    __shared__ float acc[RPB > 1 ? TPR * NV * V * 2 : 1];
+    const int lt = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+    const float n = (float)C;
+    Lanes<IO> wv[NV], aw[NV], ab[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + lt) * V;
+        if (w && c < C) wv[i] = widen<IO>(load_raw<IO>(w, c, C, wwhole));
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            if (!w) wv[i].x[e] = 1.f;
+            aw[i].x[e] = ab[i].x[e] = 0.f;
+        }
+    }
+    int buf = 0;
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    uint4 nx[NV], ny[NV];   // the next row, in flight while this one is reduced
+    float nmu = 0.f, nrs = 0.f;
+    auto fetch = [&](int64_t row) {
+        const bool on = row < rows;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + lt) * V;
+            const bool in = on && c < C;
+            nx[i] = in ? load_raw<IO>(x + row * xs, c, C, whole) : make_uint4(0, 0, 0, 0);
+            ny[i] = in ? load_raw<IO>(dy + row * dys, c, C, whole) : make_uint4(0, 0, 0, 0);
+        }
+        nmu = on ? mean[row] : 0.f;
+        nrs = on ? rstd[row] : 0.f;
+    };
+    fetch((int64_t)blockIdx.x * RPB + grp);
+    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < rows; r0 += step) {
+        const int64_t row = r0 + grp;
+        Lanes<IO> xh[NV], g[NV];
+        const float mu = nmu, rs = nrs;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            xh[i] = widen<IO>(nx[i]);
+            g[i] = widen<IO>(ny[i]);
+        }
+        fetch(row + step);
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + lt) * V;
+            if (c < C) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    // past the row's end dy reads 0, so nothing below counts there
+                    xh[i].x[e] = (xh[i].x[e] - mu) * rs;
+                    ab[i].x[e] += g[i].x[e];
+                    aw[i].x[e] = __builtin_fmaf(g[i].x[e], xh[i].x[e], aw[i].x[e]);
+                    g[i].x[e] *= wv[i].x[e];
+                    s1 += g[i].x[e];
+                    s2 = __builtin_fmaf(g[i].x[e], xh[i].x[e], s2);
+                }
+            }
+        }
+        const float m1 = row_sum<TPR>(s1, red[buf][0]) / n;
+        const float m2 = row_sum<TPR>(s2, red[buf][1]) / n;
+        buf ^= 1;
+        if (row >= rows) continue;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + lt) * V;
+            if (c >= C) continue;
+            Lanes<IO> o;
+#pragma unroll
+            for (int e = 0; e < V; ++e) o.x[e] = rs * (g[i].x[e] - m1 - xh[i].x[e] * m2);
+            store_raw<IO>(dx + row * dxs, c, C, whole, o);
+        }
+    }
+    if (!part) return;
+    float* mine = part + (int64_t)blockIdx.x * 2 * C;
+    if constexpr (RPB == 1) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const int c = (i * TPR + lt) * V + e;
+                if (c < C) {
+                    mine[c] = aw[i].x[e];
+                    mine[C + c] = ab[i].x[e];
+                }
+            }
+    } else {
+        // the row groups' shares, added in order
+        constexpr int W = TPR * NV * V;
+        for (int k = 0; k < RPB; ++k) {
+            __syncthreads();
+            if (grp == k) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        const int c = (i * TPR + lt) * V + e;
+                        acc[c] = k ? acc[c] + aw[i].x[e] : aw[i].x[e];
+                        acc[W + c] = k ? acc[W + c] + ab[i].x[e] : ab[i].x[e];
+                    }
+            }
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < C; c += NT) {
+            mine[c] = acc[c];
+            mine[C + c] = acc[W + c];
+        }
+    }
+}
+
+// dw, db from n shares of 2 C sums each: 32 columns and 32 share lanes per workgroup
+template <class IO>
+__global__ __launch_bounds__(1024) void ln_params(const float* __restrict__ part, int n, int C,
+                                                  typename IO::T* __restrict__ dw,
+                                                  typename IO::T* __restrict__ db)
+{
+    __shared__ float s[32][33];
+    const int cl = threadIdx.x & 31, pl = threadIdx.x >> 5;
+    const int64_t col = (int64_t)blockIdx.x * 32 + cl;   // of the 2 C columns
+    float v = 0.f;
+    if (col < 2 * (int64_t)C)
+        for (int p = pl; p < n; p += 32) v += part[(int64_t)p * 2 * C + col];
+    s[pl][cl] = v;
+    __syncthreads();
+    if (pl == 0 && col < 2 * (int64_t)C) {
+        float t = 0.f;
+#pragma unroll
+        for (int p = 0; p < 32; ++p) t += s[p][cl];
+        if (col < C) {
+            if (dw) IO::store(dw, col, t);
+        } else if (db) {
+            IO::store(db, col - C, t);
+        }
+    }
+}
+
+// ---- rows longer than the registers hold: one workgroup per row, the row re-read from cache
+
+template <class IO>
+__global__ __launch_bounds__(NT) void lnl_fwd(const typename IO::T* __restrict__ x,
+                                              const typename IO::T* __restrict__ w,
+                                              const typename IO::T* __restrict__ b,
+                                              typename IO::T* __restrict__ y,
+                                              float* __restrict__ mean, float* __restrict__ rstd,
+                                              int64_t rows, int C, int64_t xs, int64_t ys,
+                                              float eps, int whole, int wwhole)
+{
+    constexpr int V = vec_elems<IO>;
+    __shared__ float red[2][2][4];
+    int buf = 0;
+    const float n = (float)C;
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+        const typename IO::T* xr = x + row * xs;
+        float s = 0.f;
+        for (int64_t c = threadIdx.x * V; c < C; c += NT * V) {
+            const Lanes<IO> v = widen<IO>(load_raw<IO>(xr, (int)c, C, whole));
+#pragma unroll
+            for (int e = 0; e < V; ++e) s += v.x[e];
+        }
+        const float mu = row_sum<NT>(s, red[buf][0]) / n;
+        float q = 0.f;
+        for (int64_t c = threadIdx.x * V; c < C; c += NT * V) {
+            const Lanes<IO> v = widen<IO>(load_raw<IO>(xr, (int)c, C, whole));
+#pragma unroll
+            for (int e = 0; e < V; ++e) q += c + e < C ? (v.x[e] - mu) * (v.x[e] - mu) : 0.f;
+        }
+        const float rs = 1.0f / sqrtf(row_sum<NT>(q, red[buf][1]) / n + eps);
+        buf ^= 1;
+        if (threadIdx.x == 0) {
+            if (mean) mean[row] = mu;
+            if (rstd) rstd[row] = rs;
+        }
+        for (int64_t c = threadIdx.x * V; c < C; c += NT * V) {
+            Lanes<IO> v = widen<IO>(load_raw<IO>(xr, (int)c, C, whole));
+            Lanes<IO> wv, bv;
+            if (w) wv = widen<IO>(load_raw<IO>(w, (int)c, C, wwhole));
+            if (b) bv = widen<IO>(load_raw<IO>(b, (int)c, C, wwhole));
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                float t = (v.x[e] - mu) * rs;
+                if (w) t *= wv.x[e];
+                v.x[e] = b ? t + bv.x[e] : t;
+            }
+            store_raw<IO>(y + row * ys, (int)c, C, whole, v);
+        }
+    }
+}
+
+template <class IO>
+__global__ __launch_bounds__(NT) void lnl_bwd(const typename IO::T* __restrict__ dy,
+                                              const typename IO::T* __restrict__ x,
+                                              const typename IO::T* __restrict__ w,
+                                              const float* __restrict__ mean,
+                                              const float* __restrict__ rstd,
+                                              typename IO::T* __restrict__ dx, int64_t rows, int C,
+                                              int64_t dys, int64_t xs, int64_t dxs, int whole,
+                                              int wwhole)
+{
+    constexpr int V = vec_elems<IO>;
+    __shared__ float red[2][2][4];
+    int buf = 0;
+    const float n = (float)C;
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+        const float mu = mean[row], rs = rstd[row];
+        auto terms = [&](int c, Lanes<IO>& e, Lanes<IO>& xh) {
+            e = widen<IO>(load_raw<IO>(dy + row * dys, c, C, whole));
+            xh = widen<IO>(load_raw<IO>(x + row * xs, c, C, whole));
+            Lanes<IO> wv;
+            if (w) wv = widen<IO>(load_raw<IO>(w, c, C, wwhole));
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                xh.x[i] = (xh.x[i] - mu) * rs;
+                if (w) e.x[i] *= wv.x[i];
+            }
+        };
+        float s1 = 0.f, s2 = 0.f;
+        for (int64_t c = threadIdx.x * V; c < C; c += NT * V) {
+            Lanes<IO> e, xh;
+            terms((int)c, e, xh);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                s1 += e.x[i];
+                s2 = __builtin_fmaf(e.x[i], xh.x[i], s2);
+            }
+        }
+        const float m1 = row_sum<NT>(s1, red[buf][0]) / n;
+        const float m2 = row_sum<NT>(s2, red[buf][1]) / n;
+        buf ^= 1;
+        for (int64_t c = threadIdx.x * V; c < C; c += NT * V) {
+            Lanes<IO> e, xh;
+            terms((int)c, e, xh);
+#pragma unroll
+            for (int i = 0; i < V; ++i) e.x[i] = rs * (e.x[i] - m1 - xh.x[i] * m2);
+            store_raw<IO>(dx + row * dxs, (int)c, C, whole, e);
+        }
+    }
+}
+
+// shares of dw, db: workgroup (strip, column block) walks the rows of its strip
+template <class IO>
+__global__ __launch_bounds__(NT) void lnl_params(const typename IO::T* __restrict__ dy,
+                                                 const typename IO::T* __restrict__ x,
+                                                 const float* __restrict__ mean,
+                                                 const float* __restrict__ rstd,
+                                                 float* __restrict__ part, int64_t rows, int C,
+                                                 int64_t dys, int64_t xs)
+{
+    const int c = blockIdx.x * NT + threadIdx.x, strip = blockIdx.y;
+    if (c >= C) return;
+    float aw = 0.f, ab = 0.f;
+    for (int64_t row = strip; row < rows; row += LNL_STRIPS) {
+        const float g = IO::load(dy, row * dys + c);
+        ab += g;
+        aw = __builtin_fmaf(g, (IO::load(x, row * xs + c) - mean[row]) * rstd[row], aw);
+    }
+    float* mine = part + (int64_t)strip * 2 * C;
+    mine[c] = aw;
+    mine[C + c] = ab;
+}
+
+// Threads per row and vectors per thread for rows of C values: the fewest threads whose
+// registers hold the row (16 or 64 threads need no barrier).
+struct RowPlan {
+    int tpr, nv;   // nv 0: the row does not fit
+};
+
+RowPlan row_plan(int C, int V)
+{
+    const int vecs = (C + V - 1) / V;
+    if (vecs <= 16) return {16, 1};
+    if (vecs <= 64) return {64, 1};
+    if (vecs <= 128) return {64, 2};
+    if (vecs <= 256) return {64, 4};
+    if (vecs <= 512) return {256, 2};
+    if (vecs <= 1024) return {256, 4};
+    if (vecs <= 2048 && V == 4) return {256, 8};
+    return {256, 0};
+}
+
+// calls f(std::integral_constant<TPR>, std::integral_constant<NV>) for the plan
+template <class F>
+hipError_t with_plan(const RowPlan& p, F&& f)
+{
+    using std::integral_constant;
+    if (p.tpr == 16) return f(integral_constant<int, 16>(), integral_constant<int, 1>());
+    if (p.tpr == 64 && p.nv == 1) return f(integral_constant<int, 64>(), integral_constant<int, 1>());
+    if (p.tpr == 64 && p.nv == 2) return f(integral_constant<int, 64>(), integral_constant<int, 2>());
+    if (p.tpr == 64) return f(integral_constant<int, 64>(), integral_constant<int, 4>());
+    if (p.nv == 2) return f(integral_constant<int, 256>(), integral_constant<int, 2>());
+    if (p.nv == 4) return f(integral_constant<int, 256>(), integral_constant<int, 4>());
+    return f(integral_constant<int, 256>(), integral_constant<int, 8>());
+}
+
+// Workgroups of the backward kernel: each writes 2 C sums, so no more than fill the GPU.
+constexpr int64_t BWD_BLOCKS = 1024;
+
+int64_t bwd_blocks(int64_t rows, const RowPlan& p)
+{
+    const int64_t rpb = NT / p.tpr;
+    return std::min<int64_t>(BWD_BLOCKS, (rows + rpb - 1) / rpb);
+}
+
+bool aligned_rows(const void* p, int64_t stride, size_t es)
+{
+    return (uintptr_t)p % 16 == 0 && stride * (int64_t)es % 16 == 0;
+}
+
+template <class IO>
+hipError_t fwd(const void* x, const void* w, const void* b, void* y, float* mean, float* rstd,
+               int64_t rows, int C, int64_t xs, int64_t ys, float eps, hipStream_t st)
+{
+    using E = typename IO::T;
+    const RowPlan p = row_plan(C, vec_elems<IO>);
+    const int whole = aligned_rows(x, xs, sizeof(E)) && aligned_rows(y, ys, sizeof(E));
+    const int ww = (!w || (uintptr_t)w % 16 == 0) && (!b || (uintptr_t)b % 16 == 0);
+    // the row loop covers what a grid of this many workgroups leaves
+    const int64_t rpb = NT / p.tpr, blocks = std::min<int64_t>((rows + rpb - 1) / rpb, 1 << 20);
+    if (p.nv == 0) {
+        hipLaunchKernelGGL((lnl_fwd<IO>), dim3((unsigned)blocks), dim3(NT), 0, st, (const E*)x,
+                           (const E*)w, (const E*)b, (E*)y, mean, rstd, rows, C, xs, ys, eps,
+                           whole, ww);
+        return hipGetLastError();
+    }
+    return with_plan(p, [&](auto tpr, auto nv) {
+        if constexpr (decltype(nv)::value == 8 && IO::SIZE == 2) return hipErrorInvalidValue;
+        else {
+            hipLaunchKernelGGL((ln_fwd<IO, decltype(tpr)::value, decltype(nv)::value>),
+                               dim3((unsigned)blocks), dim3(NT), 0, st, (const E*)x, (const E*)w,
+                               (const E*)b, (E*)y, mean, rstd, rows, C, xs, ys, eps, whole, ww);
+            return hipGetLastError();
+        }
+    });
+}
+
+template <class IO>
+hipError_t bwd(const void* dy, const void* x, const void* w, const float* mean, const float* rstd,
+               void* dx, void* dw, void* db, int64_t rows, int C, int64_t dys, int64_t xs,
+               int64_t dxs, float* part, hipStream_t st)
+{
+    using E = typename IO::T;
+    const RowPlan p = row_plan(C, vec_elems<IO>);
+    const int whole = aligned_rows(dy, dys, sizeof(E)) && aligned_rows(x, xs, sizeof(E)) &&
+                      aligned_rows(dx, dxs, sizeof(E));
+    const int ww = !w || (uintptr_t)w % 16 == 0;
+    const bool params = dw || db;
+    int64_t shares = 0;
+    hipError_t e = hipSuccess;
+    if (p.nv == 0) {
+        const int64_t blocks = std::min<int64_t>(rows, 1 << 20);
+        if (blocks > 0) {
+            hipLaunchKernelGGL((lnl_bwd<IO>), dim3((unsigned)blocks), dim3(NT), 0, st,
+                               (const E*)dy, (const E*)x, (const E*)w, mean, rstd, (E*)dx, rows, C,
+                               dys, xs, dxs, whole, ww);
+            e = hipGetLastError();
+        }
+        if (e == hipSuccess && params && rows > 0) {
+            shares = LNL_STRIPS;
+            hipLaunchKernelGGL((lnl_params<IO>), dim3((unsigned)((C + NT - 1) / NT), LNL_STRIPS),
+                               dim3(NT), 0, st, (const E*)dy, (const E*)x, mean, rstd, part, rows,
+                               C, dys, xs);
+            e = hipGetLastError();
+        }
+    } else if (rows > 0) {
+        shares = bwd_blocks(rows, p);
+        e = with_plan(p, [&](auto tpr, auto nv) {
+            if constexpr (decltype(nv)::value == 8 && IO::SIZE == 2) return hipErrorInvalidValue;
+            else {
+                hipLaunchKernelGGL((ln_bwd<IO, decltype(tpr)::value, decltype(nv)::value>),
+                                   dim3((unsigned)shares), dim3(NT), 0, st, (const E*)dy,
+                                   (const E*)x, (const E*)w, mean, rstd, (E*)dx,
+                                   params ? part : nullptr, rows, C, dys, xs, dxs, whole, ww);
+                return hipGetLastError();
+            }
+        });
+    }
+    if (e != hipSuccess || !params) return e;
+    hipLaunchKernelGGL((ln_params<IO>), dim3((unsigned)((2 * (int64_t)C + 31) / 32)), dim3(1024), 0,
+                       st, part, (int)shares, C, (E*)dw, (E*)db);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_layernorm(Store s, const void* x, const void* w, const void* b, void* y,
+                            float* mean, float* rstd, int64_t rows, int C, int64_t xs, int64_t ys,
+                            float eps, hipStream_t st)
+{
+    return s == Store::F32 ? fwd<f32_io>(x, w, b, y, mean, rstd, rows, C, xs, ys, eps, st)
+                           : fwd<bf16_io>(x, w, b, y, mean, rstd, rows, C, xs, ys, eps, st);
+}
+
+size_t layernorm_bwd_bytes(Store s, int64_t rows, int C)
+{
+    const RowPlan p = row_plan(C, s == Store::F32 ? 4 : 8);
+    const int64_t shares = p.nv == 0 ? (rows > 0 ? LNL_STRIPS : 0) : bwd_blocks(rows, p);
+    return (size_t)shares * 2 * (size_t)C * sizeof(float);
+}
+
+hipError_t launch_layernorm_bwd(Store s, const void* dy, const void* x, const void* w,
+                                const float* mean, const float* rstd, void* dx, void* dw, void* db,
+                                int64_t rows, int C, int64_t dys, int64_t xs, int64_t dxs,
+                                void* ws, hipStream_t st)
+{
+    return s == Store::F32
+               ? bwd<f32_io>(dy, x, w, mean, rstd, dx, dw, db, rows, C, dys, xs, dxs, (float*)ws, st)
+               : bwd<bf16_io>(dy, x, w, mean, rstd, dx, dw, db, rows, C, dys, xs, dxs, (float*)ws, st);
+}
+
+}  // namespace sc

@@ -414,6 +414,115 @@ sc_status sc_causal_conv_shared_bwd_bf16(const uint16_t* dr, const uint16_t* v, 
                                          int64_t L, hipStream_t stream);
 
 /*
+ * Layers beside the convolution.  A Caracal stack normalises before each mixing layer and puts
+ * a sliding-window attention layer after every two Fourier layers ("Caracal: Causal
+ * Architecture via Spectral Mixing", key designs 1 and 3); a gated recurrence is the mixing
+ * layer of the models it is compared with.  These calls take SC_KIND_F32 or SC_KIND_BF16 (else
+ * SC_ERR_INVALID_ARGUMENT), token-major activations, and keep every sum, statistic and state
+ * in float32; bfloat16 results are rounded once, nearest, ties to even.  Shared conventions:
+ *  - A "row stride" is the distance in elements between consecutive rows (tokens), so columns
+ *    of a wider array can be passed; the row itself is contiguous.  Inputs take any stride
+ *    >= 0, outputs one of at least the row's length.
+ *  - An output may share no element with an input or another output (SC_ERR_INVALID_ARGUMENT);
+ *    interleaved columns of one array are told apart when the row strides are equal.
+ *  - Rows that all start 16-byte aligned are moved in 16-byte vectors; others work, slower.
+ *  - ws: scratch of the call's *_workspace_bytes (256-byte aligned, overlapping nothing else),
+ *    or null with ws_bytes 0: the call then allocates it stream-ordered.
+ *  - No table is built: every call can be captured into a graph (give it a ws there).
+ *  - Sizes whose grid a launch cannot hold -> SC_ERR_UNSUPPORTED; the other errors as above.
+ *
+ * sc_layernorm -- y = (x - mean) rstd w + b per row of C values, mean = sum x / C,
+ *   rstd = (sum (x - mean)^2 / C + eps)^-1/2 (the sum is taken about the mean).  w, b: C
+ *   values or null (1, 0); mean, rstd: rows float32 values or null (not wanted).  eps >= 0.
+ *   A row of NaN or infinity affects itself only.  C <= 2^30.
+ * sc_layernorm_bwd -- for the output gradient dy, with xh = (x - mean) rstd and e = dy w:
+ *     dx = rstd (e - mean(e) - xh mean(e xh)),  dw = sum_rows dy xh,  db = sum_rows dy
+ *   mean, rstd as the forward call returned them; dw, db null: not wanted (no ws then).  With
+ *   rows = 0 and C > 0, dw and db are set to zero.
+ */
+sc_status sc_layernorm(sc_kind kind, const void* x, const void* w, const void* b, void* y,
+                       float* mean, float* rstd, int64_t rows, int64_t C, int64_t x_stride,
+                       int64_t y_stride, float eps, hipStream_t stream);
+size_t sc_layernorm_bwd_workspace_bytes(sc_kind kind, int64_t rows, int64_t C);
+sc_status sc_layernorm_bwd(sc_kind kind, const void* dy, const void* x, const void* w,
+                           const float* mean, const float* rstd, void* dx, void* dw, void* db,
+                           int64_t rows, int64_t C, int64_t dy_stride, int64_t x_stride,
+                           int64_t dx_stride, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * sc_recur -- the gated linear recurrence of each channel over the tokens of (B, L, C) arrays:
+ *     f_t = sigmoid(z_t),   h_t = f_t h_{t-1} + (1 - f_t) u_t,   t = 0 .. L-1
+ *   z, u, h: token t of batch row b starts (b L + t) * stride elements in.  h0: the state
+ *   before token 0, (B, C) float32, or null (zero); hT: the state after the last token, or
+ *   null.  hT may be h0 itself (the state of a decoding loop).  Both gates are computed from
+ *   exp(-|z|), so neither loses precision where the other saturates.  L = 1 is the step of a
+ *   decoding loop.  An empty sequence (L = 0) copies h0 (or zero) to hT.
+ * sc_recur_bwd -- for the output gradient dh and that of hT, dhT (null: zero):
+ *     g_t = dh_t + f_{t+1} g_{t+1}  (dhT after the last),   du_t = (1 - f_t) g_t,
+ *     dz_t = g_t (h_{t-1} - u_t) f_t (1 - f_t),             dh0 = f_0 g_0
+ *   h as the forward call returned it, h0 as it was given; dh0: (B, C) float32 or null.  dh0
+ *   may be dhT itself.  L = 0 copies dhT to dh0.
+ * Limits: C <= 2^30.  The order of every sum depends on the shape alone.
+ */
+size_t sc_recur_workspace_bytes(sc_kind kind, int64_t B, int64_t L, int64_t C);
+sc_status sc_recur(sc_kind kind, const void* z, const void* u, const float* h0, void* h, float* hT,
+                   int64_t B, int64_t L, int64_t C, int64_t z_stride, int64_t u_stride,
+                   int64_t h_stride, void* ws, size_t ws_bytes, hipStream_t stream);
+sc_status sc_recur_bwd(sc_kind kind, const void* dh, const void* z, const void* u, const void* h,
+                       const float* h0, const float* dhT, void* dz, void* du, float* dh0,
+                       int64_t B, int64_t L, int64_t C, int64_t dh_stride, int64_t z_stride,
+                       int64_t u_stride, int64_t h_stride, int64_t dz_stride, int64_t du_stride,
+                       void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Causal attention over a window of keys.  Query i < Lq of batch row b sits at position
+ * p = n_b - Lq + i, n_b = kv_len[b] (clamped to 0 .. Lk) or Lk without kv_len: Lq = Lk in
+ * training, fewer new queries over a longer cache when serving.  It sees key j when
+ *     max(0, p - window + 1, doc_start[b][p]) <= j <= p,   0 <= p < n_b,   doc_start[b][j] <= j
+ * doc_start (B, Lk) int32 holds the start of each token's document in a packed row; a token
+ * whose start lies after it is padding: its row is empty and no row sees it.  Then
+ *     x = scale q_i . k_j,   s = cap tanh(x / cap) (cap > 0) or x,   s -= slopes[h] (p - j)
+ *     o_i = sum_j softmax(s)_j v_j,   lse_i = log sum_j exp(s_j)
+ * and a row that sees nothing gives o = 0, lse = -infinity (and gradients of 0).  Head h of q
+ * reads key head h / (H / Hkv).  q, k, v of padding tokens and of keys at n_b and beyond may
+ * hold anything, NaN included; those of all other tokens must be finite (a NaN may reach other
+ * rows of its tile).
+ *
+ * sc_attn describes a call.  Strides are in elements, {batch, token, head}; the D values of a
+ * head are contiguous.  D is a multiple of 8, 8 <= D <= 128, H a multiple of Hkv, Lk and
+ * Lq H / Hkv at most 2^30 (else SC_ERR_UNSUPPORTED); pointers and strides that matter are
+ * multiples of 16 bytes, scale > 0 and finite, cap >= 0 and finite, window >= 0
+ * (0: no window) (else SC_ERR_INVALID_ARGUMENT).
+ *
+ *  sc_causal_attn -- o and, if lse is not null, lse (B, H, Lq) float32.  bfloat16 storage: the
+ *      weights are rounded to bfloat16 for the second product, sums stay float32.  When the
+ *      rows alone do not fill the GPU (decoding) the keys are split over workgroups and the
+ *      parts joined, through sc_attn_workspace_bytes(kind, a, 0) bytes of ws.
+ *  sc_causal_attn_bwd -- dq (strides dq), dk, dv (of key heads: summed over the heads that
+ *      share them) for the output gradient dout (strides dout), from the forward call's o and
+ *      lse; sc_attn_workspace_bytes(kind, a, 1) bytes of ws.  dk, dv are written for every key,
+ *      0 where no row sees it.
+ */
+typedef struct sc_attn {
+    int64_t B, Lq, Lk, H, Hkv, D;
+    int64_t q[3], k[3], v[3], o[3];          /* strides */
+    int64_t dout[3], dq[3], dk[3], dv[3];    /* strides, sc_causal_attn_bwd only */
+    float scale, cap;
+    int64_t window;
+    const float* slopes;       /* (H) or null: none             */
+    const int32_t* kv_len;     /* (B) or null: Lk               */
+    const int32_t* doc_start;  /* (B, Lk) or null: one document */
+} sc_attn;
+size_t sc_attn_workspace_bytes(sc_kind kind, const sc_attn* a, int backward);
+sc_status sc_causal_attn(sc_kind kind, const sc_attn* a, const void* q, const void* k,
+                         const void* v, void* o, float* lse, void* ws, size_t ws_bytes,
+                         hipStream_t stream);
+sc_status sc_causal_attn_bwd(sc_kind kind, const sc_attn* a, const void* dout, const void* q,
+                             const void* k, const void* v, const void* o, const float* lse,
+                             void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                             hipStream_t stream);
+
+/*
  * sc_ntt_range_ok -- 1 if every |v_j| <= max_abs_v and |g_j| <= max_abs_g guarantee that
  *   the exact sums fit the symmetric residue range, i.e. L * max_abs_v * max_abs_g <=
  *   (p-1)/2; 0 otherwise (or on negative arguments).  Host only.
@@ -455,7 +564,7 @@ sc_status sc_causal_conv_noalloc(sc_kind kind, const void* v, const void* g, voi
  */
 sc_status sc_prepare(sc_kind kind, int64_t L);
 
-/* Library version: major * 10000 + minor * 100 + patch (this header: 902).  Host only. */
+/* Library version: major * 10000 + minor * 100 + patch (this header: 1000).  Host only. */
 int sc_version(void);
 
 #ifdef __cplusplus
