@@ -48,19 +48,26 @@ __device__ __forceinline__ float row_sum(float v, float* red)
     return v;
 }
 
-template <class IO, int TPR, int NV>
+template <class IO, int TPR, int NV, bool WHOLE>
 __global__ __launch_bounds__(NT) void ln_fwd(const typename IO::T* __restrict__ x,
                                              const typename IO::T* __restrict__ w,
                                              const typename IO::T* __restrict__ b,
                                              typename IO::T* __restrict__ y,
                                              float* __restrict__ mean, float* __restrict__ rstd,
                                              int64_t rows, int C, int64_t xs, int64_t ys,
-                                             float eps, int whole, int wwhole)
+                                             float eps)
 {
     constexpr int V = vec_elems<IO>, RPB = NT / TPR;
     __shared__ float red[2][2][4];   // double-buffered over the row loop
     const int lt = threadIdx.x % TPR;
     const float n = (float)C;
+    uint4 wr[NV], br[NV];   // read before the first row's sums, not after them
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + lt) * V, cc = c < C ? c : 0;
+        if (w) wr[i] = load_raw<IO, WHOLE>(w, cc, C);
+        if (b) br[i] = load_raw<IO, WHOLE>(b, cc, C);
+    }
     int buf = 0;
     // every thread of a workgroup makes the same number of turns (the barriers of TPR = 256)
     for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < rows; r0 += (int64_t)gridDim.x * RPB) {
@@ -72,7 +79,8 @@ __global__ __launch_bounds__(NT) void ln_fwd(const typename IO::T* __restrict__ 
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPR + lt) * V;
-            v[i] = widen<IO>(c < C ? load_raw<IO>(xr, c, C, whole) : make_uint4(0, 0, 0, 0));
+            const uint4 raw = load_raw<IO, WHOLE>(xr, c < C ? c : 0, C);
+            v[i] = widen<IO>(c < C ? raw : make_uint4(0, 0, 0, 0));
 #pragma unroll
             for (int e = 0; e < V; ++e) s += v[i].x[e];
         }
@@ -101,20 +109,20 @@ __global__ __launch_bounds__(NT) void ln_fwd(const typename IO::T* __restrict__ 
             if (c >= C) continue;
             Lanes<IO> o;
             Lanes<IO> wv, bv;
-            if (w) wv = widen<IO>(load_raw<IO>(w, c, C, wwhole));
-            if (b) bv = widen<IO>(load_raw<IO>(b, c, C, wwhole));
+            if (w) wv = widen<IO>(wr[i]);
+            if (b) bv = widen<IO>(br[i]);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 float t = v[i].x[e] * rs;
                 if (w) t *= wv.x[e];
                 o.x[e] = b ? t + bv.x[e] : t;
             }
-            store_raw<IO>(y + row * ys, c, C, whole, o);
+            store_raw<IO, WHOLE>(y + row * ys, c, C, o);
         }
     }
 }
 
-template <class IO, int TPR, int NV>
+template <class IO, int TPR, int NV, bool WHOLE>
 __global__ __launch_bounds__(NT) void ln_bwd(const typename IO::T* __restrict__ dy,
                                              const typename IO::T* __restrict__ x,
                                              const typename IO::T* __restrict__ w,
@@ -122,8 +130,7 @@ __global__ __launch_bounds__(NT) void ln_bwd(const typename IO::T* __restrict__ 
                                              const float* __restrict__ rstd,
                                              typename IO::T* __restrict__ dx,
                                              float* __restrict__ part, int64_t rows, int C,
-                                             int64_t dys, int64_t xs, int64_t dxs, int whole,
-                                             int wwhole)
+                                             int64_t dys, int64_t xs, int64_t dxs)
 {
     constexpr int V = vec_elems<IO>, RPB = NT / TPR;
     __shared__ float red[2][2][4];
@@ -134,7 +141,7 @@ __global__ __launch_bounds__(NT) void ln_bwd(const typename IO::T* __restrict__ 
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * TPR + lt) * V;
-        if (w && c < C) wv[i] = widen<IO>(load_raw<IO>(w, c, C, wwhole));
+        if (w) wv[i] = widen<IO>(load_raw<IO, WHOLE>(w, c < C ? c : 0, C));
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             if (!w) wv[i].x[e] = 1.f;
@@ -146,16 +153,17 @@ __global__ __launch_bounds__(NT) void ln_bwd(const typename IO::T* __restrict__ 
     uint4 nx[NV], ny[NV];   // the next row, in flight while this one is reduced
     float nmu = 0.f, nrs = 0.f;
     auto fetch = [&](int64_t row) {
-        const bool on = row < rows;
+        const int64_t r = row < rows ? row : rows - 1;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPR + lt) * V;
-            const bool in = on && c < C;
-            nx[i] = in ? load_raw<IO>(x + row * xs, c, C, whole) : make_uint4(0, 0, 0, 0);
-            ny[i] = in ? load_raw<IO>(dy + row * dys, c, C, whole) : make_uint4(0, 0, 0, 0);
+            // past the row or the last row: some valid address, zeroed where dy is used
+            const int cc = c < C ? c : 0;
+            nx[i] = load_raw<IO, WHOLE>(x + r * xs, cc, C);
+            ny[i] = load_raw<IO, WHOLE>(dy + r * dys, cc, C);
         }
-        nmu = on ? mean[row] : 0.f;
-        nrs = on ? rstd[row] : 0.f;
+        nmu = mean[r];
+        nrs = rstd[r];
     };
     fetch((int64_t)blockIdx.x * RPB + grp);
     for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < rows; r0 += step) {
@@ -164,15 +172,16 @@ __global__ __launch_bounds__(NT) void ln_bwd(const typename IO::T* __restrict__ 
         const float mu = nmu, rs = nrs;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + lt) * V;
             xh[i] = widen<IO>(nx[i]);
-            g[i] = widen<IO>(ny[i]);
+            g[i] = widen<IO>(row < rows && c < C ? ny[i] : make_uint4(0, 0, 0, 0));
         }
         fetch(row + step);
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPR + lt) * V;
-            if (c < C) {
+            if (c < C && row < rows) {
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     // past the row's end dy reads 0, so nothing below counts there
@@ -196,7 +205,7 @@ __global__ __launch_bounds__(NT) void ln_bwd(const typename IO::T* __restrict__ 
             Lanes<IO> o;
 #pragma unroll
             for (int e = 0; e < V; ++e) o.x[e] = rs * (g[i].x[e] - m1 - xh[i].x[e] * m2);
-            store_raw<IO>(dx + row * dxs, c, C, whole, o);
+            store_raw<IO, WHOLE>(dx + row * dxs, c, C, o);
         }
     }
     if (!part) return;
@@ -264,14 +273,14 @@ __global__ __launch_bounds__(1024) void ln_params(const float* __restrict__ part
 
 // ---- rows longer than the registers hold: one workgroup per row, the row re-read from cache
 
-template <class IO>
+template <class IO, bool WHOLE>
 __global__ __launch_bounds__(NT) void lnl_fwd(const typename IO::T* __restrict__ x,
                                               const typename IO::T* __restrict__ w,
                                               const typename IO::T* __restrict__ b,
                                               typename IO::T* __restrict__ y,
                                               float* __restrict__ mean, float* __restrict__ rstd,
                                               int64_t rows, int C, int64_t xs, int64_t ys,
-                                              float eps, int whole, int wwhole)
+                                              float eps)
 {
     constexpr int V = vec_elems<IO>;
     __shared__ float red[2][2][4];
@@ -281,14 +290,14 @@ __global__ __launch_bounds__(NT) void lnl_fwd(const typename IO::T* __restrict__
         const typename IO::T* xr = x + row * xs;
         float s = 0.f;
         for (int64_t c = threadIdx.x * V; c < C; c += NT * V) {
-            const Lanes<IO> v = widen<IO>(load_raw<IO>(xr, (int)c, C, whole));
+            const Lanes<IO> v = widen<IO>(load_raw<IO, WHOLE>(xr, (int)c, C));
 #pragma unroll
             for (int e = 0; e < V; ++e) s += v.x[e];
         }
         const float mu = row_sum<NT>(s, red[buf][0]) / n;
         float q = 0.f;
         for (int64_t c = threadIdx.x * V; c < C; c += NT * V) {
-            const Lanes<IO> v = widen<IO>(load_raw<IO>(xr, (int)c, C, whole));
+            const Lanes<IO> v = widen<IO>(load_raw<IO, WHOLE>(xr, (int)c, C));
 #pragma unroll
             for (int e = 0; e < V; ++e) q += c + e < C ? (v.x[e] - mu) * (v.x[e] - mu) : 0.f;
         }
@@ -299,30 +308,29 @@ __global__ __launch_bounds__(NT) void lnl_fwd(const typename IO::T* __restrict__
             if (rstd) rstd[row] = rs;
         }
         for (int64_t c = threadIdx.x * V; c < C; c += NT * V) {
-            Lanes<IO> v = widen<IO>(load_raw<IO>(xr, (int)c, C, whole));
+            Lanes<IO> v = widen<IO>(load_raw<IO, WHOLE>(xr, (int)c, C));
             Lanes<IO> wv, bv;
-            if (w) wv = widen<IO>(load_raw<IO>(w, (int)c, C, wwhole));
-            if (b) bv = widen<IO>(load_raw<IO>(b, (int)c, C, wwhole));
+            if (w) wv = widen<IO>(load_raw<IO, WHOLE>(w, (int)c, C));
+            if (b) bv = widen<IO>(load_raw<IO, WHOLE>(b, (int)c, C));
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 float t = (v.x[e] - mu) * rs;
                 if (w) t *= wv.x[e];
                 v.x[e] = b ? t + bv.x[e] : t;
             }
-            store_raw<IO>(y + row * ys, (int)c, C, whole, v);
+            store_raw<IO, WHOLE>(y + row * ys, (int)c, C, v);
         }
     }
 }
 
-template <class IO>
+template <class IO, bool WHOLE>
 __global__ __launch_bounds__(NT) void lnl_bwd(const typename IO::T* __restrict__ dy,
                                               const typename IO::T* __restrict__ x,
                                               const typename IO::T* __restrict__ w,
                                               const float* __restrict__ mean,
                                               const float* __restrict__ rstd,
                                               typename IO::T* __restrict__ dx, int64_t rows, int C,
-                                              int64_t dys, int64_t xs, int64_t dxs, int whole,
-                                              int wwhole)
+                                              int64_t dys, int64_t xs, int64_t dxs)
 {
     constexpr int V = vec_elems<IO>;
     __shared__ float red[2][2][4];
@@ -331,10 +339,10 @@ __global__ __launch_bounds__(NT) void lnl_bwd(const typename IO::T* __restrict__
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
         const float mu = mean[row], rs = rstd[row];
         auto terms = [&](int c, Lanes<IO>& e, Lanes<IO>& xh) {
-            e = widen<IO>(load_raw<IO>(dy + row * dys, c, C, whole));
-            xh = widen<IO>(load_raw<IO>(x + row * xs, c, C, whole));
+            e = widen<IO>(load_raw<IO, WHOLE>(dy + row * dys, c, C));
+            xh = widen<IO>(load_raw<IO, WHOLE>(x + row * xs, c, C));
             Lanes<IO> wv;
-            if (w) wv = widen<IO>(load_raw<IO>(w, c, C, wwhole));
+            if (w) wv = widen<IO>(load_raw<IO, WHOLE>(w, c, C));
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 xh.x[i] = (xh.x[i] - mu) * rs;
@@ -359,7 +367,7 @@ __global__ __launch_bounds__(NT) void lnl_bwd(const typename IO::T* __restrict__
             terms((int)c, e, xh);
 #pragma unroll
             for (int i = 0; i < V; ++i) e.x[i] = rs * (e.x[i] - m1 - xh.x[i] * m2);
-            store_raw<IO>(dx + row * dxs, (int)c, C, whole, e);
+            store_raw<IO, WHOLE>(dx + row * dxs, (int)c, C, e);
         }
     }
 }
@@ -384,6 +392,12 @@ __global__ __launch_bounds__(NT) void lnl_params(const typename IO::T* __restric
     float* mine = part + (int64_t)strip * 2 * C;
     mine[c] = aw;
     mine[C + c] = ab;
+}
+
+// (a null pointer counts as aligned: nothing is read there)
+bool aligned_rows(const void* p, int64_t stride, size_t es)
+{
+    return (uintptr_t)p % 16 == 0 && stride * (int64_t)es % 16 == 0;
 }
 
 // Threads per row and vectors per thread for rows of C values: the fewest threads whose
@@ -428,57 +442,46 @@ int64_t bwd_blocks(int64_t rows, const RowPlan& p)
     return std::min<int64_t>(BWD_BLOCKS, (rows + rpb - 1) / rpb);
 }
 
-bool aligned_rows(const void* p, int64_t stride, size_t es)
-{
-    return (uintptr_t)p % 16 == 0 && stride * (int64_t)es % 16 == 0;
-}
-
-template <class IO>
+template <class IO, bool WHOLE>
 hipError_t fwd(const void* x, const void* w, const void* b, void* y, float* mean, float* rstd,
                int64_t rows, int C, int64_t xs, int64_t ys, float eps, hipStream_t st)
 {
     using E = typename IO::T;
     const RowPlan p = row_plan(C, vec_elems<IO>);
-    const int whole = aligned_rows(x, xs, sizeof(E)) && aligned_rows(y, ys, sizeof(E));
-    const int ww = (!w || (uintptr_t)w % 16 == 0) && (!b || (uintptr_t)b % 16 == 0);
     // the row loop covers what a grid of this many workgroups leaves
     const int64_t rpb = NT / p.tpr, blocks = std::min<int64_t>((rows + rpb - 1) / rpb, 1 << 20);
     if (p.nv == 0) {
-        hipLaunchKernelGGL((lnl_fwd<IO>), dim3((unsigned)blocks), dim3(NT), 0, st, (const E*)x,
-                           (const E*)w, (const E*)b, (E*)y, mean, rstd, rows, C, xs, ys, eps,
-                           whole, ww);
+        hipLaunchKernelGGL((lnl_fwd<IO, WHOLE>), dim3((unsigned)blocks), dim3(NT), 0, st, (const E*)x,
+                           (const E*)w, (const E*)b, (E*)y, mean, rstd, rows, C, xs, ys, eps);
         return hipGetLastError();
     }
     return with_plan(p, [&](auto tpr, auto nv) {
         if constexpr (decltype(nv)::value == 8 && IO::SIZE == 2) return hipErrorInvalidValue;
         else {
-            hipLaunchKernelGGL((ln_fwd<IO, decltype(tpr)::value, decltype(nv)::value>),
+            hipLaunchKernelGGL((ln_fwd<IO, decltype(tpr)::value, decltype(nv)::value, WHOLE>),
                                dim3((unsigned)blocks), dim3(NT), 0, st, (const E*)x, (const E*)w,
-                               (const E*)b, (E*)y, mean, rstd, rows, C, xs, ys, eps, whole, ww);
+                               (const E*)b, (E*)y, mean, rstd, rows, C, xs, ys, eps);
             return hipGetLastError();
         }
     });
 }
 
-template <class IO>
+template <class IO, bool WHOLE>
 hipError_t bwd(const void* dy, const void* x, const void* w, const float* mean, const float* rstd,
                void* dx, void* dw, void* db, int64_t rows, int C, int64_t dys, int64_t xs,
                int64_t dxs, float* part, hipStream_t st)
 {
     using E = typename IO::T;
     const RowPlan p = row_plan(C, vec_elems<IO>);
-    const int whole = aligned_rows(dy, dys, sizeof(E)) && aligned_rows(x, xs, sizeof(E)) &&
-                      aligned_rows(dx, dxs, sizeof(E));
-    const int ww = !w || (uintptr_t)w % 16 == 0;
     const bool params = dw || db;
     int64_t shares = 0;
     hipError_t e = hipSuccess;
     if (p.nv == 0) {
         const int64_t blocks = std::min<int64_t>(rows, 1 << 20);
         if (blocks > 0) {
-            hipLaunchKernelGGL((lnl_bwd<IO>), dim3((unsigned)blocks), dim3(NT), 0, st,
+            hipLaunchKernelGGL((lnl_bwd<IO, WHOLE>), dim3((unsigned)blocks), dim3(NT), 0, st,
                                (const E*)dy, (const E*)x, (const E*)w, mean, rstd, (E*)dx, rows, C,
-                               dys, xs, dxs, whole, ww);
+                               dys, xs, dxs);
             e = hipGetLastError();
         }
         if (e == hipSuccess && params && rows > 0) {
@@ -493,10 +496,10 @@ hipError_t bwd(const void* dy, const void* x, const void* w, const float* mean, 
         e = with_plan(p, [&](auto tpr, auto nv) {
             if constexpr (decltype(nv)::value == 8 && IO::SIZE == 2) return hipErrorInvalidValue;
             else {
-                hipLaunchKernelGGL((ln_bwd<IO, decltype(tpr)::value, decltype(nv)::value>),
+                hipLaunchKernelGGL((ln_bwd<IO, decltype(tpr)::value, decltype(nv)::value, WHOLE>),
                                    dim3((unsigned)shares), dim3(NT), 0, st, (const E*)dy,
                                    (const E*)x, (const E*)w, mean, rstd, (E*)dx,
-                                   params ? part : nullptr, rows, C, dys, xs, dxs, whole, ww);
+                                   params ? part : nullptr, rows, C, dys, xs, dxs);
                 return hipGetLastError();
             }
         });
@@ -513,8 +516,12 @@ hipError_t launch_layernorm(Store s, const void* x, const void* w, const void* b
                             float* mean, float* rstd, int64_t rows, int C, int64_t xs, int64_t ys,
                             float eps, hipStream_t st)
 {
-    return s == Store::F32 ? fwd<f32_io>(x, w, b, y, mean, rstd, rows, C, xs, ys, eps, st)
-                           : fwd<bf16_io>(x, w, b, y, mean, rstd, rows, C, xs, ys, eps, st);
+    const size_t es = s == Store::F32 ? 4 : 2;
+    const bool whole = C % (16 / es) == 0 && aligned_rows(x, xs, es) && aligned_rows(y, ys, es) &&
+                       aligned_rows(w, 0, es) && aligned_rows(b, 0, es);
+    auto f = s == Store::F32 ? (whole ? fwd<f32_io, true> : fwd<f32_io, false>)
+                             : (whole ? fwd<bf16_io, true> : fwd<bf16_io, false>);
+    return f(x, w, b, y, mean, rstd, rows, C, xs, ys, eps, st);
 }
 
 size_t layernorm_bwd_bytes(Store s, int64_t rows, int C)
@@ -529,9 +536,12 @@ hipError_t launch_layernorm_bwd(Store s, const void* dy, const void* x, const vo
                                 int64_t rows, int C, int64_t dys, int64_t xs, int64_t dxs,
                                 void* ws, hipStream_t st)
 {
-    return s == Store::F32
-               ? bwd<f32_io>(dy, x, w, mean, rstd, dx, dw, db, rows, C, dys, xs, dxs, (float*)ws, st)
-               : bwd<bf16_io>(dy, x, w, mean, rstd, dx, dw, db, rows, C, dys, xs, dxs, (float*)ws, st);
+    const size_t es = s == Store::F32 ? 4 : 2;
+    const bool whole = C % (16 / es) == 0 && aligned_rows(dy, dys, es) && aligned_rows(x, xs, es) &&
+                       aligned_rows(dx, dxs, es) && aligned_rows(w, 0, es);
+    auto f = s == Store::F32 ? (whole ? bwd<f32_io, true> : bwd<f32_io, false>)
+                             : (whole ? bwd<bf16_io, true> : bwd<bf16_io, false>);
+    return f(dy, x, w, mean, rstd, dx, dw, db, rows, C, dys, xs, dxs, (float*)ws, st);
 }
 
 }  // namespace sc

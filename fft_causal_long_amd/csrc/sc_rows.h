@@ -10,6 +10,15 @@
 
 namespace sc {
 
+// Workgroups go to the eight dies round robin.  Work item of workgroup `id` of `n` such that
+// each die takes a run of consecutive items: neighbours that share cache lines or operands then
+// share an L2.  (What n leaves over a multiple of 8 stays in place.)
+__device__ __forceinline__ uint32_t die_order(uint32_t id, uint32_t n)
+{
+    const uint32_t per = n >> 3;
+    return id < (per << 3) ? (id & 7) * per + (id >> 3) : id;
+}
+
 // Elements of one 16-byte vector.
 template <class IO>
 constexpr int vec_elems = 16 / IO::SIZE;
@@ -48,37 +57,40 @@ __device__ __forceinline__ uint4 narrow(const Lanes<IO>& v)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Elements c .. c+V-1 of the row p of n elements; those at n and beyond read 0.  `whole` says
-// that every row starts 16-byte aligned; a vector that the row ends inside, and every vector of
-// an unaligned row, is read element by element.
-template <class IO>
-__device__ __forceinline__ uint4 load_raw(const typename IO::T* p, int c, int n, bool whole)
+// Elements c .. c+V-1 (c < n) of the row p of n elements.  WHOLE: every row starts 16-byte
+// aligned and n is a multiple of V, so the vector is one load; a kernel takes one form or the
+// other, since a choice at each load would make every load wait for the one before.  Otherwise
+// the elements are read one by one, those at n and beyond as 0.
+template <class IO, bool WHOLE>
+__device__ __forceinline__ uint4 load_raw(const typename IO::T* p, int c, int n)
 {
     constexpr int V = vec_elems<IO>;
-    if (whole && c + V <= n) return *(const uint4*)(p + c);
-    uint32_t w[4] = {0, 0, 0, 0};
+    if constexpr (WHOLE) {
+        return *(const uint4*)(p + c);
+    } else {
+        uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        if (c + i < n) {
-            if constexpr (IO::SIZE == 2) w[i / 2] |= (uint32_t)p[c + i] << (16 * (i & 1));
-            else w[i] = __float_as_uint(p[c + i]);
+        for (int i = 0; i < V; ++i) {
+            // the element's own address or the row's last: no branch
+            const int at = c + i < n ? c + i : n - 1;
+            if constexpr (IO::SIZE == 2) w[i / 2] |= (c + i < n ? (uint32_t)p[at] : 0u) << (16 * (i & 1));
+            else w[i] = c + i < n ? __float_as_uint(p[at]) : 0u;
         }
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <class IO>
-__device__ __forceinline__ void store_raw(typename IO::T* p, int c, int n, bool whole,
-                                          const Lanes<IO>& v)
+template <class IO, bool WHOLE>
+__device__ __forceinline__ void store_raw(typename IO::T* p, int c, int n, const Lanes<IO>& v)
 {
     constexpr int V = vec_elems<IO>;
-    if (whole && c + V <= n) {
+    if constexpr (WHOLE) {
         *(uint4*)(p + c) = narrow<IO>(v);
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (c + i < n) IO::store(p, c + i, v.x[i]);
+        for (int i = 0; i < V; ++i)
+            if (c + i < n) IO::store(p, c + i, v.x[i]);
+    }
 }
 
 }  // namespace sc

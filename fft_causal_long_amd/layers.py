@@ -102,6 +102,7 @@ _KIND = {torch.float32: KIND_F32, torch.bfloat16: KIND_BF16}
 # the current stream's handle without building a Stream object: a decoding step is a handful of
 # microseconds, most of them spent here
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_get_device = torch._C._cuda_getDevice
 
 
 def _check(x, *others):
@@ -166,6 +167,8 @@ def _scratch(need, workspace, dev):
 
 def _out(out, like, name):
     if out is None:
+        if like.is_contiguous():
+            return torch.empty_like(like)
         return torch.empty(like.shape, dtype=like.dtype, device=like.device)
     if out.shape != like.shape or out.dtype != like.dtype or out.device != like.device:
         raise ValueError("%s must match the inputs in shape, dtype and device" % name)
@@ -174,7 +177,7 @@ def _out(out, like, name):
 
 def _run(what, fn, dev, *args):
     """fn(*args, stream) on dev's current stream."""
-    if dev.index == torch.cuda.current_device():
+    if dev.index == _get_device():
         st = fn(*args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
@@ -185,7 +188,7 @@ def _run(what, fn, dev, *args):
 
 def _params(x, *ps):
     for p in ps:
-        if p is not None and (p.shape != x.shape[-1:] or not p.is_contiguous()):
+        if p is not None and (p.dim() != 1 or p.shape[0] != x.shape[-1] or not p.is_contiguous()):
             raise ValueError("weight and bias must be contiguous (C,) tensors")
 
 
@@ -266,7 +269,9 @@ def gated_recurrence(z: torch.Tensor, u: torch.Tensor, h0: torch.Tensor | None =
     _state(h0, z, "h0")
     _state(hT, z, "hT")
     h = _out(out, z, "out")
-    if hT is None:
+    if hT is None and h0 is not None:
+        hT = torch.empty_like(h0)
+    elif hT is None:
         hT = torch.empty(z.shape[:-2] + z.shape[-1:], dtype=torch.float32, device=z.device)
     keep, ws, n = _scratch(_lib.sc_recur_workspace_bytes(kind, B, L, C), workspace, z.device)
     _run("gated_recurrence", _lib.sc_recur, z.device, kind, z.data_ptr(), u.data_ptr(), _ptr(h0),
