@@ -14,6 +14,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "sc_device.h"
 #include "sc_internal.h"
 
@@ -136,6 +138,22 @@ __device__ __forceinline__ float gmax(float v)
     v = fmaxf(v, __shfl_xor(v, 16));
     return fmaxf(v, __shfl_xor(v, 32));
 }
+// sum over N neighbouring lanes (8, 16 or 32, aligned), by lane permutations in the add itself up
+// to 16: quad swaps, then mirrors of 8 and of 16
+template <int N>
+__device__ __forceinline__ float lane_sum(float v)
+{
+    auto swapped = [](float x, auto ctrl) {
+        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), decltype(ctrl)::value, 0xf, 0xf, true));
+    };
+    using std::integral_constant;
+    v += swapped(v, integral_constant<int, 0xb1>());    // quad_perm 1, 0, 3, 2
+    v += swapped(v, integral_constant<int, 0x4e>());    // quad_perm 2, 3, 0, 1
+    v += swapped(v, integral_constant<int, 0x141>());   // row_half_mirror
+    if constexpr (N >= 16) v += swapped(v, integral_constant<int, 0x140>());   // row_mirror
+    if constexpr (N >= 32) v += __shfl_xor(v, 16);
+    return v;
+}
 __device__ __forceinline__ int wave_min(int v)
 {
 #pragma unroll
@@ -148,6 +166,10 @@ __device__ __forceinline__ int wave_max(int v)
     for (int m = 1; m < 64; m <<= 1) v = max(v, __shfl_xor(v, m));
     return __builtin_amdgcn_readfirstlane(v);
 }
+
+// Inside a rarely taken block: keeps it a branch.  The compiler would otherwise compute the
+// block's selects on every pass (the masks of attn_fwd: 100 of 330 vector instructions a tile).
+__device__ __forceinline__ void keep_branch() { asm volatile(""); }
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -194,6 +216,120 @@ __device__ __forceinline__ int first_key(const AttnArgs& a, int b, int p, int n)
 __device__ __forceinline__ bool key_live(const AttnArgs& a, int b, int j, int n)
 {
     return j < n && (!a.doc || a.doc[(int64_t)b * a.Lk + j] <= j);
+}
+
+// What a strip of packed rows sees: its lowest and highest key, the highest first key of a row
+// and the lowest position (a key tile at or above `last` and at or below `pos` needs no mask).
+// A strip of empty rows has lo = BIG, hi = -1.
+struct RowRange {
+    int lo, hi, last, pos;
+};
+
+// Without documents it follows from the first and the last row: tokens t .. t + count - 1.
+__device__ __forceinline__ RowRange token_range(const AttnArgs& a, int n, int t, int count)
+{
+    const int off = n - a.Lq, p1 = off + min(t + count, a.Lq) - 1;
+    if (t >= a.Lq || p1 < 0) return {BIG, -1, 0, BIG};
+    const int p0 = max(off + t, 0);
+    return {max(0, p0 - a.window + 1), p1, max(0, p1 - a.window + 1), p0};
+}
+// Packed rows r .. r + rows - 1.
+__device__ __forceinline__ RowRange packed_range(const AttnArgs& a, int n, int r, int rows)
+{
+    if (r >= a.nrow) return {BIG, -1, 0, BIG};
+    const int t = r / a.G;
+    return token_range(a, n, t, (min(r + rows, a.nrow) - 1) / a.G - t + 1);
+}
+
+// The range of a wave's strip from its lanes' rows (lo = BIG: empty).
+template <int NR>
+__device__ __forceinline__ RowRange lanes_range(const int (&lo)[NR], const int (&pos)[NR])
+{
+    RowRange x = {BIG, -1, 0, BIG};
+#pragma unroll
+    for (int m = 0; m < NR; ++m)
+        if (lo[m] != BIG) {
+            x.lo = min(x.lo, lo[m]);
+            x.hi = max(x.hi, pos[m]);
+            x.last = max(x.last, lo[m]);
+            x.pos = min(x.pos, pos[m]);
+        }
+    return {wave_min(x.lo), wave_max(x.hi), wave_max(x.last), wave_min(x.pos)};
+}
+
+// The key tiles a workgroup walks: 64 keys of k and v, fetched into registers one tile ahead and
+// put into LDS rows of pitch<IO, DP>.  Keys past the sequence and padding read as 0, whatever the
+// memory holds.
+template <class IO, int DP>
+struct KeyTiles {
+    using E = typename IO::T;
+    static constexpr int BN = 64, V = 16 / IO::SIZE, CH = DP / V, NCH = BN * CH / NT, P = pitch<IO, DP>;
+    const AttnArgs& a;
+    const int32_t* doc;
+    const E *kp, *vp;
+    int n, r0, d0, lane;   // this thread's pieces: rows r0 + NT / CH i, columns d0 .. d0 + V - 1
+    bool din;
+    uint4 rk[NCH], rv[NCH];
+    int rdoc = 0;
+
+    __device__ __forceinline__ KeyTiles(const AttnArgs& args, int b, int hk, int len, int tid)
+        : a(args), doc(args.doc ? args.doc + (int64_t)b * args.Lk : nullptr), n(len), r0(tid / CH),
+          d0(tid % CH * V), lane(tid & 63), din(d0 < args.D)
+    {
+        kp = (const E*)a.k + b * a.ks[0] + hk * a.ks[2] + (din ? d0 : 0);
+        vp = (const E*)a.v + b * a.vs[0] + hk * a.vs[2] + (din ? d0 : 0);
+    }
+    // only where some row sees a key, so n > 0; nothing here waits for a load
+    __device__ __forceinline__ void fetch(int j0)
+    {
+        if (j0 + BN <= n) {
+            const E *k = kp + (int64_t)(j0 + r0) * a.ks[1], *v = vp + (int64_t)(j0 + r0) * a.vs[1];
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) {
+                rk[i] = *(const uint4*)(k + (int64_t)(NT / CH * i) * a.ks[1]);
+                rv[i] = *(const uint4*)(v + (int64_t)(NT / CH * i) * a.vs[1]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) {
+                const int64_t j = min(j0 + r0 + NT / CH * i, n - 1);
+                rk[i] = *(const uint4*)(kp + j * a.ks[1]);
+                rv[i] = *(const uint4*)(vp + j * a.vs[1]);
+            }
+        }
+        if (doc) rdoc = doc[min(j0 + lane, n - 1)];
+    }
+    // returns which keys of the tile exist and are not padding, bit j - j0
+    __device__ __forceinline__ uint64_t put(E* kt, E* vt, int j0)
+    {
+        const uint64_t live = __ballot(j0 + lane < n && (!doc || rdoc <= j0 + lane));
+        if (live == ~0ull && DP == a.D) {
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) {
+                const int at = (r0 + NT / CH * i) * P + d0;
+                *(uint4*)(kt + at) = rk[i];
+                *(uint4*)(vt + at) = rv[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) {
+                const int r = r0 + NT / CH * i, at = r * P + d0;
+                const bool on = din && live >> r & 1;
+                *(uint4*)(kt + at) = on ? rk[i] : make_uint4(0, 0, 0, 0);
+                *(uint4*)(vt + at) = on ? rv[i] : make_uint4(0, 0, 0, 0);
+            }
+        }
+        // keys past the sequence lie past every position: no mask of their own
+        return doc ? live : ~0ull;
+    }
+};
+
+// four consecutive results of a row
+template <class IO>
+__device__ __forceinline__ void put4(typename IO::T* p, const f32x4& x)
+{
+    if constexpr (IO::SIZE == 2) *(uint2*)p = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+    else *(float4*)p = make_float4(x[0], x[1], x[2], x[3]);
 }
 
 }  // namespace attn

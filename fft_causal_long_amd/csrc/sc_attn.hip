@@ -35,12 +35,16 @@ constexpr int BN = 64;            // keys of a tile
 constexpr int NQ = 2;             // 16-row blocks of a wave
 constexpr int WM = 16 * NQ;       // rows of a wave
 constexpr int BM = 4 * WM;        // rows of a workgroup
+constexpr float SLACK = 8.f;      // a row's base may lag its maximum by this (base 2)
 
+#ifndef FWV
+#define FWV(DP, SZ) (SZ == 4 ? 1 : DP == 64 ? 3 : 2)
+#endif
 template <class IO, int DP, bool CAP, bool BIAS>
-__global__ __launch_bounds__(NT) void attn_fwd(AttnArgs a)
+__global__ __launch_bounds__(NT, FWV(DP, IO::SIZE)) void attn_fwd(AttnArgs a)
 {
     using E = typename IO::T;
-    constexpr int P = pitch<IO, DP>, V = vec_elems<IO>, CH = DP / V, NCH = BN * CH / NT;
+    constexpr int P = pitch<IO, DP>;
     constexpr int KK = DP / 32, ND = DP / 16;
     __shared__ __attribute__((aligned(16))) E Kt[BN * P];
     __shared__ __attribute__((aligned(16))) E Vt[BN * P];
@@ -61,25 +65,15 @@ __global__ __launch_bounds__(NT) void attn_fwd(AttnArgs a)
     bool empty[NQ];
     Frag<IO> q[NQ][KK];
     float slope[NQ];
-    int wlo = BIG, whi = -1, mlo = 0, mpos = BIG;   // lowest key, highest key; to skip masking
+    const int rw = tile * BM + wave * WM;   // the wave's first row
 #pragma unroll
     for (int m = 0; m < NQ; ++m) {
-        row[m] = tile * BM + wave * WM + 16 * m + c;
+        row[m] = rw + 16 * m + c;
         const bool in = row[m] < a.nrow;
         const int i = in ? row[m] / a.G : 0, h = hk * a.G + (in ? row[m] % a.G : 0);
         pos[m] = n - a.Lq + i;
         lo[m] = in ? first_key(a, b, pos[m], n) : BIG;
         empty[m] = lo[m] == BIG;
-        if (!empty[m]) {
-            wlo = min(wlo, lo[m]);
-            whi = max(whi, pos[m]);
-            mlo = max(mlo, lo[m]);
-            mpos = min(mpos, pos[m]);
-        } else {
-            // an empty row takes part with q = 0 and nothing masked; its result is dropped
-            lo[m] = 0;
-            pos[m] = BIG;
-        }
         slope[m] = BIAS ? a.slopes[h] * LOG2E : 0.f;
         const E* qp = (const E*)a.q + b * a.qs[0] + (int64_t)i * a.qs[1] + h * a.qs[2];
 #pragma unroll
@@ -88,17 +82,30 @@ __global__ __launch_bounds__(NT) void attn_fwd(AttnArgs a)
             q[m][k] = !empty[m] && d < a.D ? frag_at<IO>(qp + d) : frag_zero<IO>();
         }
     }
-    wlo = wave_min(wlo);
-    whi = wave_max(whi);
-    mlo = wave_max(mlo);
-    mpos = wave_min(mpos);
-    if (lane == 0) {
-        range[0][wave] = wlo;
-        range[1][wave] = whi;
+    const RowRange rr = a.doc ? lanes_range(lo, pos) : packed_range(a, n, rw, WM);
+    int klo = rr.lo, khi = rr.hi;
+    if (a.doc) {
+        if (lane == 0) {
+            range[0][wave] = rr.lo;
+            range[1][wave] = rr.hi;
+        }
+        __syncthreads();
+        klo = min(min(range[0][0], range[0][1]), min(range[0][2], range[0][3]));
+        khi = max(max(range[1][0], range[1][1]), max(range[1][2], range[1][3]));
+    } else {
+        const RowRange all = packed_range(a, n, tile * BM, BM);
+        klo = all.lo;
+        khi = all.hi;
     }
-    __syncthreads();
-    const int klo = min(min(range[0][0], range[0][1]), min(range[0][2], range[0][3]));
-    const int khi = max(max(range[1][0], range[1][1]), max(range[1][2], range[1][3]));
+    klo = __builtin_amdgcn_readfirstlane(klo);
+    khi = __builtin_amdgcn_readfirstlane(khi);
+#pragma unroll
+    for (int m = 0; m < NQ; ++m)
+        if (empty[m]) {
+            // an empty row takes part with q = 0 and nothing masked; its result is dropped
+            lo[m] = 0;
+            pos[m] = BIG;
+        }
     int t0 = khi < 0 ? 0 : klo / BN, t1 = khi < 0 ? 0 : khi / BN + 1;
     if (a.nsplit > 1) {
         const int per = (t1 - t0 + a.nsplit - 1) / a.nsplit;
@@ -117,35 +124,15 @@ __global__ __launch_bounds__(NT) void attn_fwd(AttnArgs a)
         for (int d = 0; d < ND; ++d) o[d][m] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    const E* kp = (const E*)a.k + b * a.ks[0] + hk * a.ks[2];
-    const E* vp = (const E*)a.v + b * a.vs[0] + hk * a.vs[2];
-    uint4 rk[NCH], rv[NCH];
-    int rdoc = 0;
-    // keys past the sequence and padding read as 0, whatever the memory holds
-    auto fetch = [&](int j0) {
-#pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-            const int id_ = tid + NT * i, j = j0 + id_ / CH, d = (id_ % CH) * V;
-            const bool on = d < a.D && key_live(a, b, j, n);
-            rk[i] = on ? *(const uint4*)(kp + (int64_t)j * a.ks[1] + d) : make_uint4(0, 0, 0, 0);
-            rv[i] = on ? *(const uint4*)(vp + (int64_t)j * a.vs[1] + d) : make_uint4(0, 0, 0, 0);
-        }
-        if (a.doc) rdoc = j0 + lane < n ? a.doc[(int64_t)b * a.Lk + j0 + lane] : BIG;
-    };
-    if (t0 < t1) fetch(t0 * BN);
+    KeyTiles<IO, DP> tiles(a, b, hk, n, tid);
+    if (t0 < t1) tiles.fetch(t0 * BN);
     for (int t = t0; t < t1; ++t) {
         const int j0 = t * BN;
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-            const int id_ = tid + NT * i, at = (id_ / CH) * P + (id_ % CH) * V;
-            *(uint4*)(Kt + at) = rk[i];
-            *(uint4*)(Vt + at) = rv[i];
-        }
-        const uint64_t live = a.doc ? __ballot(rdoc <= j0 + lane) : ~0ull;
+        const uint64_t live = tiles.put(Kt, Vt, j0);
         __syncthreads();
-        if (t + 1 < t1) fetch(j0 + BN);
-        if (j0 > whi || j0 + BN - 1 < wlo) continue;   // no row of this wave sees it
+        if (t + 1 < t1) tiles.fetch(j0 + BN);
+        if (j0 > rr.hi || j0 + BN - 1 < rr.lo) continue;   // no row of this wave sees it
 
         // scores, keys x rows
         f32x4 s[4][NQ];
@@ -160,56 +147,67 @@ __global__ __launch_bounds__(NT) void attn_fwd(AttnArgs a)
                 for (int m = 0; m < NQ; ++m) s[kb][m] = mma(f, q[m][k], s[kb][m]);
             }
         }
-        const bool edge = j0 < mlo || j0 + BN - 1 > mpos || live != ~0ull;
+        const bool edge = j0 < rr.last || j0 + BN - 1 > rr.pos;
         Frag<IO> w[2][NQ];
 #pragma unroll
         for (int m = 0; m < NQ; ++m) {
-            // CAP and BIAS: s becomes the score in base 2; otherwise it stays the raw product
-            // and the scale goes into the exponential's multiply-add
-            const float far = (float)(j0 + 4 * g - pos[m]);
+            // scores in base 2, less the row's base: the running maximum as it was when a score
+            // last passed it by 2^SLACK.  Weights then reach 2^SLACK, which float32 sums and
+            // either storage type hold as well as 1, and the accumulators are rescaled a few
+            // times a row instead of whenever the maximum moves.
+            const float base = mx[m] == -INFINITY ? 0.f : mx[m];
+            const float shift = BIAS ? slope[m] * (float)(j0 + 4 * g - pos[m]) - base : -base;
 #pragma unroll
             for (int kb = 0; kb < 4; ++kb)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    float x = s[kb][m][r];
-                    if constexpr (CAP) x = cap2 * tanh_of<IO>(x * scale2);
-                    if constexpr (BIAS) {
-                        const float bias = slope[m] * (far + (float)(16 * kb + r));
-                        x = CAP ? x + bias : __builtin_fmaf(x, scale2, bias);
-                    }
-                    s[kb][m][r] = x;
+                    const float add = BIAS ? __builtin_fmaf(slope[m], (float)(16 * kb + r), shift) : shift;
+                    if constexpr (CAP) s[kb][m][r] = __builtin_fmaf(cap2, tanh_of<IO>(s[kb][m][r] * scale2), add);
+                    else s[kb][m][r] = __builtin_fmaf(s[kb][m][r], scale2, add);
                 }
             if (edge) {
+                keep_branch();
+                const int first = lo[m] - j0 - 4 * g;
+                const uint32_t span = (uint32_t)(pos[m] - lo[m]);   // keys the row sees, less 1
 #pragma unroll
                 for (int kb = 0; kb < 4; ++kb)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int jj = 16 * kb + 4 * g + r, j = j0 + jj;
-                        if (j < lo[m] || j > pos[m] || !(live >> jj & 1)) s[kb][m][r] = -INFINITY;
-                    }
+                    for (int r = 0; r < 4; ++r)
+                        if ((uint32_t)(16 * kb + r - first) > span) s[kb][m][r] = -INFINITY;
+            }
+            if (live != ~0ull) {
+                keep_branch();
+                const uint64_t mine = live >> (4 * g);
+#pragma unroll
+                for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (!(mine >> (16 * kb + r) & 1)) s[kb][m][r] = -INFINITY;
             }
             float top = s[0][m][0];
 #pragma unroll
             for (int kb = 0; kb < 4; ++kb)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) top = fmaxf(top, s[kb][m][r]);
-            top = gmax(top);
-            if constexpr (!CAP && !BIAS) top *= scale2;
-            const float now = fmaxf(mx[m], top);
-            const float base = now == -INFINITY ? 0.f : now;   // nothing seen yet: weights are 0
-            if (__any(now > mx[m])) {
-                const float f = exp2_hw(mx[m] - base);
-                sum[m] *= f;
+            if (__any(top > (mx[m] == -INFINITY ? -INFINITY : SLACK))) {
+                top = gmax(top);
+                if (top > (mx[m] == -INFINITY ? -INFINITY : SLACK)) {
+                    const float now = base + top, f = exp2_hw(mx[m] - now);
+                    sum[m] *= f;
 #pragma unroll
-                for (int d = 0; d < ND; ++d) o[d][m] *= f;
-                mx[m] = now;
+                    for (int d = 0; d < ND; ++d) o[d][m] *= f;
+                    mx[m] = now;
+#pragma unroll
+                    for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) s[kb][m][r] -= top;
+                }
             }
 #pragma unroll
             for (int kb = 0; kb < 4; ++kb)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float e = exp2_hw(CAP || BIAS ? s[kb][m][r] - base
-                                                        : __builtin_fmaf(s[kb][m][r], scale2, -base));
+                    const float e = exp2_hw(s[kb][m][r]);
                     s[kb][m][r] = e;
                     sum[m] += e;
                 }
@@ -254,19 +252,197 @@ __global__ __launch_bounds__(NT) void attn_fwd(AttnArgs a)
         for (int d = 0; d < ND; ++d) {
             const int d0 = 16 * d + 4 * g;
             if (d0 >= a.D) continue;
-            float x[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] = none ? 0.f : o[d][m][r] * inv;
-            if constexpr (IO::SIZE == 2)
-                *(uint2*)(op + d0) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-            else
-                *(float4*)(op + d0) = make_float4(x[0], x[1], x[2], x[3]);
+            put4<IO>(op + d0, none ? f32x4{0.f, 0.f, 0.f, 0.f} : o[d][m] * inv);
         }
         if (a.lse && g == 0) a.lse[((int64_t)b * a.H + h) * a.Lq + i] = ls * LN2;
     }
 }
 
-// Joins the splits of a row: o = sum_s 2^(lse_s - lse) o_s.  One wave per row, 64 columns a turn.
+// Few rows (decoding): the rows of one key head are RT at most, and a key is read once and used
+// for them all in vector registers; the matrix instructions would leave 16 - RT of their columns
+// idle and make every key pass through LDS.  LPK lanes hold a key's D values (one 16-byte vector
+// each), a wave reads 64 / LPK keys a load, and every group of LPK lanes keeps running statistics
+// of its own, joined over the wave by shuffles and over the waves through LDS at the end.
+template <class IO, int LPK, int RT, bool CAP>
+__global__ __launch_bounds__(NT) void attn_few(AttnArgs a)
+{
+    using E = typename IO::T;
+    constexpr int V = vec_elems<IO>, KPW = 64 / LPK;   // keys of a load
+    constexpr int U = 4;                               // loads in flight of k, and of v
+    constexpr int STEP = KPW * U;                      // keys of a wave's turn
+    __shared__ float sm[4][RT], sl[4][RT], so[4][RT][LPK * V];
+
+    uint32_t id = blockIdx.x;
+    const int bh = (int)(id % (uint32_t)a.nbh), split = (int)(id / (uint32_t)a.nbh);
+    const int b = bh / a.Hkv, hk = bh % a.Hkv;
+    const int n = seq_len(a, b);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int grp = lane / LPK, d0 = lane % LPK * V;
+    const bool din = d0 < a.D;
+    const int32_t* doc = a.doc ? a.doc + (int64_t)b * a.Lk : nullptr;
+
+    float q[RT][V], slope[RT], acc[RT][V], mx[RT], sum[RT];
+    int lo[RT], pos[RT], klo = BIG, khi = -1, last = 0, first = BIG;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        const bool in = r < a.nrow;
+        const int i = in ? r / a.G : 0, h = hk * a.G + (in ? r % a.G : 0);
+        pos[r] = n - a.Lq + i;
+        lo[r] = in ? first_key(a, b, pos[r], n) : BIG;
+        if (lo[r] != BIG) {
+            klo = min(klo, lo[r]);
+            khi = max(khi, pos[r]);
+        }
+        last = max(last, lo[r]);      // BIG for an empty row: its scores are always masked
+        first = min(first, pos[r]);
+        slope[r] = a.slopes ? a.slopes[h] * LOG2E : 0.f;
+        const bool on = lo[r] != BIG && din;
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (on) raw = *(const uint4*)((const E*)a.q + b * a.qs[0] + (int64_t)i * a.qs[1] + h * a.qs[2] + d0);
+        const Lanes<IO> x = widen<IO>(raw);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            q[r][e] = x.x[e];
+            acc[r][e] = 0.f;
+        }
+        mx[r] = -INFINITY;
+        sum[r] = 0.f;
+    }
+    // this split's keys, whole turns of the four waves
+    int k0 = 0, k1 = 0;
+    if (khi >= 0) {
+        const int turns = (khi - klo + 1 + 4 * STEP - 1) / (4 * STEP);
+        const int per = (turns + a.nsplit - 1) / a.nsplit;
+        const int64_t s0 = (int64_t)klo + (int64_t)split * per * 4 * STEP;
+        k0 = (int)min<int64_t>(s0, khi + 1);
+        k1 = (int)min<int64_t>(s0 + (int64_t)per * 4 * STEP, khi + 1);
+    }
+    const float scale2 = CAP ? a.scale / a.cap : a.scale * LOG2E, cap2 = a.cap * LOG2E;
+    const E* kp = (const E*)a.k + b * a.ks[0] + hk * a.ks[2] + (din ? d0 : 0);
+    const E* vp = (const E*)a.v + b * a.vs[0] + hk * a.vs[2] + (din ? d0 : 0);
+    for (int j0 = k0 + wave * STEP; j0 < k1; j0 += 4 * STEP) {
+        uint4 rk[U], rv[U];
+        bool on[U];
+#pragma unroll
+        for (int t = 0; t < U; ++t) {
+            const int j = j0 + t * KPW + grp, jc = j < k1 ? j : k1 - 1;   // some key of the sequence
+            on[t] = j < k1 && (!doc || doc[jc] <= jc);
+            rk[t] = *(const uint4*)(kp + (int64_t)jc * a.ks[1]);
+            rv[t] = *(const uint4*)(vp + (int64_t)jc * a.vs[1]);
+        }
+        const bool edge = j0 < last || j0 + STEP - 1 > first || j0 + STEP > k1 || doc;
+        float s[RT][U];
+#pragma unroll
+        for (int t = 0; t < U; ++t) {
+            // padding reads as 0, whatever the memory holds
+            const Lanes<IO> k = widen<IO>(on[t] && din ? rk[t] : make_uint4(0, 0, 0, 0));
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                float x = 0.f;
+#pragma unroll
+                for (int e = 0; e < V; ++e) x = __builtin_fmaf(q[r][e], k.x[e], x);
+                s[r][t] = x;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int t = 0; t < U; ++t) s[r][t] = lane_sum<LPK>(s[r][t]);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const float base = mx[r] == -INFINITY ? 0.f : mx[r];
+            float top = -INFINITY;
+#pragma unroll
+            for (int t = 0; t < U; ++t) {
+                const int j = j0 + t * KPW + grp;
+                const float add = __builtin_fmaf(slope[r], (float)(j - pos[r]), -base);
+                float x;
+                if constexpr (CAP) x = __builtin_fmaf(cap2, tanh_of<IO>(s[r][t] * scale2), add);
+                else x = __builtin_fmaf(s[r][t], scale2, add);
+                if (edge && (!on[t] || j < lo[r] || j > pos[r])) x = -INFINITY;
+                s[r][t] = x;
+                top = fmaxf(top, x);
+            }
+            if (__any(top > (mx[r] == -INFINITY ? -INFINITY : SLACK))) {
+                if (top > (mx[r] == -INFINITY ? -INFINITY : SLACK)) {
+                    const float now = base + top, f = exp2_hw(mx[r] - now);
+                    sum[r] *= f;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) acc[r][e] *= f;
+                    mx[r] = now;
+#pragma unroll
+                    for (int t = 0; t < U; ++t) s[r][t] -= top;
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < U; ++t) {
+                s[r][t] = exp2_hw(s[r][t]);
+                sum[r] += s[r][t];
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < U; ++t) {
+            const Lanes<IO> v = widen<IO>(on[t] && din ? rv[t] : make_uint4(0, 0, 0, 0));
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int e = 0; e < V; ++e) acc[r][e] = __builtin_fmaf(s[r][t], v.x[e], acc[r][e]);
+        }
+    }
+    // join the wave's groups, then the waves
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        float top = mx[r];
+#pragma unroll
+        for (int m = LPK; m < 64; m <<= 1) top = fmaxf(top, __shfl_xor(top, m));
+        const float f = mx[r] == -INFINITY ? 0.f : exp2_hw(mx[r] - top);
+        sum[r] *= f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[r][e] *= f;
+#pragma unroll
+        for (int m = LPK; m < 64; m <<= 1) {
+            sum[r] += __shfl_xor(sum[r], m);
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[r][e] += __shfl_xor(acc[r][e], m);
+        }
+        if (lane < LPK) {
+            if (lane == 0) {
+                sm[wave][r] = top;
+                sl[wave][r] = sum[r];
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) so[wave][r][d0 + e] = acc[r][e];
+        }
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < RT * LPK * V; x += NT) {
+        const int r = x / (LPK * V), d = x % (LPK * V);
+        if (r >= a.nrow || d >= a.D) continue;
+        const float top = fmaxf(fmaxf(sm[0][r], sm[1][r]), fmaxf(sm[2][r], sm[3][r]));
+        float l = 0.f, o = 0.f;
+        if (top != -INFINITY)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float f = exp2_hw(sm[w][r] - top);
+                l = __builtin_fmaf(f, sl[w][r], l);
+                o = __builtin_fmaf(f, so[w][r][d], o);
+            }
+        o = top == -INFINITY ? 0.f : o / l;
+        const float ls = top == -INFINITY ? -INFINITY : top + __builtin_amdgcn_logf(l);
+        const int i = r / a.G, h = hk * a.G + r % a.G;
+        if (a.nsplit > 1) {
+            const int64_t at = ((int64_t)split * a.nbh + bh) * a.nrow + r;
+            a.part[at * a.D + d] = o;
+            if (d == 0) a.part_lse[at] = ls;
+        } else {
+            IO::store((E*)a.o + b * a.os[0] + (int64_t)i * a.os[1] + h * a.os[2], d, o);
+            if (a.lse && d == 0) a.lse[((int64_t)b * a.H + h) * a.Lq + i] = ls * LN2;
+        }
+    }
+}
+
+// Joins the splits of a row: o = sum_s 2^(lse_s - lse) o_s.  One wave per row: lane s weighs
+// split s (at most 64), then the lanes hold the columns.
 template <class IO>
 __global__ __launch_bounds__(NT) void attn_join(AttnArgs a)
 {
@@ -275,41 +451,47 @@ __global__ __launch_bounds__(NT) void attn_join(AttnArgs a)
     const int64_t at = (int64_t)blockIdx.x * (NT / 64) + (threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
     if (at >= total) return;
-    float mx = -INFINITY;
-    for (int s = lane; s < a.nsplit; s += 64) mx = fmaxf(mx, a.part_lse[s * total + at]);
+    const float ls = lane < a.nsplit ? a.part_lse[lane * total + at] : -INFINITY;
+    float mx = ls;
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) mx = fmaxf(mx, __shfl_xor(mx, m));
-    const float base = mx == -INFINITY ? 0.f : mx;
-    float sum = 0.f;
-    for (int s = lane; s < a.nsplit; s += 64) sum += exp2_hw(a.part_lse[s * total + at] - base);
+    const float e = ls == -INFINITY ? 0.f : exp2_hw(ls - mx);
+    float sum = e;
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
+    const float w = sum > 0.f ? e / sum : 0.f;
     const int bh = (int)(at / a.nrow), r = (int)(at % a.nrow);
     const int b = bh / a.Hkv, i = r / a.G, h = bh % a.Hkv * a.G + r % a.G;
-    const float inv = sum > 0.f ? 1.0f / sum : 0.f;
     E* op = (E*)a.o + b * a.os[0] + (int64_t)i * a.os[1] + h * a.os[2];
-    for (int d = lane; d < a.D; d += 64) {
+    for (int d = lane; d < (a.D + 63) / 64 * 64; d += 64) {
+        const float* p = a.part + at * a.D + min(d, a.D - 1);
         float x = 0.f;
-        for (int s = 0; s < a.nsplit; ++s) {
-            const float w = exp2_hw(a.part_lse[s * total + at] - base) * inv;
-            x = __builtin_fmaf(w, a.part[(s * total + at) * a.D + d], x);
-        }
-        IO::store(op, d, x);
+#pragma unroll 8
+        for (int s = 0; s < a.nsplit; ++s)
+            x = __builtin_fmaf(__shfl(w, s), p[s * total * a.D], x);
+        if (d < a.D) IO::store(op, d, x);
     }
     if (a.lse && lane == 0)
         a.lse[((int64_t)b * a.H + h) * a.Lq + i] = sum > 0.f ? (mx + __builtin_amdgcn_logf(sum)) * LN2 : -INFINITY;
 }
 
+#ifndef FEWFILL
+#define FEWFILL 1024
+#endif
+// Rows of a key head up to this go to attn_few.
+constexpr int FEW = 8;
 // Key splits: as many as fill the GPU when the rows alone do not, each of at least 256 keys.
-constexpr int64_t FILL = 512;
+constexpr int64_t FILL = 512, FILL_FEW = FEWFILL;
 constexpr int64_t SPLIT_MIN = 256;
-constexpr int64_t SPLIT_MAX = 64;
+constexpr int64_t SPLIT_MAX = 64;   // attn_join weighs one split a lane
 
-int splits(int64_t wgs, int64_t Lk, int window, int64_t Lq)
+int splits(const AttnArgs& a)
 {
-    const int64_t keys = std::min<int64_t>(Lk, (int64_t)window + std::min<int64_t>(Lq, BM));
-    if (wgs <= 0 || 2 * wgs > FILL) return 1;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({(FILL + wgs - 1) / wgs, keys / SPLIT_MIN, SPLIT_MAX}));
+    const bool few = a.nrow <= FEW;
+    const int64_t wgs = (few ? 1 : (a.nrow + BM - 1) / BM) * (int64_t)a.nbh, fill = few ? FILL_FEW : FILL;
+    const int64_t keys = std::min<int64_t>(a.Lk, (int64_t)a.window + std::min<int64_t>(a.Lq, BM));
+    if (wgs <= 0 || 2 * wgs > fill) return 1;
+    return (int)std::max<int64_t>(1, std::min<int64_t>({(fill + wgs - 1) / wgs, keys / SPLIT_MIN, SPLIT_MAX}));
 }
 
 template <class IO, int DP, bool CAP, bool BIAS>
@@ -327,16 +509,38 @@ hipError_t pick(const AttnArgs& a, int64_t blocks, hipStream_t st)
     return a.slopes ? go<IO, DP, false, true>(a, blocks, st) : go<IO, DP, false, false>(a, blocks, st);
 }
 
+template <class IO, int LPK, int RT>
+hipError_t few(const AttnArgs& a, int64_t blocks, hipStream_t st)
+{
+    if (a.cap > 0.f)
+        hipLaunchKernelGGL((attn_few<IO, LPK, RT, true>), dim3((unsigned)blocks), dim3(NT), 0, st, a);
+    else
+        hipLaunchKernelGGL((attn_few<IO, LPK, RT, false>), dim3((unsigned)blocks), dim3(NT), 0, st, a);
+    return hipGetLastError();
+}
+
+template <class IO, int LPK>
+hipError_t few_rows(const AttnArgs& a, int64_t blocks, hipStream_t st)
+{
+    return a.nrow == 1   ? few<IO, LPK, 1>(a, blocks, st)
+           : a.nrow == 2 ? few<IO, LPK, 2>(a, blocks, st)
+           : a.nrow <= 4 ? few<IO, LPK, 4>(a, blocks, st)
+                         : few<IO, LPK, 8>(a, blocks, st);
+}
+
 template <class IO>
 hipError_t run(AttnArgs a, hipStream_t st)
 {
-    a.ntile = (a.nrow + BM - 1) / BM;
-    const int64_t wgs = (int64_t)a.ntile * a.nbh;
-    a.nsplit = splits(wgs, a.Lk, a.window, a.Lq);
-    const int64_t blocks = wgs * a.nsplit;
+    constexpr int LPK = 64 / vec_elems<IO>;   // lanes of a key of 64
+    const bool is_few = a.nrow <= FEW;
+    a.ntile = is_few ? 1 : (a.nrow + BM - 1) / BM;
+    a.nsplit = splits(a);
+    const int64_t blocks = (int64_t)a.ntile * a.nbh * a.nsplit;
     if (!grid_ok(blocks, NT)) return hipErrorInvalidValue;
     a.part_lse = a.part + (int64_t)a.nsplit * a.nbh * a.nrow * a.D;
-    const hipError_t e = a.D <= 64 ? pick<IO, 64>(a, blocks, st) : pick<IO, 128>(a, blocks, st);
+    hipError_t e;
+    if (is_few) e = a.D <= 64 ? few_rows<IO, LPK>(a, blocks, st) : few_rows<IO, 2 * LPK>(a, blocks, st);
+    else e = a.D <= 64 ? pick<IO, 64>(a, blocks, st) : pick<IO, 128>(a, blocks, st);
     if (e != hipSuccess || a.nsplit == 1) return e;
     const int64_t jb = ((int64_t)a.nbh * a.nrow + NT / 64 - 1) / (NT / 64);
     hipLaunchKernelGGL((attn_join<IO>), dim3((unsigned)jb), dim3(NT), 0, st, a);
@@ -347,9 +551,8 @@ hipError_t run(AttnArgs a, hipStream_t st)
 
 size_t attn_fwd_bytes(const AttnArgs& a)
 {
-    const int64_t rows = (int64_t)a.nbh * a.nrow;
-    const int ns = splits((a.nrow + BM - 1) / BM * (int64_t)a.nbh, a.Lk, a.window, a.Lq);
-    return ns > 1 ? (size_t)ns * rows * (a.D + 1) * sizeof(float) : 0;
+    const int ns = splits(a);
+    return ns > 1 ? (size_t)ns * a.nbh * a.nrow * (a.D + 1) * sizeof(float) : 0;
 }
 
 hipError_t launch_attn(Store s, const AttnArgs& a, void* ws, hipStream_t st)

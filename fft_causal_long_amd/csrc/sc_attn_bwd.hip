@@ -7,14 +7,15 @@
 //     dx_ij = dS_ij (1 - tanh^2),   dq_i = scale sum_j dx_ij k_j,   dk_j = scale sum_i dx_ij q_i
 //
 // Two kernels, neither with atomics, so the sums have a fixed order:
-//  * attn_bwd_q: a workgroup owns 128 packed rows (token r / G, head r % G of the group) and
-//    walks key tiles; it makes delta on the way in and leaves (lse, delta) of each row and the
-//    key range of each 32-row strip for the second kernel.
-//  * attn_bwd_kv: a workgroup owns 128 keys of a key head and walks the strips of packed rows,
-//    all heads of the group in turn, so the gradients of shared heads are plain sums.
+//  * attn_bwd_q: a workgroup owns 128 tokens of one head and walks key tiles; it makes delta on
+//    the way in and leaves (lse, delta) of each row for the second kernel, and with documents
+//    the key range of each 32-token strip.
+//  * attn_bwd_kv: a workgroup owns 128 keys of a key head and walks the tokens that see them, all
+//    heads of the group in turn, so the gradients of shared heads are plain sums.
 // Both keep their own side's operands in registers (B operands), stage the other side through
-// LDS, and feed the score-shaped products to the next product from registers (sc_attn.h).
-// Seven products instead of the five of a single kernel that would add dq with atomics.
+// LDS with the next stage's loads in flight, and feed the score-shaped products to the next
+// product from registers (sc_attn.h).  Seven products instead of the five of a single kernel
+// that would add dq with atomics.
 
 #include <hip/hip_runtime.h>
 
@@ -29,73 +30,66 @@ namespace {
 
 using namespace attn;
 
-constexpr int BN = 64;        // keys of a tile (attn_bwd_q)
+constexpr int BN = 64;        // keys of a tile (attn_bwd_q), tokens of a stage (attn_bwd_kv)
 constexpr int NQ = 2;         // 16-row blocks of a wave
-constexpr int WM = 16 * NQ;   // rows of a wave and of a strip
-constexpr int BM = 4 * WM;    // rows of a workgroup
-constexpr int NK = 2;         // 16-key blocks of a wave (attn_bwd_kv)
-constexpr int WK = 16 * NK;
-constexpr int BK = 4 * WK;    // keys of a workgroup
+constexpr int WM = 16 * NQ;   // tokens of a wave and of a strip
+constexpr int BM = 4 * WM;    // tokens of a workgroup
 
-// Score and the factor of dS that the cap adds; y = raw product q.k, dist = j - p.
-template <class IO, bool CAP, bool BIAS>
-__device__ __forceinline__ float score2(float y, float scale2, float cap2, float slope, float dist,
-                                        float& dcap)
+// 16-key blocks of a wave (attn_bwd_kv): float32 operands of 128 leave room for one
+template <class IO, int DP>
+constexpr int key_blocks = IO::SIZE == 4 && DP == 128 ? 1 : 2;
+
+#ifndef BQV
+#define BQV(DP, SZ) (SZ == 4 ? 1 : DP == 64 ? 3 : 2)
+#endif
+#ifndef BKV
+#define BKV(DP, SZ) (SZ == 4 ? 1 : DP == 64 ? 2 : 1)
+#endif
+
+// The score in base 2 of the raw product y plus `add`; dcap: the factor of dS that the cap adds.
+template <class IO, bool CAP>
+__device__ __forceinline__ float score2(float y, float scale2, float cap2, float add, float& dcap)
 {
-    float x;
     if constexpr (CAP) {
         const float t = tanh_of<IO>(y * scale2);
         dcap = 1.0f - t * t;
-        x = cap2 * t;
-        if constexpr (BIAS) x = __builtin_fmaf(slope, dist, x);
-    } else if constexpr (BIAS) {
-        x = __builtin_fmaf(y, scale2, slope * dist);
+        return __builtin_fmaf(cap2, t, add);
     } else {
-        x = y * scale2;
+        return __builtin_fmaf(y, scale2, add);
     }
-    return x;
 }
 
 template <class IO, int DP, bool CAP, bool BIAS>
-__global__ __launch_bounds__(NT) void attn_bwd_q(AttnArgs a)
+__global__ __launch_bounds__(NT, BQV(DP, IO::SIZE)) void attn_bwd_q(AttnArgs a)
 {
     using E = typename IO::T;
-    constexpr int P = pitch<IO, DP>, V = vec_elems<IO>, CH = DP / V, NCH = BN * CH / NT;
-    constexpr int KK = DP / 32, ND = DP / 16;
+    constexpr int P = pitch<IO, DP>, V = vec_elems<IO>, KK = DP / 32, ND = DP / 16;
     __shared__ __attribute__((aligned(16))) E Kt[BN * P];
     __shared__ __attribute__((aligned(16))) E Vt[BN * P];
     __shared__ int range[2][4];
 
+    const int nbh = a.B * a.H;
     uint32_t id = blockIdx.x;
-    const int bh = (int)(id % (uint32_t)a.nbh);
-    const int tile = a.ntile - 1 - (int)(id / (uint32_t)a.nbh);
-    const int b = bh / a.Hkv, hk = bh % a.Hkv;
+    const int bh = (int)(id % (uint32_t)nbh);
+    const int tile = a.ntile - 1 - (int)(id / (uint32_t)nbh);
+    const int b = bh / a.H, h = bh % a.H, hk = h / a.G;
     const int n = seq_len(a, b);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
 
-    int row[NQ], pos[NQ], lo[NQ];
+    int pos[NQ], lo[NQ];
     bool empty[NQ];
     Frag<IO> q[NQ][KK], go[NQ][KK];
-    float slope[NQ], lse2[NQ], delta[NQ];
-    int wlo = BIG, whi = -1, mlo = 0, mpos = BIG;
+    float lse2[NQ], delta[NQ];
+    const int rw = tile * BM + wave * WM;
+    const float slope = BIAS ? a.slopes[h] * LOG2E : 0.f;
 #pragma unroll
     for (int m = 0; m < NQ; ++m) {
-        row[m] = tile * BM + wave * WM + 16 * m + c;
-        const bool in = row[m] < a.nrow;
-        const int i = in ? row[m] / a.G : 0, h = hk * a.G + (in ? row[m] % a.G : 0);
+        const int t = rw + 16 * m + c;
+        const bool in = t < a.Lq;
+        const int i = in ? t : 0;
         pos[m] = n - a.Lq + i;
         lo[m] = in ? first_key(a, b, pos[m], n) : BIG;
         empty[m] = lo[m] == BIG;
-        if (!empty[m]) {
-            wlo = min(wlo, lo[m]);
-            whi = max(whi, pos[m]);
-            mlo = max(mlo, lo[m]);
-            mpos = min(mpos, pos[m]);
-        } else {
-            lo[m] = 0;
-            pos[m] = BIG;
-        }
-        slope[m] = BIAS ? a.slopes[h] * LOG2E : 0.f;
         // an empty row's weights are 2^-inf = 0
         lse2[m] = empty[m] ? INFINITY : a.lse[((int64_t)b * a.H + h) * a.Lq + i] * LOG2E;
         const E* qp = (const E*)a.q + b * a.qs[0] + (int64_t)i * a.qs[1] + h * a.qs[2];
@@ -125,22 +119,33 @@ __global__ __launch_bounds__(NT) void attn_bwd_q(AttnArgs a)
             }
         }
         delta[m] = gsum(dl);
-        if (g == 0 && in) a.rowstat[(int64_t)bh * a.nrow + row[m]] = make_float2(lse2[m], delta[m]);
+        if (g == 0 && in) a.rowstat[(int64_t)bh * a.Lq + i] = make_float2(lse2[m], delta[m]);
     }
-    wlo = wave_min(wlo);
-    whi = wave_max(whi);
-    mlo = wave_max(mlo);
-    mpos = wave_min(mpos);
-    if (lane == 0) {
-        range[0][wave] = wlo;
-        range[1][wave] = whi;
-        // every key head's rows have the same ranges: the first one's workgroup records them
-        if (hk == 0)
-            a.strips[(int64_t)b * a.ntile * 4 + tile * 4 + wave] = make_int4(wlo, whi, mlo, mpos);
+    const RowRange rr = a.doc ? lanes_range(lo, pos) : token_range(a, n, rw, WM);
+    int klo, khi;
+    if (a.doc) {
+        if (lane == 0) {
+            range[0][wave] = rr.lo;
+            range[1][wave] = rr.hi;
+            // every head's rows have the same ranges: the first one's workgroup records them
+            if (h == 0) a.strips[((int64_t)b * a.ntile + tile) * 4 + wave] = make_int4(rr.lo, rr.hi, rr.last, rr.pos);
+        }
+        __syncthreads();
+        klo = min(min(range[0][0], range[0][1]), min(range[0][2], range[0][3]));
+        khi = max(max(range[1][0], range[1][1]), max(range[1][2], range[1][3]));
+    } else {
+        const RowRange all = token_range(a, n, tile * BM, BM);
+        klo = all.lo;
+        khi = all.hi;
     }
-    __syncthreads();
-    const int klo = min(min(range[0][0], range[0][1]), min(range[0][2], range[0][3]));
-    const int khi = max(max(range[1][0], range[1][1]), max(range[1][2], range[1][3]));
+    klo = __builtin_amdgcn_readfirstlane(klo);
+    khi = __builtin_amdgcn_readfirstlane(khi);
+#pragma unroll
+    for (int m = 0; m < NQ; ++m)
+        if (empty[m]) {
+            lo[m] = 0;
+            pos[m] = BIG;
+        }
     const int t0 = khi < 0 ? 0 : klo / BN, t1 = khi < 0 ? 0 : khi / BN + 1;
 
     const float scale2 = CAP ? a.scale / a.cap : a.scale * LOG2E, cap2 = a.cap * LOG2E;
@@ -150,36 +155,17 @@ __global__ __launch_bounds__(NT) void attn_bwd_q(AttnArgs a)
 #pragma unroll
         for (int m = 0; m < NQ; ++m) acc[d][m] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const E* kp = (const E*)a.k + b * a.ks[0] + hk * a.ks[2];
-    const E* vp = (const E*)a.v + b * a.vs[0] + hk * a.vs[2];
-    uint4 rk[NCH], rv[NCH];
-    int rdoc = 0;
-    auto fetch = [&](int j0) {
-#pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-            const int id_ = tid + NT * i, j = j0 + id_ / CH, d = (id_ % CH) * V;
-            const bool on = d < a.D && key_live(a, b, j, n);
-            rk[i] = on ? *(const uint4*)(kp + (int64_t)j * a.ks[1] + d) : make_uint4(0, 0, 0, 0);
-            rv[i] = on ? *(const uint4*)(vp + (int64_t)j * a.vs[1] + d) : make_uint4(0, 0, 0, 0);
-        }
-        if (a.doc) rdoc = j0 + lane < n ? a.doc[(int64_t)b * a.Lk + j0 + lane] : BIG;
-    };
-    if (t0 < t1) fetch(t0 * BN);
+    KeyTiles<IO, DP> tiles(a, b, hk, n, tid);
+    if (t0 < t1) tiles.fetch(t0 * BN);
     for (int t = t0; t < t1; ++t) {
         const int j0 = t * BN;
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-            const int id_ = tid + NT * i, at = (id_ / CH) * P + (id_ % CH) * V;
-            *(uint4*)(Kt + at) = rk[i];
-            *(uint4*)(Vt + at) = rv[i];
-        }
-        const uint64_t live = a.doc ? __ballot(rdoc <= j0 + lane) : ~0ull;
+        const uint64_t live = tiles.put(Kt, Vt, j0);
         __syncthreads();
-        if (t + 1 < t1) fetch(j0 + BN);
-        if (j0 > whi || j0 + BN - 1 < wlo) continue;
+        if (t + 1 < t1) tiles.fetch(j0 + BN);
+        if (j0 > rr.hi || j0 + BN - 1 < rr.lo) continue;
 
-        const bool edge = j0 < mlo || j0 + BN - 1 > mpos || live != ~0ull;
+        const bool edge = j0 < rr.last || j0 + BN - 1 > rr.pos || live != ~0ull;
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {   // 32 keys at a time
             f32x4 s[2][NQ], dp[2][NQ];
@@ -201,20 +187,36 @@ __global__ __launch_bounds__(NT) void attn_bwd_q(AttnArgs a)
             Frag<IO> w[NQ];
 #pragma unroll
             for (int m = 0; m < NQ; ++m) {
-                const float far = (float)(j0 + 4 * g - pos[m]);
+                const float shift = BIAS ? slope * (float)(j0 + 4 * g - pos[m]) - lse2[m] : -lse2[m];
+                f32x4 cf[2];   // the cap's factors
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int jj = 32 * hf + 16 * kb + 4 * g + r, j = j0 + jj;
+                        const float add = BIAS ? __builtin_fmaf(slope, (float)(32 * hf + 16 * kb + r), shift) : shift;
                         float dcap = 1.f;
-                        const float x = score2<IO, CAP, BIAS>(s[kb][m][r], scale2, cap2, slope[m],
-                                                          far + (float)(32 * hf + 16 * kb + r), dcap);
-                        float p = exp2_hw(x - lse2[m]);
-                        if (edge && (j < lo[m] || j > pos[m] || !(live >> jj & 1))) p = 0.f;
-                        float ds = p * (dp[kb][m][r] - delta[m]);
-                        if constexpr (CAP) ds *= dcap;
-                        s[kb][m][r] = ds;
+                        s[kb][m][r] = exp2_hw(score2<IO, CAP>(s[kb][m][r], scale2, cap2, add, dcap));
+                        cf[kb][r] = dcap;
+                    }
+                if (edge) {
+                    keep_branch();
+                    const int first = lo[m] - j0 - 4 * g;
+                    const uint32_t span = (uint32_t)(pos[m] - lo[m]);
+                    const uint64_t mine = live >> (4 * g);
+#pragma unroll
+                    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int jj = 32 * hf + 16 * kb + r;
+                            if ((uint32_t)(jj - first) > span || !(mine >> jj & 1)) s[kb][m][r] = 0.f;
+                        }
+                }
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        s[kb][m][r] *= dp[kb][m][r] - delta[m];
+                        if constexpr (CAP) s[kb][m][r] *= cf[kb][r];
                     }
                 w[m] = frag_of<IO>(s[0][m], s[1][m]);
             }
@@ -228,37 +230,27 @@ __global__ __launch_bounds__(NT) void attn_bwd_q(AttnArgs a)
     }
 #pragma unroll
     for (int m = 0; m < NQ; ++m) {
-        if (row[m] >= a.nrow) continue;
-        const int i = row[m] / a.G, h = hk * a.G + row[m] % a.G;
-        E* p = (E*)a.dq + b * a.dqs[0] + (int64_t)i * a.dqs[1] + h * a.dqs[2];
-        const float f = empty[m] ? 0.f : a.scale;
+        const int t = rw + 16 * m + c;
+        if (t >= a.Lq) continue;
+        E* p = (E*)a.dq + b * a.dqs[0] + (int64_t)t * a.dqs[1] + h * a.dqs[2];
 #pragma unroll
         for (int d = 0; d < ND; ++d) {
             const int d0 = 16 * d + 4 * g;
-            if (d0 >= a.D) continue;
-            float x[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] = empty[m] ? 0.f : f * acc[d][m][r];
-            if constexpr (IO::SIZE == 2)
-                *(uint2*)(p + d0) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-            else
-                *(float4*)(p + d0) = make_float4(x[0], x[1], x[2], x[3]);
+            if (d0 < a.D) put4<IO>(p + d0, empty[m] ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[d][m] * a.scale);
         }
     }
 }
 
 template <class IO, int DP, bool CAP, bool BIAS>
-__global__ __launch_bounds__(NT) void attn_bwd_kv(AttnArgs a)
+__global__ __launch_bounds__(NT, BKV(DP, IO::SIZE)) void attn_bwd_kv(AttnArgs a)
 {
     using E = typename IO::T;
-    constexpr int P = pitch<IO, DP>, V = vec_elems<IO>, CH = DP / V;
-    constexpr int NCH = (WM * CH + NT - 1) / NT;
-    constexpr int KK = DP / 32, ND = DP / 16;
-    static_assert(WM * CH % NT == 0, "whole rounds of loads");
-    __shared__ __attribute__((aligned(16))) E Qt[WM * P];
-    __shared__ __attribute__((aligned(16))) E Gt[WM * P];
-    __shared__ __attribute__((aligned(16))) float Ls[WM], Dl[WM], Sl[WM];
-    __shared__ __attribute__((aligned(16))) int Lo[WM], Ps[WM];
+    constexpr int P = pitch<IO, DP>, V = vec_elems<IO>, CH = DP / V, NCH = BN * CH / NT;
+    constexpr int KK = DP / 32, ND = DP / 16, NK = key_blocks<IO, DP>, WK = 16 * NK, BK = 4 * WK;
+    __shared__ __attribute__((aligned(16))) E Qt[BN * P];
+    __shared__ __attribute__((aligned(16))) E Gt[BN * P];
+    __shared__ __attribute__((aligned(16))) float Rt[BN], Dl[BN];
+    __shared__ __attribute__((aligned(16))) int Lo[BN];
 
     uint32_t id = blockIdx.x;
     const int bh = (int)(id % (uint32_t)a.nbh);
@@ -296,136 +288,180 @@ __global__ __launch_bounds__(NT) void attn_bwd_kv(AttnArgs a)
         for (int m = 0; m < NK; ++m) dk[d][m] = dv[d][m] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     const float scale2 = CAP ? a.scale / a.cap : a.scale * LOG2E, cap2 = a.cap * LOG2E;
-    const int off = n - a.Lq;   // position of row 0
-    // strips of packed rows at positions jb .. jb + BK - 1 + window - 1
+    const int off = n - a.Lq;   // position of token 0
+    // stages of tokens at positions jb .. jb + BK - 1 + window - 1
     int s0 = 0, s1 = 0;
     {
         const int64_t plo = std::max<int64_t>(jb, off);
         const int64_t phi = std::min<int64_t>(n - 1, (int64_t)jb + BK - 1 + a.window - 1);
         if (plo <= phi) {
-            s0 = (int)((plo - off) * a.G / WM);
-            s1 = (int)(((phi - off + 1) * a.G - 1) / WM + 1);
+            s0 = (int)((plo - off) / BN);
+            s1 = (int)((phi - off) / BN + 1);
         }
     }
     const int4* strips = a.strips + (int64_t)b * a.ntile * 4;
-    // the next strip at or after s whose keys meet this workgroup's, 64 looked at together
+    // the next stage at or after s whose tokens see this workgroup's keys, 64 looked at together
     auto seek = [&](int s) {
+        if (!a.doc) return s;
         while (s < s1) {
             bool hit = false;
             if (s + lane < s1) {
-                const int4 r = strips[s + lane];
-                hit = r.x <= jb + BK - 1 && r.y >= jb;
+                const int4 x = strips[2 * (s + lane)], y = strips[2 * (s + lane) + 1];
+                hit = min(x.x, y.x) <= jb + BK - 1 && max(x.y, y.y) >= jb;
             }
             const uint64_t m = __ballot(hit);
-            if (m) return s + __builtin_ctzll(m);
+            if (m) return __builtin_amdgcn_readfirstlane(s + (int)__builtin_ctzll(m));
             s += 64;
         }
         return s1;
     };
 
-    uint4 rq[NCH], rg[NCH];
-    float2 rs = make_float2(0.f, 0.f);
-    int rlo = BIG, rpos = 0;
-    float rsl = 0.f;
-    auto fetch = [&](int s) {
+    const int r0 = tid / CH, d0 = tid % CH * V;
+    const bool din = d0 < a.D;
+    const int32_t* doc = a.doc ? a.doc + (int64_t)b * a.Lk : nullptr;
+    for (int h = hk * a.G; h < (hk + 1) * a.G; ++h) {
+        const E* qp = (const E*)a.q + b * a.qs[0] + h * a.qs[2] + (din ? d0 : 0);
+        const E* gp = (const E*)a.dout + b * a.dos[0] + h * a.dos[2] + (din ? d0 : 0);
+        const float2* stat = a.rowstat + ((int64_t)b * a.H + h) * a.Lq;
+        const float slope = BIAS ? a.slopes[h] * LOG2E : 0.f;
+        uint4 rq[NCH], rg[NCH];
+        float2 rs = make_float2(INFINITY, 0.f);
+        int rdoc = 0;
+        // nothing here waits for a load
+        auto fetch = [&](int s) {
+            const int tb = s * BN;
+            if (tb + BN <= a.Lq) {
+                const E *q = qp + (int64_t)(tb + r0) * a.qs[1], *g_ = gp + (int64_t)(tb + r0) * a.dos[1];
 #pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-            const int id_ = tid + NT * i, r = s * WM + id_ / CH, d = (id_ % CH) * V;
-            const bool in = r < a.nrow;
-            const int t = in ? r / a.G : 0, h = hk * a.G + (in ? r % a.G : 0);
-            const bool on = in && d < a.D && first_key(a, b, off + t, n) != BIG;
-            rq[i] = on ? *(const uint4*)((const E*)a.q + b * a.qs[0] + (int64_t)t * a.qs[1] + h * a.qs[2] + d)
-                       : make_uint4(0, 0, 0, 0);
-            rg[i] = on ? *(const uint4*)((const E*)a.dout + b * a.dos[0] + (int64_t)t * a.dos[1] + h * a.dos[2] + d)
-                       : make_uint4(0, 0, 0, 0);
-        }
-        if (tid < WM) {
-            const int r = s * WM + tid;
-            const bool in = r < a.nrow;
-            const int t = in ? r / a.G : 0;
-            rpos = off + t;
-            rlo = in ? first_key(a, b, rpos, n) : BIG;
-            rs = in ? a.rowstat[(int64_t)bh * a.nrow + r] : make_float2(INFINITY, 0.f);
-            rsl = BIAS && in ? a.slopes[hk * a.G + r % a.G] * LOG2E : 0.f;
-        }
-    };
-    int s = seek(s0);
-    if (s < s1) fetch(s);
-    while (s < s1) {
-        __syncthreads();
+                for (int i = 0; i < NCH; ++i) {
+                    rq[i] = *(const uint4*)(q + (int64_t)(NT / CH * i) * a.qs[1]);
+                    rg[i] = *(const uint4*)(g_ + (int64_t)(NT / CH * i) * a.dos[1]);
+                }
+            } else {
 #pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-            const int id_ = tid + NT * i, at = (id_ / CH) * P + (id_ % CH) * V;
-            *(uint4*)(Qt + at) = rq[i];
-            *(uint4*)(Gt + at) = rg[i];
-        }
-        if (tid < WM) {
-            Ls[tid] = rs.x;
-            Dl[tid] = rs.y;
-            Sl[tid] = rsl;
-            Lo[tid] = rlo;
-            Ps[tid] = rpos;
-        }
-        __syncthreads();
-        const int4 st = strips[s];   // lowest key, highest key, highest first key, lowest position
-        s = seek(s + 1);
-        if (s < s1) fetch(s);
-        if (st.x > jw + WK - 1 || st.y < jw) continue;   // no row of the strip sees this wave's keys
-        const bool edge = dead || st.z > jw || st.w < jw + WK - 1;
-
-        // rows x keys
-        f32x4 w[2][NK], dp[2][NK];
-#pragma unroll
-        for (int rb = 0; rb < 2; ++rb) {
-#pragma unroll
-            for (int m = 0; m < NK; ++m) w[rb][m] = dp[rb][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk) {
-                const int at = (16 * rb + c) * P + 32 * kk + 8 * g;
-                const Frag<IO> fq = frag_at<IO>(Qt + at), fg = frag_at<IO>(Gt + at);
-#pragma unroll
-                for (int m = 0; m < NK; ++m) {
-                    w[rb][m] = mma(fq, k[m][kk], w[rb][m]);
-                    dp[rb][m] = mma(fg, v[m][kk], dp[rb][m]);
+                for (int i = 0; i < NCH; ++i) {
+                    const int64_t t = min(tb + r0 + NT / CH * i, a.Lq - 1);
+                    rq[i] = *(const uint4*)(qp + t * a.qs[1]);
+                    rg[i] = *(const uint4*)(gp + t * a.dos[1]);
                 }
             }
-        }
+            const int t = min(tb + lane, a.Lq - 1);   // each wave: lane's row of the stage
+            rs = stat[t];
+            if (doc) rdoc = doc[min(max(off + t, 0), n - 1)];
+        };
+        int s = seek(s0);
+        if (s < s1) fetch(s);
+        while (s < s1) {
+            __syncthreads();
+            {
+                const int tb = s * BN, p = off + tb + lane;
+                int first = max(max(0, p - a.window + 1), doc ? rdoc : 0);
+                if (tb + lane >= a.Lq || p < 0 || first > p) first = BIG;
+                // empty rows read as 0, whatever the memory holds
+                const uint64_t alive = __ballot(first != BIG);
+                if (alive == ~0ull && DP == a.D) {
 #pragma unroll
-        for (int rb = 0; rb < 2; ++rb) {
-            const f32x4 ls = *(const f32x4*)(Ls + 16 * rb + 4 * g), dl = *(const f32x4*)(Dl + 16 * rb + 4 * g);
-            const int4 lo4 = *(const int4*)(Lo + 16 * rb + 4 * g), ps4 = *(const int4*)(Ps + 16 * rb + 4 * g);
-            const int lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, ps[4] = {ps4.x, ps4.y, ps4.z, ps4.w};
-            f32x4 sl = f32x4{0.f, 0.f, 0.f, 0.f};
-            if constexpr (BIAS) sl = *(const f32x4*)(Sl + 16 * rb + 4 * g);
+                    for (int i = 0; i < NCH; ++i) {
+                        const int at = (r0 + NT / CH * i) * P + d0;
+                        *(uint4*)(Qt + at) = rq[i];
+                        *(uint4*)(Gt + at) = rg[i];
+                    }
+                } else {
 #pragma unroll
-            for (int m = 0; m < NK; ++m)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    float dcap = 1.f;
-                    const float x = score2<IO, CAP, BIAS>(w[rb][m][r], scale2, cap2, sl[r],
-                                                      (float)(key[m] - ps[r]), dcap);
-                    float p = exp2_hw(x - ls[r]);
-                    if (edge && (key[m] < lo[r] || key[m] > ps[r])) p = 0.f;
-                    float ds = p * (dp[rb][m][r] - dl[r]);
-                    if constexpr (CAP) ds *= dcap;
-                    w[rb][m][r] = p;
-                    dp[rb][m][r] = ds;
+                    for (int i = 0; i < NCH; ++i) {
+                        const int r = r0 + NT / CH * i, at = r * P + d0;
+                        const bool on = din && alive >> r & 1;
+                        *(uint4*)(Qt + at) = on ? rq[i] : make_uint4(0, 0, 0, 0);
+                        *(uint4*)(Gt + at) = on ? rg[i] : make_uint4(0, 0, 0, 0);
+                    }
                 }
-        }
-        Frag<IO> fp[NK], fs[NK];
+                if (tid < BN) {
+                    // the row's part of the exponent: - lse (infinite for an empty row), and - slope of
+                    // its distance to the stage's first token
+                    Rt[tid] = first == BIG ? -INFINITY : BIAS ? -rs.x - slope * (float)tid : -rs.x;
+                    Dl[tid] = first == BIG ? 0.f : rs.y;
+                    Lo[tid] = first;
+                }
+            }
+            __syncthreads();
+            const int tb = s * BN, pb = off + tb;
+            s = seek(s + 1);
+            if (s < s1) fetch(s);
 #pragma unroll
-        for (int m = 0; m < NK; ++m) {
-            fp[m] = frag_of<IO>(w[0][m], w[1][m]);
-            fs[m] = frag_of<IO>(dp[0][m], dp[1][m]);
-        }
+            for (int hf = 0; hf < 2; ++hf) {   // 32 tokens at a time
+                const int tw = tb + 32 * hf;
+                RowRange st;
+                if (doc) {
+                    const int4 x = strips[tw / WM];
+                    st = {x.x, x.y, x.z, x.w};
+                } else {
+                    st = token_range(a, n, tw, WM);
+                }
+                if (st.lo > jw + WK - 1 || st.hi < jw) continue;   // no row of the strip sees this wave's keys
+                const bool edge = dead || st.last > jw || st.pos < jw + WK - 1;
+                // rows x keys
+                f32x4 w[2][NK], dp[2][NK];
 #pragma unroll
-        for (int d = 0; d < ND; ++d) {
-            const Frag<IO> fg = frag_tr<IO, P>(Gt, 0, 16 * d, g, c);
-            const Frag<IO> fq = frag_tr<IO, P>(Qt, 0, 16 * d, g, c);
+                for (int rb = 0; rb < 2; ++rb) {
 #pragma unroll
-            for (int m = 0; m < NK; ++m) {
-                dv[d][m] = mma(fg, fp[m], dv[d][m]);
-                dk[d][m] = mma(fq, fs[m], dk[d][m]);
+                    for (int m = 0; m < NK; ++m) w[rb][m] = dp[rb][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int kk = 0; kk < KK; ++kk) {
+                        const int at = (32 * hf + 16 * rb + c) * P + 32 * kk + 8 * g;
+                        const Frag<IO> fq = frag_at<IO>(Qt + at), fg = frag_at<IO>(Gt + at);
+#pragma unroll
+                        for (int m = 0; m < NK; ++m) {
+                            w[rb][m] = mma(fq, k[m][kk], w[rb][m]);
+                            dp[rb][m] = mma(fg, v[m][kk], dp[rb][m]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int rb = 0; rb < 2; ++rb) {
+                    const int rr = 32 * hf + 16 * rb + 4 * g;
+                    const f32x4 rt = *(const f32x4*)(Rt + rr), dl = *(const f32x4*)(Dl + rr);
+#pragma unroll
+                    for (int m = 0; m < NK; ++m) {
+                        const float kterm = BIAS ? slope * (float)(key[m] - pb) : 0.f;
+                        f32x4 cf;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            float dcap = 1.f;
+                            const float add = BIAS ? rt[r] + kterm : rt[r];
+                            w[rb][m][r] = exp2_hw(score2<IO, CAP>(w[rb][m][r], scale2, cap2, add, dcap));
+                            cf[r] = dcap;
+                        }
+                        if (edge) {
+                            keep_branch();
+                            const int4 lo4 = *(const int4*)(Lo + rr);
+                            const int lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w};
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                if (key[m] < lo[r] || key[m] > pb + rr + r) w[rb][m][r] = 0.f;
+                        }
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            dp[rb][m][r] = w[rb][m][r] * (dp[rb][m][r] - dl[r]);
+                            if constexpr (CAP) dp[rb][m][r] *= cf[r];
+                        }
+                    }
+                }
+                Frag<IO> fp[NK], fs[NK];
+#pragma unroll
+                for (int m = 0; m < NK; ++m) {
+                    fp[m] = frag_of<IO>(w[0][m], w[1][m]);
+                    fs[m] = frag_of<IO>(dp[0][m], dp[1][m]);
+                }
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+                    const Frag<IO> fg = frag_tr<IO, P>(Gt, 32 * hf, 16 * d, g, c);
+                    const Frag<IO> fq = frag_tr<IO, P>(Qt, 32 * hf, 16 * d, g, c);
+#pragma unroll
+                    for (int m = 0; m < NK; ++m) {
+                        dv[d][m] = mma(fg, fp[m], dv[d][m]);
+                        dk[d][m] = mma(fq, fs[m], dk[d][m]);
+                    }
+                }
             }
         }
     }
@@ -437,16 +473,10 @@ __global__ __launch_bounds__(NT) void attn_bwd_kv(AttnArgs a)
         E* vp = (E*)a.dv + b * a.dvs[0] + (int64_t)j * a.dvs[1] + hk * a.dvs[2];
 #pragma unroll
         for (int d = 0; d < ND; ++d) {
-            const int d0 = 16 * d + 4 * g;
-            if (d0 >= a.D) continue;
-            const f32x4 x = dk[d][m] * a.scale, y = dv[d][m];
-            if constexpr (IO::SIZE == 2) {
-                *(uint2*)(kp + d0) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-                *(uint2*)(vp + d0) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-            } else {
-                *(float4*)(kp + d0) = make_float4(x[0], x[1], x[2], x[3]);
-                *(float4*)(vp + d0) = make_float4(y[0], y[1], y[2], y[3]);
-            }
+            const int x = 16 * d + 4 * g;
+            if (x >= a.D) continue;
+            put4<IO>(kp + x, dk[d][m] * a.scale);
+            put4<IO>(vp + x, dv[d][m]);
         }
     }
 }
@@ -454,7 +484,8 @@ __global__ __launch_bounds__(NT) void attn_bwd_kv(AttnArgs a)
 template <class IO, int DP, bool CAP, bool BIAS>
 hipError_t go(const AttnArgs& a, hipStream_t st)
 {
-    const int64_t qb = (int64_t)a.ntile * a.nbh, kb = (int64_t)((a.Lk + BK - 1) / BK) * a.nbh;
+    constexpr int BK = 64 * key_blocks<IO, DP>;
+    const int64_t qb = (int64_t)a.ntile * a.B * a.H, kb = (int64_t)((a.Lk + BK - 1) / BK) * a.nbh;
     if (!grid_ok(qb, NT) || !grid_ok(kb, NT)) return hipErrorInvalidValue;
     if (qb > 0) {
         hipLaunchKernelGGL((attn_bwd_q<IO, DP, CAP, BIAS>), dim3((unsigned)qb), dim3(NT), 0, st, a);
@@ -474,19 +505,19 @@ hipError_t pick(const AttnArgs& a, hipStream_t st)
     return a.slopes ? go<IO, DP, false, true>(a, st) : go<IO, DP, false, false>(a, st);
 }
 
-size_t stat_bytes(const AttnArgs& a) { return ((size_t)a.nbh * a.nrow * sizeof(float2) + 255) / 256 * 256; }
+size_t stat_bytes(const AttnArgs& a) { return ((size_t)a.B * a.H * a.Lq * sizeof(float2) + 255) / 256 * 256; }
 
 }  // namespace
 
 size_t attn_bwd_bytes(const AttnArgs& a)
 {
-    return stat_bytes(a) + (size_t)a.B * ((a.nrow + BM - 1) / BM) * 4 * sizeof(int4);
+    return stat_bytes(a) + (a.doc ? (size_t)a.B * ((a.Lq + BM - 1) / BM) * 4 * sizeof(int4) : 0);
 }
 
 hipError_t launch_attn_bwd(Store s, const AttnArgs& a, void* ws, hipStream_t st)
 {
     AttnArgs x = a;
-    x.ntile = (a.nrow + BM - 1) / BM;
+    x.ntile = (a.Lq + BM - 1) / BM;
     x.rowstat = (float2*)ws;
     x.strips = (int4*)((char*)ws + stat_bytes(a));
     if (s == Store::F32) return a.D <= 64 ? pick<f32_io, 64>(x, st) : pick<f32_io, 128>(x, st);
