@@ -61,12 +61,7 @@ __device__ __forceinline__ f32x4 mma(const Frag<f32_io>& a, const Frag<f32_io>& 
     return __builtin_amdgcn_mfma_f32_16x16x4f32(a.b.w, b.b.w, c, 0, 0, 0);
 }
 
-// LDS tile row pitch in elements for rows of DP: 16 bytes of padding, so that 16 lanes reading
-// 16 bytes each of 16 rows touch every bank once.
-template <class IO, int DP>
-constexpr int pitch = DP + 16 / IO::SIZE;
-
-// Row r of a tile (or of memory), elements at p[0..7] (16-byte aligned).
+// Eight elements of a row in memory (16-byte aligned).
 template <class IO>
 __device__ __forceinline__ Frag<IO> frag_at(const typename IO::T* p)
 {
@@ -89,26 +84,85 @@ __device__ __forceinline__ Frag<IO> frag_zero()
     return f;
 }
 
+// LDS tiles hold rows of DP elements without padding (asynchronous loads write 1024 contiguous
+// bytes a wave); the 16-byte chunk k of row r sits at chunk k ^ (r & 7), so that the rows that
+// lanes read together lie in different banks.
+
+// A operand: row r0 + c, elements 32 k + 8 g .. + 7.  r0 a multiple of 8.
+template <class IO, int DP>
+__device__ __forceinline__ Frag<IO> frag_row(const typename IO::T* tile, int r0, int k, int g, int c)
+{
+    const typename IO::T* row = tile + (r0 + c) * DP;
+    Frag<IO> f;
+    if constexpr (IO::SIZE == 2) {
+        f.v = *(const uint4*)(row + ((4 * k + g) ^ (c & 7)) * 8);
+    } else {
+        f.a = *(const float4*)(row + ((8 * k + 2 * g) ^ (c & 7)) * 4);
+        f.b = *(const float4*)(row + ((8 * k + 2 * g + 1) ^ (c & 7)) * 4);
+    }
+    return f;
+}
+
 // A operand read transposed: column d0 + c of the tile, rows r0 + 4 g + e and r0 + 16 + 4 g + e.
-template <class IO, int P>
+// r0 a multiple of 32, d0 of 16.
+template <class IO, int DP>
 __device__ __forceinline__ Frag<IO> frag_tr(const typename IO::T* tile, int r0, int d0, int g, int c)
 {
     Frag<IO> f;
     if constexpr (IO::SIZE == 2) {
         // lane c of a 16-lane group addresses row c / 4, columns 4 (c % 4) .. + 3, and receives
         // column c of the group's four rows
-        const uint16_t* p = tile + (r0 + 4 * g + (c >> 2)) * P + d0 + 4 * (c & 3);
+        const int r = 4 * g + (c >> 2), k = (d0 / 8 + ((c & 3) >> 1)) ^ (r & 7);
+        const uint16_t* p = tile + (r0 + r) * DP + 8 * k + 4 * (c & 1);
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 16 * P));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 16 * DP));
         const uint2 l = __builtin_bit_cast(uint2, lo), h = __builtin_bit_cast(uint2, hi);
         f.v = make_uint4(l.x, l.y, h.x, h.y);
     } else {
-        const float* p = tile + (r0 + 4 * g) * P + d0 + c;
-        f.a = make_float4(p[0], p[P], p[2 * P], p[3 * P]);
-        p += 16 * P;
-        f.b = make_float4(p[0], p[P], p[2 * P], p[3 * P]);
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = 4 * g + e, k = (d0 / 4 + (c >> 2)) ^ (r & 7);
+            const float* p = tile + (r0 + r) * DP + 4 * k + (c & 3);
+            x[e] = p[0];
+            x[4 + e] = p[16 * DP];
+        }
+        f.a = make_float4(x[0], x[1], x[2], x[3]);
+        f.b = make_float4(x[4], x[5], x[6], x[7]);
     }
     return f;
+}
+
+// ---- asynchronous loads from memory into LDS: every lane's 16 (or 4) bytes go to consecutive
+// places from `lds` on (a wave-uniform byte offset under 64 KB).  No register receives them; a
+// wave waits for its own with wait_loads, and a barrier then covers the others'.
+__device__ __forceinline__ uint32_t lds_offset(const void* p)
+{
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"   // m0 is reserved: nothing else here uses it
+__device__ __forceinline__ void load_lds16(const void* p, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory", "m0");
+}
+__device__ __forceinline__ void load_lds4(const void* p, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(p) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+// waits until at most N of the wave's loads are in flight; they end in the order of their issue
+template <int N>
+__device__ __forceinline__ void wait_loads()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// all of the workgroup's LDS reads are done and the asynchronous loads waited for are visible
+__device__ __forceinline__ void stage_barrier()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 // B operand from two result blocks (the halves of a 32-row strip), rounded to the storage type:
@@ -257,71 +311,111 @@ __device__ __forceinline__ RowRange lanes_range(const int (&lo)[NR], const int (
     return {wave_min(x.lo), wave_max(x.hi), wave_max(x.last), wave_min(x.pos)};
 }
 
-// The key tiles a workgroup walks: 64 keys of k and v, fetched into registers one tile ahead and
-// put into LDS rows of pitch<IO, DP>.  Keys past the sequence and padding read as 0, whatever the
-// memory holds.
+// Rows of one stage (keys, or tokens of a head), and how many stages a workgroup's LDS holds:
+// three (48 KB), two in flight while one is used; float32 heads of 128 leave room for one, whose
+// loads are not hidden.  All under 64 KB, the reach of an asynchronous load's LDS offset.
 template <class IO, int DP>
-struct KeyTiles {
-    using E = typename IO::T;
-    static constexpr int BN = 64, V = 16 / IO::SIZE, CH = DP / V, NCH = BN * CH / NT, P = pitch<IO, DP>;
-    const AttnArgs& a;
-    const int32_t* doc;
-    const E *kp, *vp;
-    int n, r0, d0, lane;   // this thread's pieces: rows r0 + NT / CH i, columns d0 .. d0 + V - 1
-    bool din;
-    uint4 rk[NCH], rv[NCH];
-    int rdoc = 0;
+constexpr int stage_rows = IO::SIZE == 2 && DP == 64 ? 64 : 32;
+template <class IO, int DP>
+constexpr int stages = IO::SIZE == 4 && DP == 128 ? 1 : 3;
 
-    __device__ __forceinline__ KeyTiles(const AttnArgs& args, int b, int hk, int len, int tid)
-        : a(args), doc(args.doc ? args.doc + (int64_t)b * args.Lk : nullptr), n(len), r0(tid / CH),
-          d0(tid % CH * V), lane(tid & 63), din(d0 < args.D)
+// A ring of stages, each BN rows of two tensors x and y (k and v, or q and dout) and up to three
+// 32-bit values a row.  issue(s, t) starts stage s's loads into place t; rows past the last are
+// read from the last.  ready() waits until they are in LDS for the whole workgroup; after it the
+// place used before is free.
+template <class IO, int DP>
+struct Ring {
+    using E = typename IO::T;
+    static constexpr int BN = stage_rows<IO, DP>, NS = stages<IO, DP>, V = 16 / IO::SIZE, CH = DP / V;
+    static constexpr int NCH = BN * CH / NT, TILE = BN * DP;   // loads a thread and tensor; elements
+    struct Shared {
+        E x[NS][TILE], y[NS][TILE];
+        uint32_t w[3][NS][64];   // a wave writes 64 of them, whatever BN
+    };
+    static_assert(sizeof(Shared) <= 64 * 1024, "the reach of an asynchronous load");
+    Shared& sh;
+    const E *xp, *yp;
+    const uint32_t* wp[3];   // null: not wanted
+    int64_t xs, ys;          // row strides
+    int rows, vfirst = 0;    // vfirst: the first row that has values
+    int r0, lane, wave;
+
+    __device__ __forceinline__ Ring(Shared& s, int n, int D, int64_t xs_, int64_t ys_)
+        : sh(s), wp{nullptr, nullptr, nullptr}, xs(xs_), ys(ys_), rows(n), r0(threadIdx.x / CH),
+          lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), D_(D)
     {
-        kp = (const E*)a.k + b * a.ks[0] + hk * a.ks[2] + (din ? d0 : 0);
-        vp = (const E*)a.v + b * a.vs[0] + hk * a.vs[2] + (din ? d0 : 0);
     }
-    // only where some row sees a key, so n > 0; nothing here waits for a load
-    __device__ __forceinline__ void fetch(int j0)
+    __device__ __forceinline__ void from(const E* x, const E* y)
     {
-        if (j0 + BN <= n) {
-            const E *k = kp + (int64_t)(j0 + r0) * a.ks[1], *v = vp + (int64_t)(j0 + r0) * a.vs[1];
+        // this thread's chunk of a row; columns past D take the row's first (they meet zeros of the
+        // other operand, or results that are not stored)
+        const int d = (((int)threadIdx.x % CH) ^ (r0 & 7)) * V;
+        xp = x + (d < D_ ? d : 0);
+        yp = y + (d < D_ ? d : 0);
+    }
+    __device__ __forceinline__ void issue(int s, int t) const
+    {
+        const int b = s * BN + r0;
+        const uint32_t lx = lds_offset(sh.x[t]) + wave * 1024, ly = lds_offset(sh.y[t]) + wave * 1024;
 #pragma unroll
-            for (int i = 0; i < NCH; ++i) {
-                rk[i] = *(const uint4*)(k + (int64_t)(NT / CH * i) * a.ks[1]);
-                rv[i] = *(const uint4*)(v + (int64_t)(NT / CH * i) * a.vs[1]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < NCH; ++i) {
-                const int64_t j = min(j0 + r0 + NT / CH * i, n - 1);
-                rk[i] = *(const uint4*)(kp + j * a.ks[1]);
-                rv[i] = *(const uint4*)(vp + j * a.vs[1]);
-            }
+        for (int i = 0; i < NCH; ++i) {
+            const int64_t r = min(b + NT / CH * i, rows - 1);
+            load_lds16(xp + r * xs, __builtin_amdgcn_readfirstlane(lx + i * 4096));
+            load_lds16(yp + r * ys, __builtin_amdgcn_readfirstlane(ly + i * 4096));
         }
-        if (doc) rdoc = doc[min(j0 + lane, n - 1)];
+        // every wave brings the whole row of values (the same bytes to the same place)
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            if (wp[k]) load_lds4(wp[k] + max(min(s * BN + lane % BN, rows - 1), vfirst),
+                                 __builtin_amdgcn_readfirstlane(lds_offset(sh.w[k][t])));
     }
-    // returns which keys of the tile exist and are not padding, bit j - j0
-    __device__ __forceinline__ uint64_t put(E* kt, E* vt, int j0)
+    // `more`: the next stage's loads are in flight too and may stay so
+    __device__ __forceinline__ void ready(bool more) const
     {
-        const uint64_t live = __ballot(j0 + lane < n && (!doc || rdoc <= j0 + lane));
-        if (live == ~0ull && DP == a.D) {
-#pragma unroll
-            for (int i = 0; i < NCH; ++i) {
-                const int at = (r0 + NT / CH * i) * P + d0;
-                *(uint4*)(kt + at) = rk[i];
-                *(uint4*)(vt + at) = rv[i];
-            }
+        if (!more) {
+            wait_loads<0>();
         } else {
-#pragma unroll
-            for (int i = 0; i < NCH; ++i) {
-                const int r = r0 + NT / CH * i, at = r * P + d0;
-                const bool on = din && live >> r & 1;
-                *(uint4*)(kt + at) = on ? rk[i] : make_uint4(0, 0, 0, 0);
-                *(uint4*)(vt + at) = on ? rv[i] : make_uint4(0, 0, 0, 0);
-            }
+            // values wanted: so many more loads a stage
+            const int extra = (wp[0] != nullptr) + (wp[1] != nullptr) + (wp[2] != nullptr);
+            if (extra == 0) wait_loads<2 * NCH>();
+            else if (extra == 1) wait_loads<2 * NCH + 1>();
+            else if (extra == 2) wait_loads<2 * NCH + 2>();
+            else wait_loads<2 * NCH + 3>();
         }
-        // keys past the sequence lie past every position: no mask of their own
-        return doc ? live : ~0ull;
+        stage_barrier();
     }
+    // place t's successor, and the place that ready() has freed
+    __device__ __forceinline__ static int after(int t) { return t + 1 == NS ? 0 : t + 1; }
+    __device__ __forceinline__ static int freed(int t) { return t ? t - 1 : NS - 1; }
+    // a walk over stages first .. end - 1: start(first, end), then step() at each
+    __device__ __forceinline__ void start(int first, int end) const
+    {
+        for (int s = first; s < min(end, first + NS - 1); ++s) issue(s, s - first);
+    }
+    __device__ __forceinline__ void step(int s, int end, int place) const
+    {
+        if constexpr (NS == 1) {
+            __syncthreads();
+            issue(s, 0);
+            ready(false);
+        } else {
+            ready(s + 1 < end);
+            if (s + NS - 1 < end) issue(s + NS - 1, freed(place));
+        }
+    }
+    // rows whose bit of `live` is clear become 0 in x and y of place t, whatever memory held
+    __device__ __forceinline__ void blank(int t, uint64_t live) const
+    {
+        for (int q = threadIdx.x; q < BN * CH; q += NT)
+            if (!(live >> (q / CH) & 1)) {
+                *(uint4*)(sh.x[t] + q * V) = make_uint4(0, 0, 0, 0);
+                *(uint4*)(sh.y[t] + q * V) = make_uint4(0, 0, 0, 0);
+            }
+        __syncthreads();
+    }
+
+  private:
+    int D_;
 };
 
 // four consecutive results of a row

@@ -31,7 +31,6 @@ namespace {
 
 using namespace attn;
 
-constexpr int BN = 64;            // keys of a tile
 constexpr int NQ = 2;             // 16-row blocks of a wave
 constexpr int WM = 16 * NQ;       // rows of a wave
 constexpr int BM = 4 * WM;        // rows of a workgroup
@@ -44,10 +43,9 @@ template <class IO, int DP, bool CAP, bool BIAS>
 __global__ __launch_bounds__(NT, FWV(DP, IO::SIZE)) void attn_fwd(AttnArgs a)
 {
     using E = typename IO::T;
-    constexpr int P = pitch<IO, DP>;
-    constexpr int KK = DP / 32, ND = DP / 16;
-    __shared__ __attribute__((aligned(16))) E Kt[BN * P];
-    __shared__ __attribute__((aligned(16))) E Vt[BN * P];
+    using R = Ring<IO, DP>;
+    constexpr int KK = DP / 32, ND = DP / 16, BN = R::BN, KB = BN / 16;   // 16-key blocks of a tile
+    __shared__ __attribute__((aligned(1024))) typename R::Shared sh;
     __shared__ int range[2][4];
 
     uint32_t id = blockIdx.x;
@@ -124,31 +122,39 @@ __global__ __launch_bounds__(NT, FWV(DP, IO::SIZE)) void attn_fwd(AttnArgs a)
         for (int d = 0; d < ND; ++d) o[d][m] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    KeyTiles<IO, DP> tiles(a, b, hk, n, tid);
-    if (t0 < t1) tiles.fetch(t0 * BN);
-    for (int t = t0; t < t1; ++t) {
+    R ring(sh, n, a.D, a.ks[1], a.vs[1]);
+    ring.from((const E*)a.k + b * a.ks[0] + hk * a.ks[2], (const E*)a.v + b * a.vs[0] + hk * a.vs[2]);
+    if (a.doc) ring.wp[0] = (const uint32_t*)a.doc + (int64_t)b * a.Lk;
+    ring.start(t0, t1);
+    int place = 0;
+    for (int t = t0; t < t1; ++t, place = R::after(place)) {
         const int j0 = t * BN;
-        __syncthreads();
-        const uint64_t live = tiles.put(Kt, Vt, j0);
-        __syncthreads();
-        if (t + 1 < t1) tiles.fetch(j0 + BN);
+        ring.step(t, t1, place);
+        const E *Kt = sh.x[place], *Vt = sh.y[place];
+        uint64_t live = ~0ull;   // keys that are not padding, bit j - j0
+        if (a.doc || j0 + BN > n) {
+            const int j = j0 + lane % BN;
+            live = __ballot(j < n && (!a.doc || (int)sh.w[0][place][lane % BN] <= j));
+            if (BN < 64) live |= ~0ull << (BN & 63);
+            if (live != ~0ull) ring.blank(place, live);
+        }
         if (j0 > rr.hi || j0 + BN - 1 < rr.lo) continue;   // no row of this wave sees it
 
         // scores, keys x rows
-        f32x4 s[4][NQ];
+        f32x4 s[KB][NQ];
 #pragma unroll
-        for (int kb = 0; kb < 4; ++kb) {
+        for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
             for (int m = 0; m < NQ; ++m) s[kb][m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < KK; ++k) {
-                const Frag<IO> f = frag_at<IO>(Kt + (16 * kb + c) * P + 32 * k + 8 * g);
+                const Frag<IO> f = frag_row<IO, DP>(Kt, 16 * kb, k, g, c);
 #pragma unroll
                 for (int m = 0; m < NQ; ++m) s[kb][m] = mma(f, q[m][k], s[kb][m]);
             }
         }
         const bool edge = j0 < rr.last || j0 + BN - 1 > rr.pos;
-        Frag<IO> w[2][NQ];
+        Frag<IO> w[KB / 2][NQ];
 #pragma unroll
         for (int m = 0; m < NQ; ++m) {
             // scores in base 2, less the row's base: the running maximum as it was when a score
@@ -158,7 +164,7 @@ __global__ __launch_bounds__(NT, FWV(DP, IO::SIZE)) void attn_fwd(AttnArgs a)
             const float base = mx[m] == -INFINITY ? 0.f : mx[m];
             const float shift = BIAS ? slope[m] * (float)(j0 + 4 * g - pos[m]) - base : -base;
 #pragma unroll
-            for (int kb = 0; kb < 4; ++kb)
+            for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float add = BIAS ? __builtin_fmaf(slope[m], (float)(16 * kb + r), shift) : shift;
@@ -170,7 +176,7 @@ __global__ __launch_bounds__(NT, FWV(DP, IO::SIZE)) void attn_fwd(AttnArgs a)
                 const int first = lo[m] - j0 - 4 * g;
                 const uint32_t span = (uint32_t)(pos[m] - lo[m]);   // keys the row sees, less 1
 #pragma unroll
-                for (int kb = 0; kb < 4; ++kb)
+                for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         if ((uint32_t)(16 * kb + r - first) > span) s[kb][m][r] = -INFINITY;
@@ -179,14 +185,14 @@ __global__ __launch_bounds__(NT, FWV(DP, IO::SIZE)) void attn_fwd(AttnArgs a)
                 keep_branch();
                 const uint64_t mine = live >> (4 * g);
 #pragma unroll
-                for (int kb = 0; kb < 4; ++kb)
+                for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         if (!(mine >> (16 * kb + r) & 1)) s[kb][m][r] = -INFINITY;
             }
             float top = s[0][m][0];
 #pragma unroll
-            for (int kb = 0; kb < 4; ++kb)
+            for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) top = fmaxf(top, s[kb][m][r]);
             if (__any(top > (mx[m] == -INFINITY ? -INFINITY : SLACK))) {
@@ -198,28 +204,28 @@ __global__ __launch_bounds__(NT, FWV(DP, IO::SIZE)) void attn_fwd(AttnArgs a)
                     for (int d = 0; d < ND; ++d) o[d][m] *= f;
                     mx[m] = now;
 #pragma unroll
-                    for (int kb = 0; kb < 4; ++kb)
+                    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                         for (int r = 0; r < 4; ++r) s[kb][m][r] -= top;
                 }
             }
 #pragma unroll
-            for (int kb = 0; kb < 4; ++kb)
+            for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float e = exp2_hw(s[kb][m][r]);
                     s[kb][m][r] = e;
                     sum[m] += e;
                 }
-            w[0][m] = frag_of<IO>(s[0][m], s[1][m]);
-            w[1][m] = frag_of<IO>(s[2][m], s[3][m]);
+#pragma unroll
+            for (int hf = 0; hf < KB / 2; ++hf) w[hf][m] = frag_of<IO>(s[2 * hf][m], s[2 * hf + 1][m]);
         }
         // o^T += v^T w
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const Frag<IO> f = frag_tr<IO, P>(Vt, 32 * hf, 16 * d, g, c);
+            for (int hf = 0; hf < KB / 2; ++hf) {
+                const Frag<IO> f = frag_tr<IO, DP>(Vt, 32 * hf, 16 * d, g, c);
 #pragma unroll
                 for (int m = 0; m < NQ; ++m) o[d][m] = mma(f, w[hf][m], o[d][m]);
             }
@@ -441,16 +447,15 @@ __global__ __launch_bounds__(NT) void attn_few(AttnArgs a)
     }
 }
 
-// Joins the splits of a row: o = sum_s 2^(lse_s - lse) o_s.  One wave per row: lane s weighs
-// split s (at most 64), then the lanes hold the columns.
+// Joins the splits of a row: o = sum_s 2^(lse_s - lse) o_s.  One workgroup per row: lane s weighs
+// split s (at most 64), then each wave sums a quarter of the splits for 64 columns at a time.
 template <class IO>
 __global__ __launch_bounds__(NT) void attn_join(AttnArgs a)
 {
     using E = typename IO::T;
-    const int64_t total = (int64_t)a.nbh * a.nrow;
-    const int64_t at = (int64_t)blockIdx.x * (NT / 64) + (threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63;
-    if (at >= total) return;
+    __shared__ float weight[64], sum4[4][64];
+    const int64_t total = (int64_t)a.nbh * a.nrow, at = blockIdx.x;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const float ls = lane < a.nsplit ? a.part_lse[lane * total + at] : -INFINITY;
     float mx = ls;
 #pragma unroll
@@ -459,19 +464,22 @@ __global__ __launch_bounds__(NT) void attn_join(AttnArgs a)
     float sum = e;
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
-    const float w = sum > 0.f ? e / sum : 0.f;
+    if (wave == 0) weight[lane] = sum > 0.f ? e / sum : 0.f;
     const int bh = (int)(at / a.nrow), r = (int)(at % a.nrow);
     const int b = bh / a.Hkv, i = r / a.G, h = bh % a.Hkv * a.G + r % a.G;
     E* op = (E*)a.o + b * a.os[0] + (int64_t)i * a.os[1] + h * a.os[2];
-    for (int d = lane; d < (a.D + 63) / 64 * 64; d += 64) {
-        const float* p = a.part + at * a.D + min(d, a.D - 1);
+    for (int d0 = 0; d0 < a.D; d0 += 64) {
+        __syncthreads();
+        const float* p = a.part + at * a.D + min(d0 + lane, a.D - 1);
         float x = 0.f;
-#pragma unroll 8
-        for (int s = 0; s < a.nsplit; ++s)
-            x = __builtin_fmaf(__shfl(w, s), p[s * total * a.D], x);
-        if (d < a.D) IO::store(op, d, x);
+#pragma unroll 4
+        for (int s = wave; s < a.nsplit; s += 4) x = __builtin_fmaf(weight[s], p[s * total * a.D], x);
+        sum4[wave][lane] = x;
+        __syncthreads();
+        if (wave == 0 && d0 + lane < a.D)
+            IO::store(op, d0 + lane, (sum4[0][lane] + sum4[1][lane]) + (sum4[2][lane] + sum4[3][lane]));
     }
-    if (a.lse && lane == 0)
+    if (a.lse && threadIdx.x == 0)
         a.lse[((int64_t)b * a.H + h) * a.Lq + i] = sum > 0.f ? (mx + __builtin_amdgcn_logf(sum)) * LN2 : -INFINITY;
 }
 
@@ -542,8 +550,9 @@ hipError_t run(AttnArgs a, hipStream_t st)
     if (is_few) e = a.D <= 64 ? few_rows<IO, LPK>(a, blocks, st) : few_rows<IO, 2 * LPK>(a, blocks, st);
     else e = a.D <= 64 ? pick<IO, 64>(a, blocks, st) : pick<IO, 128>(a, blocks, st);
     if (e != hipSuccess || a.nsplit == 1) return e;
-    const int64_t jb = ((int64_t)a.nbh * a.nrow + NT / 64 - 1) / (NT / 64);
-    hipLaunchKernelGGL((attn_join<IO>), dim3((unsigned)jb), dim3(NT), 0, st, a);
+    const int64_t rows = (int64_t)a.nbh * a.nrow;
+    if (!grid_ok(rows, NT)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((attn_join<IO>), dim3((unsigned)rows), dim3(NT), 0, st, a);
     return hipGetLastError();
 }
 

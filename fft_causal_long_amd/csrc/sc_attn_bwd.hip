@@ -30,7 +30,6 @@ namespace {
 
 using namespace attn;
 
-constexpr int BN = 64;        // keys of a tile (attn_bwd_q), tokens of a stage (attn_bwd_kv)
 constexpr int NQ = 2;         // 16-row blocks of a wave
 constexpr int WM = 16 * NQ;   // tokens of a wave and of a strip
 constexpr int BM = 4 * WM;    // tokens of a workgroup
@@ -63,9 +62,9 @@ template <class IO, int DP, bool CAP, bool BIAS>
 __global__ __launch_bounds__(NT, BQV(DP, IO::SIZE)) void attn_bwd_q(AttnArgs a)
 {
     using E = typename IO::T;
-    constexpr int P = pitch<IO, DP>, V = vec_elems<IO>, KK = DP / 32, ND = DP / 16;
-    __shared__ __attribute__((aligned(16))) E Kt[BN * P];
-    __shared__ __attribute__((aligned(16))) E Vt[BN * P];
+    using R = Ring<IO, DP>;
+    constexpr int V = vec_elems<IO>, KK = DP / 32, ND = DP / 16, BN = R::BN;
+    __shared__ __attribute__((aligned(1024))) typename R::Shared sh;
     __shared__ int range[2][4];
 
     const int nbh = a.B * a.H;
@@ -119,7 +118,11 @@ __global__ __launch_bounds__(NT, BQV(DP, IO::SIZE)) void attn_bwd_q(AttnArgs a)
             }
         }
         delta[m] = gsum(dl);
-        if (g == 0 && in) a.rowstat[(int64_t)bh * a.Lq + i] = make_float2(lse2[m], delta[m]);
+        if (g == 0 && in) {
+            const int64_t at = (int64_t)bh * a.Lq + i;
+            a.rowstat[at] = lse2[m];
+            a.rowstat[(int64_t)nbh * a.Lq + at] = delta[m];
+        }
     }
     const RowRange rr = a.doc ? lanes_range(lo, pos) : token_range(a, n, rw, WM);
     int klo, khi;
@@ -155,19 +158,27 @@ __global__ __launch_bounds__(NT, BQV(DP, IO::SIZE)) void attn_bwd_q(AttnArgs a)
 #pragma unroll
         for (int m = 0; m < NQ; ++m) acc[d][m] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    KeyTiles<IO, DP> tiles(a, b, hk, n, tid);
-    if (t0 < t1) tiles.fetch(t0 * BN);
-    for (int t = t0; t < t1; ++t) {
+    R ring(sh, n, a.D, a.ks[1], a.vs[1]);
+    ring.from((const E*)a.k + b * a.ks[0] + hk * a.ks[2], (const E*)a.v + b * a.vs[0] + hk * a.vs[2]);
+    if (a.doc) ring.wp[0] = (const uint32_t*)a.doc + (int64_t)b * a.Lk;
+    ring.start(t0, t1);
+    int place = 0;
+    for (int t = t0; t < t1; ++t, place = R::after(place)) {
         const int j0 = t * BN;
-        __syncthreads();
-        const uint64_t live = tiles.put(Kt, Vt, j0);
-        __syncthreads();
-        if (t + 1 < t1) tiles.fetch(j0 + BN);
+        ring.step(t, t1, place);
+        const E *Kt = sh.x[place], *Vt = sh.y[place];
+        uint64_t live = ~0ull;   // keys that are not padding, bit j - j0
+        if (a.doc || j0 + BN > n) {
+            const int j = j0 + lane % BN;
+            live = __ballot(j < n && (!a.doc || (int)sh.w[0][place][lane % BN] <= j));
+            if (BN < 64) live |= ~0ull << (BN & 63);
+            if (live != ~0ull) ring.blank(place, live);
+        }
         if (j0 > rr.hi || j0 + BN - 1 < rr.lo) continue;
 
         const bool edge = j0 < rr.last || j0 + BN - 1 > rr.pos || live != ~0ull;
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {   // 32 keys at a time
+        for (int hf = 0; hf < BN / 32; ++hf) {   // 32 keys at a time
             f32x4 s[2][NQ], dp[2][NQ];
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) {
@@ -175,8 +186,8 @@ __global__ __launch_bounds__(NT, BQV(DP, IO::SIZE)) void attn_bwd_q(AttnArgs a)
                 for (int m = 0; m < NQ; ++m) s[kb][m] = dp[kb][m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int k = 0; k < KK; ++k) {
-                    const int at = (32 * hf + 16 * kb + c) * P + 32 * k + 8 * g;
-                    const Frag<IO> fk = frag_at<IO>(Kt + at), fv = frag_at<IO>(Vt + at);
+                    const Frag<IO> fk = frag_row<IO, DP>(Kt, 32 * hf + 16 * kb, k, g, c);
+                    const Frag<IO> fv = frag_row<IO, DP>(Vt, 32 * hf + 16 * kb, k, g, c);
 #pragma unroll
                     for (int m = 0; m < NQ; ++m) {
                         s[kb][m] = mma(fk, q[m][k], s[kb][m]);
@@ -222,7 +233,7 @@ __global__ __launch_bounds__(NT, BQV(DP, IO::SIZE)) void attn_bwd_q(AttnArgs a)
             }
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
-                const Frag<IO> f = frag_tr<IO, P>(Kt, 32 * hf, 16 * d, g, c);
+                const Frag<IO> f = frag_tr<IO, DP>(Kt, 32 * hf, 16 * d, g, c);
 #pragma unroll
                 for (int m = 0; m < NQ; ++m) acc[d][m] = mma(f, w[m], acc[d][m]);
             }
@@ -245,12 +256,10 @@ template <class IO, int DP, bool CAP, bool BIAS>
 __global__ __launch_bounds__(NT, BKV(DP, IO::SIZE)) void attn_bwd_kv(AttnArgs a)
 {
     using E = typename IO::T;
-    constexpr int P = pitch<IO, DP>, V = vec_elems<IO>, CH = DP / V, NCH = BN * CH / NT;
+    using R = Ring<IO, DP>;
     constexpr int KK = DP / 32, ND = DP / 16, NK = key_blocks<IO, DP>, WK = 16 * NK, BK = 4 * WK;
-    __shared__ __attribute__((aligned(16))) E Qt[BN * P];
-    __shared__ __attribute__((aligned(16))) E Gt[BN * P];
-    __shared__ __attribute__((aligned(16))) float Rt[BN], Dl[BN];
-    __shared__ __attribute__((aligned(16))) int Lo[BN];
+    constexpr int BN = R::BN, SP = BN / WM;   // tokens and strips of a stage
+    __shared__ __attribute__((aligned(1024))) typename R::Shared sh;
 
     uint32_t id = blockIdx.x;
     const int bh = (int)(id % (uint32_t)a.nbh);
@@ -300,105 +309,100 @@ __global__ __launch_bounds__(NT, BKV(DP, IO::SIZE)) void attn_bwd_kv(AttnArgs a)
         }
     }
     const int4* strips = a.strips + (int64_t)b * a.ntile * 4;
-    // the next stage at or after s whose tokens see this workgroup's keys, 64 looked at together
+    // With documents: which of 64 stages from sbase on see this workgroup's keys, and which of their
+    // strips this wave's (hit) and every key of them (full), read together so that the walk itself
+    // waits for no load of its own.
+    int sbase = 0, sfilled = -1;
+    uint64_t stage_hit = 0, hit[SP], full[SP];
+    auto look = [&](int s) {
+        sbase = s;
+        sfilled = 1;
+        bool any = false;
+#pragma unroll
+        for (int x = 0; x < SP; ++x) {
+            bool h = false, f = false;
+            if (s + lane < s1) {
+                const int4 r = strips[SP * (s + lane) + x];
+                any |= r.x <= jb + BK - 1 && r.y >= jb;
+                h = r.x <= jw + WK - 1 && r.y >= jw;
+                f = r.z <= jw && r.w >= jw + WK - 1;
+            }
+            hit[x] = __ballot(h);
+            full[x] = __ballot(f);
+        }
+        stage_hit = __ballot(any);
+    };
+    // the next stage at or after s that sees this workgroup's keys
     auto seek = [&](int s) {
         if (!a.doc) return s;
         while (s < s1) {
-            bool hit = false;
-            if (s + lane < s1) {
-                const int4 x = strips[2 * (s + lane)], y = strips[2 * (s + lane) + 1];
-                hit = min(x.x, y.x) <= jb + BK - 1 && max(x.y, y.y) >= jb;
-            }
-            const uint64_t m = __ballot(hit);
-            if (m) return __builtin_amdgcn_readfirstlane(s + (int)__builtin_ctzll(m));
-            s += 64;
+            if (sfilled < 0 || s < sbase || s >= sbase + 64) look(s);
+            const uint64_t m = stage_hit >> (s - sbase);
+            if (m) return s + (int)__builtin_ctzll(m);
+            s = sbase + 64;
         }
         return s1;
     };
 
-    const int r0 = tid / CH, d0 = tid % CH * V;
-    const bool din = d0 < a.D;
     const int32_t* doc = a.doc ? a.doc + (int64_t)b * a.Lk : nullptr;
+    R ring(sh, a.Lq, a.D, a.qs[1], a.dos[1]);
     for (int h = hk * a.G; h < (hk + 1) * a.G; ++h) {
-        const E* qp = (const E*)a.q + b * a.qs[0] + h * a.qs[2] + (din ? d0 : 0);
-        const E* gp = (const E*)a.dout + b * a.dos[0] + h * a.dos[2] + (din ? d0 : 0);
-        const float2* stat = a.rowstat + ((int64_t)b * a.H + h) * a.Lq;
+        ring.from((const E*)a.q + b * a.qs[0] + h * a.qs[2], (const E*)a.dout + b * a.dos[0] + h * a.dos[2]);
+        const float* stat = a.rowstat + ((int64_t)b * a.H + h) * a.Lq;
+        ring.wp[0] = (const uint32_t*)stat;
+        ring.wp[1] = (const uint32_t*)(stat + (int64_t)a.B * a.H * a.Lq);
         const float slope = BIAS ? a.slopes[h] * LOG2E : 0.f;
-        uint4 rq[NCH], rg[NCH];
-        float2 rs = make_float2(INFINITY, 0.f);
-        int rdoc = 0;
-        // nothing here waits for a load
-        auto fetch = [&](int s) {
-            const int tb = s * BN;
-            if (tb + BN <= a.Lq) {
-                const E *q = qp + (int64_t)(tb + r0) * a.qs[1], *g_ = gp + (int64_t)(tb + r0) * a.dos[1];
-#pragma unroll
-                for (int i = 0; i < NCH; ++i) {
-                    rq[i] = *(const uint4*)(q + (int64_t)(NT / CH * i) * a.qs[1]);
-                    rg[i] = *(const uint4*)(g_ + (int64_t)(NT / CH * i) * a.dos[1]);
-                }
+        __syncthreads();   // the places the last head used are free
+        if (doc) {
+            ring.wp[2] = (const uint32_t*)(doc + off);   // the rows' own documents
+            ring.vfirst = max(0, -off);
+        }
+        // q0: the stage to use, q1 the one after, whose loads are in flight (NS = 3)
+        int q0 = seek(s0), q1 = q0 < s1 ? seek(q0 + 1) : s1;
+        if (R::NS > 1 && q0 < s1) ring.issue(q0, 0);
+        if (R::NS > 1 && q1 < s1) ring.issue(q1, 1);
+        int place = 0;
+        for (; q0 < s1; place = R::after(place)) {
+            const int tb = q0 * BN, pb = off + tb, here = q0;
+            if constexpr (R::NS == 1) {
+                __syncthreads();
+                ring.issue(q0, 0);
+                ring.ready(false);
             } else {
-#pragma unroll
-                for (int i = 0; i < NCH; ++i) {
-                    const int64_t t = min(tb + r0 + NT / CH * i, a.Lq - 1);
-                    rq[i] = *(const uint4*)(qp + t * a.qs[1]);
-                    rg[i] = *(const uint4*)(gp + t * a.dos[1]);
-                }
+                ring.ready(q1 < s1);
             }
-            const int t = min(tb + lane, a.Lq - 1);   // each wave: lane's row of the stage
-            rs = stat[t];
-            if (doc) rdoc = doc[min(max(off + t, 0), n - 1)];
-        };
-        int s = seek(s0);
-        if (s < s1) fetch(s);
-        while (s < s1) {
-            __syncthreads();
-            {
-                const int tb = s * BN, p = off + tb + lane;
-                int first = max(max(0, p - a.window + 1), doc ? rdoc : 0);
-                if (tb + lane >= a.Lq || p < 0 || first > p) first = BIG;
-                // empty rows read as 0, whatever the memory holds
-                const uint64_t alive = __ballot(first != BIG);
-                if (alive == ~0ull && DP == a.D) {
+            // what look() said of this stage, before it may look further
+            bool whit[SP], wfull[SP];
 #pragma unroll
-                    for (int i = 0; i < NCH; ++i) {
-                        const int at = (r0 + NT / CH * i) * P + d0;
-                        *(uint4*)(Qt + at) = rq[i];
-                        *(uint4*)(Gt + at) = rg[i];
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < NCH; ++i) {
-                        const int r = r0 + NT / CH * i, at = r * P + d0;
-                        const bool on = din && alive >> r & 1;
-                        *(uint4*)(Qt + at) = on ? rq[i] : make_uint4(0, 0, 0, 0);
-                        *(uint4*)(Gt + at) = on ? rg[i] : make_uint4(0, 0, 0, 0);
-                    }
-                }
-                if (tid < BN) {
-                    // the row's part of the exponent: - lse (infinite for an empty row), and - slope of
-                    // its distance to the stage's first token
-                    Rt[tid] = first == BIG ? -INFINITY : BIAS ? -rs.x - slope * (float)tid : -rs.x;
-                    Dl[tid] = first == BIG ? 0.f : rs.y;
-                    Lo[tid] = first;
-                }
-            }
-            __syncthreads();
-            const int tb = s * BN, pb = off + tb;
-            s = seek(s + 1);
-            if (s < s1) fetch(s);
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {   // 32 tokens at a time
-                const int tw = tb + 32 * hf;
-                RowRange st;
+            for (int x = 0; x < SP; ++x) {
                 if (doc) {
-                    const int4 x = strips[tw / WM];
-                    st = {x.x, x.y, x.z, x.w};
+                    if (here < sbase || here >= sbase + 64) look(here);
+                    whit[x] = hit[x] >> (here - sbase) & 1;
+                    wfull[x] = full[x] >> (here - sbase) & 1;
                 } else {
-                    st = token_range(a, n, tw, WM);
+                    const RowRange st = token_range(a, n, tb + WM * x, WM);
+                    whit[x] = st.lo <= jw + WK - 1 && st.hi >= jw;
+                    wfull[x] = st.last <= jw && st.pos >= jw + WK - 1;
                 }
-                if (st.lo > jw + WK - 1 || st.hi < jw) continue;   // no row of the strip sees this wave's keys
-                const bool edge = dead || st.last > jw || st.pos < jw + WK - 1;
+            }
+            q0 = q1;
+            q1 = q1 < s1 ? seek(q1 + 1) : s1;
+            if (R::NS > 1 && q1 < s1) ring.issue(q1, R::freed(place));
+            const E *Qt = sh.x[place], *Gt = sh.y[place];
+            const float *Ls = (const float*)sh.w[0][place], *Dl = (const float*)sh.w[1][place];
+            // rows that see nothing, or lie past the last: 0, whatever the memory holds
+            uint64_t alive = ~0ull;
+            const int* Doc = (const int*)sh.w[2][place];
+            if (doc || pb < 0 || tb + BN > a.Lq) {
+                const int t = tb + lane % BN, p = off + t;
+                alive = __ballot(t < a.Lq && p >= 0 && (!doc || Doc[lane % BN] <= p));
+                if (BN < 64) alive |= ~0ull << (BN & 63);
+                if (alive != ~0ull) ring.blank(place, alive);
+            }
+#pragma unroll
+            for (int hf = 0; hf < SP; ++hf) {   // 32 tokens at a time
+                if (!whit[hf]) continue;   // no row of the strip sees this wave's keys
+                const bool edge = dead || !wfull[hf] || alive != ~0ull;
                 // rows x keys
                 f32x4 w[2][NK], dp[2][NK];
 #pragma unroll
@@ -407,8 +411,8 @@ __global__ __launch_bounds__(NT, BKV(DP, IO::SIZE)) void attn_bwd_kv(AttnArgs a)
                     for (int m = 0; m < NK; ++m) w[rb][m] = dp[rb][m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int kk = 0; kk < KK; ++kk) {
-                        const int at = (32 * hf + 16 * rb + c) * P + 32 * kk + 8 * g;
-                        const Frag<IO> fq = frag_at<IO>(Qt + at), fg = frag_at<IO>(Gt + at);
+                        const Frag<IO> fq = frag_row<IO, DP>(Qt, 32 * hf + 16 * rb, kk, g, c);
+                        const Frag<IO> fg = frag_row<IO, DP>(Gt, 32 * hf + 16 * rb, kk, g, c);
 #pragma unroll
                         for (int m = 0; m < NK; ++m) {
                             w[rb][m] = mma(fq, k[m][kk], w[rb][m]);
@@ -419,7 +423,12 @@ __global__ __launch_bounds__(NT, BKV(DP, IO::SIZE)) void attn_bwd_kv(AttnArgs a)
 #pragma unroll
                 for (int rb = 0; rb < 2; ++rb) {
                     const int rr = 32 * hf + 16 * rb + 4 * g;
-                    const f32x4 rt = *(const f32x4*)(Rt + rr), dl = *(const f32x4*)(Dl + rr);
+                    // the row's part of the exponent: - lse, and - slope of its distance to the
+                    // stage's first token
+                    const f32x4 ls = *(const f32x4*)(Ls + rr), dl = *(const f32x4*)(Dl + rr);
+                    f32x4 rt;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) rt[r] = BIAS ? __builtin_fmaf(-slope, (float)(rr + r), -ls[r]) : -ls[r];
 #pragma unroll
                     for (int m = 0; m < NK; ++m) {
                         const float kterm = BIAS ? slope * (float)(key[m] - pb) : 0.f;
@@ -433,11 +442,13 @@ __global__ __launch_bounds__(NT, BKV(DP, IO::SIZE)) void attn_bwd_kv(AttnArgs a)
                         }
                         if (edge) {
                             keep_branch();
-                            const int4 lo4 = *(const int4*)(Lo + rr);
-                            const int lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w};
 #pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                if (key[m] < lo[r] || key[m] > pb + rr + r) w[rb][m][r] = 0.f;
+                            for (int r = 0; r < 4; ++r) {
+                                const int p = pb + rr + r;
+                                int lo = max(0, p - a.window + 1);
+                                if (doc) lo = max(lo, Doc[rr + r]);
+                                if (key[m] < lo || key[m] > p || !(alive >> (rr + r) & 1)) w[rb][m][r] = 0.f;
+                            }
                         }
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
@@ -454,8 +465,8 @@ __global__ __launch_bounds__(NT, BKV(DP, IO::SIZE)) void attn_bwd_kv(AttnArgs a)
                 }
 #pragma unroll
                 for (int d = 0; d < ND; ++d) {
-                    const Frag<IO> fg = frag_tr<IO, P>(Gt, 32 * hf, 16 * d, g, c);
-                    const Frag<IO> fq = frag_tr<IO, P>(Qt, 32 * hf, 16 * d, g, c);
+                    const Frag<IO> fg = frag_tr<IO, DP>(Gt, 32 * hf, 16 * d, g, c);
+                    const Frag<IO> fq = frag_tr<IO, DP>(Qt, 32 * hf, 16 * d, g, c);
 #pragma unroll
                     for (int m = 0; m < NK; ++m) {
                         dv[d][m] = mma(fg, fp[m], dv[d][m]);
@@ -505,7 +516,7 @@ hipError_t pick(const AttnArgs& a, hipStream_t st)
     return a.slopes ? go<IO, DP, false, true>(a, st) : go<IO, DP, false, false>(a, st);
 }
 
-size_t stat_bytes(const AttnArgs& a) { return ((size_t)a.B * a.H * a.Lq * sizeof(float2) + 255) / 256 * 256; }
+size_t stat_bytes(const AttnArgs& a) { return ((size_t)a.B * a.H * a.Lq * 2 * sizeof(float) + 255) / 256 * 256; }
 
 }  // namespace
 
@@ -518,7 +529,7 @@ hipError_t launch_attn_bwd(Store s, const AttnArgs& a, void* ws, hipStream_t st)
 {
     AttnArgs x = a;
     x.ntile = (a.Lq + BM - 1) / BM;
-    x.rowstat = (float2*)ws;
+    x.rowstat = (float*)ws;
     x.strips = (int4*)((char*)ws + stat_bytes(a));
     if (s == Store::F32) return a.D <= 64 ? pick<f32_io, 64>(x, st) : pick<f32_io, 128>(x, st);
     return a.D <= 64 ? pick<bf16_io, 64>(x, st) : pick<bf16_io, 128>(x, st);

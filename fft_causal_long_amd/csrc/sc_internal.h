@@ -320,9 +320,9 @@ struct AttnArgs {
     // set by the launchers
     int ntile, nsplit;
     float *part, *part_lse;  // forward: the splits' results
-    float2* rowstat;         // backward: (lse in base 2, delta) of each packed row
-    int4* strips;            // backward: per 32-row strip the lowest and the highest key seen,
-                             // the highest first key and the lowest position
+    float* rowstat;          // backward: lse in base 2 of each row (B, H, Lq), then delta
+    int4* strips;            // backward with documents: per 32-token strip the lowest and the
+                             // highest key seen, the highest first key and the lowest position
 };
 size_t attn_fwd_bytes(const AttnArgs& a);
 hipError_t launch_attn(Store st, const AttnArgs& a, void* ws, hipStream_t stream);
