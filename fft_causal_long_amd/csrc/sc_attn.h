@@ -256,6 +256,9 @@ __device__ __forceinline__ int seq_len(const AttnArgs& a, int b)
     return a.kv_len ? min(max(a.kv_len[b], 0), a.Lk) : a.Lk;
 }
 
+// Token of a packed row (its head within the group is the remainder).
+__device__ __forceinline__ int token_of(const AttnArgs& a, int row) { return a.G == 1 ? row : row / a.G; }
+
 // First key that position p may see: past p if its row is empty (p outside the sequence, or its
 // document starts after it).
 __device__ __forceinline__ int first_key(const AttnArgs& a, int b, int p, int n)
@@ -291,8 +294,8 @@ __device__ __forceinline__ RowRange token_range(const AttnArgs& a, int n, int t,
 __device__ __forceinline__ RowRange packed_range(const AttnArgs& a, int n, int r, int rows)
 {
     if (r >= a.nrow) return {BIG, -1, 0, BIG};
-    const int t = r / a.G;
-    return token_range(a, n, t, (min(r + rows, a.nrow) - 1) / a.G - t + 1);
+    const int t = token_of(a, r);
+    return token_range(a, n, t, token_of(a, min(r + rows, a.nrow) - 1) - t + 1);
 }
 
 // The range of a wave's strip from its lanes' rows (lo = BIG: empty).

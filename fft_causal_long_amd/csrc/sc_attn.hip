@@ -56,7 +56,8 @@ __global__ __launch_bounds__(NT, FWV(DP, IO::SIZE)) void attn_fwd(AttnArgs a)
     const int tile = a.ntile - 1 - (int)(id / (uint32_t)a.nsplit);
     const int b = bh / a.Hkv, hk = bh % a.Hkv;
     const int n = seq_len(a, b);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);   // uniform, so that branches on it are
 
     // this lane's rows
     int row[NQ], pos[NQ], lo[NQ];
@@ -68,7 +69,7 @@ __global__ __launch_bounds__(NT, FWV(DP, IO::SIZE)) void attn_fwd(AttnArgs a)
     for (int m = 0; m < NQ; ++m) {
         row[m] = rw + 16 * m + c;
         const bool in = row[m] < a.nrow;
-        const int i = in ? row[m] / a.G : 0, h = hk * a.G + (in ? row[m] % a.G : 0);
+        const int i = in ? token_of(a, row[m]) : 0, h = in ? hk * a.G + row[m] - i * a.G : hk * a.G;
         pos[m] = n - a.Lq + i;
         lo[m] = in ? first_key(a, b, pos[m], n) : BIG;
         empty[m] = lo[m] == BIG;
@@ -239,7 +240,7 @@ __global__ __launch_bounds__(NT, FWV(DP, IO::SIZE)) void attn_fwd(AttnArgs a)
         const bool none = empty[m] || l == 0.f;
         const float inv = none ? 0.f : 1.0f / l;
         const float ls = none ? -INFINITY : mx[m] + __builtin_amdgcn_logf(l);
-        const int i = row[m] / a.G, h = hk * a.G + row[m] % a.G;
+        const int i = token_of(a, row[m]), h = hk * a.G + row[m] - i * a.G;
         if (a.nsplit > 1) {
             const int64_t at = ((int64_t)split * a.nbh + bh) * a.nrow + row[m];
             float* op = a.part + at * a.D;
@@ -282,7 +283,7 @@ __global__ __launch_bounds__(NT) void attn_few(AttnArgs a)
     const int bh = (int)(id % (uint32_t)a.nbh), split = (int)(id / (uint32_t)a.nbh);
     const int b = bh / a.Hkv, hk = bh % a.Hkv;
     const int n = seq_len(a, b);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int grp = lane / LPK, d0 = lane % LPK * V;
     const bool din = d0 < a.D;
     const int32_t* doc = a.doc ? a.doc + (int64_t)b * a.Lk : nullptr;

@@ -73,7 +73,8 @@ __global__ __launch_bounds__(NT, BQV(DP, IO::SIZE)) void attn_bwd_q(AttnArgs a)
     const int tile = a.ntile - 1 - (int)(id / (uint32_t)nbh);
     const int b = bh / a.H, h = bh % a.H, hk = h / a.G;
     const int n = seq_len(a, b);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);   // uniform, so that branches on it are
 
     int pos[NQ], lo[NQ];
     bool empty[NQ];
@@ -266,7 +267,8 @@ __global__ __launch_bounds__(NT, BKV(DP, IO::SIZE)) void attn_bwd_kv(AttnArgs a)
     const int kt = (int)(id / (uint32_t)a.nbh);   // the first keys are seen by most rows: first
     const int b = bh / a.Hkv, hk = bh % a.Hkv;
     const int n = seq_len(a, b);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);   // uniform, so that branches on it are
     const int jb = kt * BK, jw = jb + wave * WK;   // first key of the workgroup, of the wave
 
     Frag<IO> k[NK][KK], v[NK][KK];
