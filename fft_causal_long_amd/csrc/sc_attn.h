@@ -29,7 +29,6 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float LN2 = 0.69314718055994530942f;
-constexpr int NT = 256;   // threads of a workgroup
 constexpr int BIG = 0x7fffffff;
 
 // Eight elements of an operand row.
@@ -326,11 +325,12 @@ constexpr int stages = IO::SIZE == 4 && DP == 128 ? 1 : 3;
 // 32-bit values a row.  issue(s, t) starts stage s's loads into place t; rows past the last are
 // read from the last.  ready() waits until they are in LDS for the whole workgroup; after it the
 // place used before is free.
-template <class IO, int DP>
+template <class IO, int DP, int NT>
 struct Ring {
     using E = typename IO::T;
     static constexpr int BN = stage_rows<IO, DP>, NS = stages<IO, DP>, V = 16 / IO::SIZE, CH = DP / V;
     static constexpr int NCH = BN * CH / NT, TILE = BN * DP;   // loads a thread and tensor; elements
+    static_assert(BN * CH % NT == 0, "whole rounds of loads");
     struct Shared {
         E x[NS][TILE], y[NS][TILE];
         uint32_t w[3][NS][64];   // a wave writes 64 of them, whatever BN
@@ -363,8 +363,8 @@ struct Ring {
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
             const int64_t r = min(b + NT / CH * i, rows - 1);
-            load_lds16(xp + r * xs, __builtin_amdgcn_readfirstlane(lx + i * 4096));
-            load_lds16(yp + r * ys, __builtin_amdgcn_readfirstlane(ly + i * 4096));
+            load_lds16(xp + r * xs, __builtin_amdgcn_readfirstlane(lx + i * (NT * 16)));
+            load_lds16(yp + r * ys, __builtin_amdgcn_readfirstlane(ly + i * (NT * 16)));
         }
         // every wave brings the whole row of values (the same bytes to the same place)
 #pragma unroll
@@ -427,6 +427,21 @@ __device__ __forceinline__ void put4(typename IO::T* p, const f32x4& x)
 {
     if constexpr (IO::SIZE == 2) *(uint2*)p = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
     else *(float4*)p = make_float4(x[0], x[1], x[2], x[3]);
+}
+
+// The smallest and the largest key of the waves' ranges (through LDS, NW of them).
+template <int NW>
+__device__ __forceinline__ void join_ranges(int4 (&sh)[NW], const RowRange& r, int wave, int lane, int& lo, int& hi)
+{
+    if (lane == 0) sh[wave] = make_int4(r.lo, r.hi, r.last, r.pos);
+    __syncthreads();
+    lo = BIG;
+    hi = -1;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        lo = min(lo, sh[w].x);
+        hi = max(hi, sh[w].y);
+    }
 }
 
 }  // namespace attn

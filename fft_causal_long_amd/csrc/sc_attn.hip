@@ -31,22 +31,31 @@ namespace {
 
 using namespace attn;
 
-constexpr int NQ = 2;             // 16-row blocks of a wave
-constexpr int WM = 16 * NQ;       // rows of a wave
-constexpr int BM = 4 * WM;        // rows of a workgroup
+constexpr int NT = 256;           // threads of attn_few and attn_join
+constexpr int BM = 128;           // rows of a workgroup of attn_fwd
 constexpr float SLACK = 8.f;      // a row's base may lag its maximum by this (base 2)
 
-#ifndef FWV
-#define FWV(DP, SZ) (SZ == 4 ? 1 : DP == 64 ? 3 : 2)
+#ifndef FNQ
+#define FNQ(DP, SZ) (SZ == 4 ? 1 : 2)
 #endif
+#ifndef FWV
+#define FWV(DP, SZ) (SZ == 4 ? 2 : DP == 64 ? 3 : 2)
+#endif
+// 16-row blocks of a wave, and its waves
+template <class IO, int DP>
+constexpr int fwd_blocks = FNQ(DP, IO::SIZE);
+template <class IO, int DP>
+constexpr int fwd_waves = BM / 16 / fwd_blocks<IO, DP>;
+
 template <class IO, int DP, bool CAP, bool BIAS>
-__global__ __launch_bounds__(NT, FWV(DP, IO::SIZE)) void attn_fwd(AttnArgs a)
+__global__ __launch_bounds__((64 * fwd_waves<IO, DP>), FWV(DP, IO::SIZE)) void attn_fwd(AttnArgs a)
 {
     using E = typename IO::T;
-    using R = Ring<IO, DP>;
+    constexpr int NQ = fwd_blocks<IO, DP>, NW = fwd_waves<IO, DP>, WM = 16 * NQ;   // WM: rows of a wave
+    using R = Ring<IO, DP, 64 * NW>;
     constexpr int KK = DP / 32, ND = DP / 16, BN = R::BN, KB = BN / 16;   // 16-key blocks of a tile
     __shared__ __attribute__((aligned(1024))) typename R::Shared sh;
-    __shared__ int range[2][4];
+    __shared__ int4 range[NW];
 
     uint32_t id = blockIdx.x;
     const int bh = (int)(id % (uint32_t)a.nbh);
@@ -84,13 +93,7 @@ __global__ __launch_bounds__(NT, FWV(DP, IO::SIZE)) void attn_fwd(AttnArgs a)
     const RowRange rr = a.doc ? lanes_range(lo, pos) : packed_range(a, n, rw, WM);
     int klo = rr.lo, khi = rr.hi;
     if (a.doc) {
-        if (lane == 0) {
-            range[0][wave] = rr.lo;
-            range[1][wave] = rr.hi;
-        }
-        __syncthreads();
-        klo = min(min(range[0][0], range[0][1]), min(range[0][2], range[0][3]));
-        khi = max(max(range[1][0], range[1][1]), max(range[1][2], range[1][3]));
+        join_ranges<NW>(range, rr, wave, lane, klo, khi);
     } else {
         const RowRange all = packed_range(a, n, tile * BM, BM);
         klo = all.lo;
@@ -275,11 +278,15 @@ __global__ __launch_bounds__(NT) void attn_few(AttnArgs a)
 {
     using E = typename IO::T;
     constexpr int V = vec_elems<IO>, KPW = 64 / LPK;   // keys of a load
-    constexpr int U = 4;                               // loads in flight of k, and of v
+#ifndef FEWU
+#define FEWU 4
+#define FEWORDER 1
+#endif
+    constexpr int U = FEWU;                               // loads in flight of k, and of v
     constexpr int STEP = KPW * U;                      // keys of a wave's turn
     __shared__ float sm[4][RT], sl[4][RT], so[4][RT][LPK * V];
 
-    uint32_t id = blockIdx.x;
+    const uint32_t id = FEWORDER ? die_order(blockIdx.x, gridDim.x) : blockIdx.x;
     const int bh = (int)(id % (uint32_t)a.nbh), split = (int)(id / (uint32_t)a.nbh);
     const int b = bh / a.Hkv, hk = bh % a.Hkv;
     const int n = seq_len(a, b);
@@ -327,16 +334,30 @@ __global__ __launch_bounds__(NT) void attn_few(AttnArgs a)
     const float scale2 = CAP ? a.scale / a.cap : a.scale * LOG2E, cap2 = a.cap * LOG2E;
     const E* kp = (const E*)a.k + b * a.ks[0] + hk * a.ks[2] + (din ? d0 : 0);
     const E* vp = (const E*)a.v + b * a.vs[0] + hk * a.vs[2] + (din ? d0 : 0);
+    // a turn's loads are issued while the turn before is computed; keys past the last read it again
+    uint4 nk[U], nv[U];
+    int nd[U];
+    auto fetch = [&](int j0) {
+#pragma unroll
+        for (int t = 0; t < U; ++t) {
+            const int64_t j = min(j0 + t * KPW + grp, k1 - 1);
+            nk[t] = *(const uint4*)(kp + j * a.ks[1]);
+            nv[t] = *(const uint4*)(vp + j * a.vs[1]);
+            if (doc) nd[t] = doc[j];
+        }
+    };
+    if (k0 + wave * STEP < k1) fetch(k0 + wave * STEP);
     for (int j0 = k0 + wave * STEP; j0 < k1; j0 += 4 * STEP) {
         uint4 rk[U], rv[U];
         bool on[U];
 #pragma unroll
         for (int t = 0; t < U; ++t) {
-            const int j = j0 + t * KPW + grp, jc = j < k1 ? j : k1 - 1;   // some key of the sequence
-            on[t] = j < k1 && (!doc || doc[jc] <= jc);
-            rk[t] = *(const uint4*)(kp + (int64_t)jc * a.ks[1]);
-            rv[t] = *(const uint4*)(vp + (int64_t)jc * a.vs[1]);
+            const int j = j0 + t * KPW + grp;
+            on[t] = j < k1 && (!doc || nd[t] <= j);
+            rk[t] = nk[t];
+            rv[t] = nv[t];
         }
+        if (j0 + 4 * STEP < k1) fetch(j0 + 4 * STEP);
         const bool edge = j0 < last || j0 + STEP - 1 > first || j0 + STEP > k1 || doc;
         float s[RT][U];
 #pragma unroll
@@ -506,7 +527,9 @@ int splits(const AttnArgs& a)
 template <class IO, int DP, bool CAP, bool BIAS>
 hipError_t go(const AttnArgs& a, int64_t blocks, hipStream_t st)
 {
-    hipLaunchKernelGGL((attn_fwd<IO, DP, CAP, BIAS>), dim3((unsigned)blocks), dim3(NT), 0, st, a);
+    constexpr int threads = 64 * fwd_waves<IO, DP>;
+    if (!grid_ok(blocks, threads)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((attn_fwd<IO, DP, CAP, BIAS>), dim3((unsigned)blocks), dim3(threads), 0, st, a);
     return hipGetLastError();
 }
 

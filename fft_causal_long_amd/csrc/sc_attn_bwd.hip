@@ -30,20 +30,34 @@ namespace {
 
 using namespace attn;
 
-constexpr int NQ = 2;         // 16-row blocks of a wave
-constexpr int WM = 16 * NQ;   // tokens of a wave and of a strip
-constexpr int BM = 4 * WM;    // tokens of a workgroup
+constexpr int STRIP = 32;     // tokens of a strip (half a stage, or a stage)
+constexpr int BM = 128;       // tokens of a workgroup of attn_bwd_q
 
-// 16-key blocks of a wave (attn_bwd_kv): float32 operands of 128 leave room for one
-template <class IO, int DP>
-constexpr int key_blocks = IO::SIZE == 4 && DP == 128 ? 1 : 2;
-
+#ifndef QNQ
+#define QNQ(DP, SZ) (SZ == 4 ? 1 : 2)
+#endif
+#ifndef KNK
+#define KNK(DP, SZ) (SZ == 4 ? 1 : 2)
+#endif
+#ifndef KNW
+#define KNW(DP, SZ) (SZ == 4 ? 8 : 4)
+#endif
 #ifndef BQV
-#define BQV(DP, SZ) (SZ == 4 ? 1 : DP == 64 ? 3 : 2)
+#define BQV(DP, SZ) (SZ == 4 ? 2 : DP == 64 ? 3 : 2)
 #endif
 #ifndef BKV
-#define BKV(DP, SZ) (SZ == 4 ? 1 : DP == 64 ? 2 : 1)
+#define BKV(DP, SZ) (SZ == 4 ? 2 : DP == 64 ? 2 : 1)
 #endif
+// 16-row blocks of a wave of attn_bwd_q, and its waves; 16-key blocks of a wave of attn_bwd_kv,
+// and its waves
+template <class IO, int DP>
+constexpr int q_blocks = QNQ(DP, IO::SIZE);
+template <class IO, int DP>
+constexpr int q_waves = BM / 16 / q_blocks<IO, DP>;
+template <class IO, int DP>
+constexpr int kv_blocks = KNK(DP, IO::SIZE);
+template <class IO, int DP>
+constexpr int kv_waves = KNW(DP, IO::SIZE);
 
 // The score in base 2 of the raw product y plus `add`; dcap: the factor of dS that the cap adds.
 template <class IO, bool CAP>
@@ -59,13 +73,14 @@ __device__ __forceinline__ float score2(float y, float scale2, float cap2, float
 }
 
 template <class IO, int DP, bool CAP, bool BIAS>
-__global__ __launch_bounds__(NT, BQV(DP, IO::SIZE)) void attn_bwd_q(AttnArgs a)
+__global__ __launch_bounds__((64 * q_waves<IO, DP>), BQV(DP, IO::SIZE)) void attn_bwd_q(AttnArgs a)
 {
     using E = typename IO::T;
-    using R = Ring<IO, DP>;
+    constexpr int NQ = q_blocks<IO, DP>, NW = q_waves<IO, DP>, WM = 16 * NQ;   // WM: tokens of a wave
+    using R = Ring<IO, DP, 64 * NW>;
     constexpr int V = vec_elems<IO>, KK = DP / 32, ND = DP / 16, BN = R::BN;
     __shared__ __attribute__((aligned(1024))) typename R::Shared sh;
-    __shared__ int range[2][4];
+    __shared__ int4 range[NW];
 
     const int nbh = a.B * a.H;
     uint32_t id = blockIdx.x;
@@ -128,15 +143,17 @@ __global__ __launch_bounds__(NT, BQV(DP, IO::SIZE)) void attn_bwd_q(AttnArgs a)
     const RowRange rr = a.doc ? lanes_range(lo, pos) : token_range(a, n, rw, WM);
     int klo, khi;
     if (a.doc) {
-        if (lane == 0) {
-            range[0][wave] = rr.lo;
-            range[1][wave] = rr.hi;
-            // every head's rows have the same ranges: the first one's workgroup records them
-            if (h == 0) a.strips[((int64_t)b * a.ntile + tile) * 4 + wave] = make_int4(rr.lo, rr.hi, rr.last, rr.pos);
+        join_ranges<NW>(range, rr, wave, lane, klo, khi);
+        // every head's rows have the same ranges: the first one's workgroup records them
+        if (h == 0 && tid < BM / STRIP) {
+            constexpr int per = STRIP / WM;   // waves of a strip
+            int4 x = range[tid * per];
+            if (per > 1) {
+                const int4 y = range[tid * per + per - 1];
+                x = make_int4(min(x.x, y.x), max(x.y, y.y), max(x.z, y.z), min(x.w, y.w));
+            }
+            a.strips[((int64_t)b * a.ntile + tile) * (BM / STRIP) + tid] = x;
         }
-        __syncthreads();
-        klo = min(min(range[0][0], range[0][1]), min(range[0][2], range[0][3]));
-        khi = max(max(range[1][0], range[1][1]), max(range[1][2], range[1][3]));
     } else {
         const RowRange all = token_range(a, n, tile * BM, BM);
         klo = all.lo;
@@ -177,7 +194,7 @@ __global__ __launch_bounds__(NT, BQV(DP, IO::SIZE)) void attn_bwd_q(AttnArgs a)
         }
         if (j0 > rr.hi || j0 + BN - 1 < rr.lo) continue;
 
-        const bool edge = j0 < rr.last || j0 + BN - 1 > rr.pos || live != ~0ull;
+        const bool edge = j0 < rr.last || j0 + BN - 1 > rr.pos;
 #pragma unroll
         for (int hf = 0; hf < BN / 32; ++hf) {   // 32 keys at a time
             f32x4 s[2][NQ], dp[2][NQ];
@@ -214,14 +231,20 @@ __global__ __launch_bounds__(NT, BQV(DP, IO::SIZE)) void attn_bwd_q(AttnArgs a)
                     keep_branch();
                     const int first = lo[m] - j0 - 4 * g;
                     const uint32_t span = (uint32_t)(pos[m] - lo[m]);
+#pragma unroll
+                    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if ((uint32_t)(32 * hf + 16 * kb + r - first) > span) s[kb][m][r] = 0.f;
+                }
+                if (live != ~0ull) {
+                    keep_branch();
                     const uint64_t mine = live >> (4 * g);
 #pragma unroll
                     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const int jj = 32 * hf + 16 * kb + r;
-                            if ((uint32_t)(jj - first) > span || !(mine >> jj & 1)) s[kb][m][r] = 0.f;
-                        }
+                        for (int r = 0; r < 4; ++r)
+                            if (!(mine >> (32 * hf + 16 * kb + r) & 1)) s[kb][m][r] = 0.f;
                 }
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb)
@@ -254,13 +277,14 @@ __global__ __launch_bounds__(NT, BQV(DP, IO::SIZE)) void attn_bwd_q(AttnArgs a)
 }
 
 template <class IO, int DP, bool CAP, bool BIAS>
-__global__ __launch_bounds__(NT, BKV(DP, IO::SIZE)) void attn_bwd_kv(AttnArgs a)
+__global__ __launch_bounds__((64 * kv_waves<IO, DP>), BKV(DP, IO::SIZE)) void attn_bwd_kv(AttnArgs a)
 {
     using E = typename IO::T;
-    using R = Ring<IO, DP>;
-    constexpr int KK = DP / 32, ND = DP / 16, NK = key_blocks<IO, DP>, WK = 16 * NK, BK = 4 * WK;
-    constexpr int BN = R::BN, SP = BN / WM;   // tokens and strips of a stage
+    constexpr int NW = kv_waves<IO, DP>, NK = kv_blocks<IO, DP>, WK = 16 * NK, BK = NW * WK;
+    using R = Ring<IO, DP, 64 * NW>;
+    constexpr int KK = DP / 32, ND = DP / 16, BN = R::BN, SP = BN / STRIP;   // tokens and strips of a stage
     __shared__ __attribute__((aligned(1024))) typename R::Shared sh;
+    __shared__ __attribute__((aligned(16))) int first[NW][BN], span[NW][BN];   // each wave its own copy
 
     uint32_t id = blockIdx.x;
     const int bh = (int)(id % (uint32_t)a.nbh);
@@ -310,7 +334,7 @@ __global__ __launch_bounds__(NT, BKV(DP, IO::SIZE)) void attn_bwd_kv(AttnArgs a)
             s1 = (int)((phi - off) / BN + 1);
         }
     }
-    const int4* strips = a.strips + (int64_t)b * a.ntile * 4;
+    const int4* strips = a.strips + (int64_t)b * a.ntile * (BM / STRIP);
     // With documents: which of 64 stages from sbase on see this workgroup's keys, and which of their
     // strips this wave's (hit) and every key of them (full), read together so that the walk itself
     // waits for no load of its own.
@@ -382,7 +406,7 @@ __global__ __launch_bounds__(NT, BKV(DP, IO::SIZE)) void attn_bwd_kv(AttnArgs a)
                     whit[x] = hit[x] >> (here - sbase) & 1;
                     wfull[x] = full[x] >> (here - sbase) & 1;
                 } else {
-                    const RowRange st = token_range(a, n, tb + WM * x, WM);
+                    const RowRange st = token_range(a, n, tb + STRIP * x, STRIP);
                     whit[x] = st.lo <= jw + WK - 1 && st.hi >= jw;
                     wfull[x] = st.last <= jw && st.pos >= jw + WK - 1;
                 }
@@ -392,12 +416,21 @@ __global__ __launch_bounds__(NT, BKV(DP, IO::SIZE)) void attn_bwd_kv(AttnArgs a)
             if (R::NS > 1 && q1 < s1) ring.issue(q1, R::freed(place));
             const E *Qt = sh.x[place], *Gt = sh.y[place];
             const float *Ls = (const float*)sh.w[0][place], *Dl = (const float*)sh.w[1][place];
-            // rows that see nothing, or lie past the last: 0, whatever the memory holds
-            uint64_t alive = ~0ull;
             const int* Doc = (const int*)sh.w[2][place];
-            if (doc || pb < 0 || tb + BN > a.Lq) {
-                const int t = tb + lane % BN, p = off + t;
-                alive = __ballot(t < a.Lq && p >= 0 && (!doc || Doc[lane % BN] <= p));
+            uint64_t alive = ~0ull;
+            bool masked = dead;   // some strip needs its rows' bounds
+#pragma unroll
+            for (int x = 0; x < SP; ++x) masked |= whit[x] && !wfull[x];
+            if (doc || pb < 0 || tb + BN > a.Lq || masked) {
+                // lane's row of the stage: its first key, and how many it sees less one
+                const int r = lane % BN, p = pb + r;
+                int lo = max(0, p - a.window + 1);
+                if (doc) lo = max(lo, Doc[r]);
+                const bool some = tb + r < a.Lq && p >= 0 && lo <= p;
+                first[wave][r] = some ? lo : BIG;
+                span[wave][r] = some ? p - lo : -1;
+                // rows that see nothing, or lie past the last: 0, whatever the memory holds
+                alive = __ballot(some);
                 if (BN < 64) alive |= ~0ull << (BN & 63);
                 if (alive != ~0ull) ring.blank(place, alive);
             }
@@ -444,13 +477,11 @@ __global__ __launch_bounds__(NT, BKV(DP, IO::SIZE)) void attn_bwd_kv(AttnArgs a)
                         }
                         if (edge) {
                             keep_branch();
+                            const int4 fi = *(const int4*)&first[wave][rr], sp = *(const int4*)&span[wave][rr];
+                            const int f4[4] = {fi.x, fi.y, fi.z, fi.w}, s4[4] = {sp.x, sp.y, sp.z, sp.w};
 #pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                const int p = pb + rr + r;
-                                int lo = max(0, p - a.window + 1);
-                                if (doc) lo = max(lo, Doc[rr + r]);
-                                if (key[m] < lo || key[m] > p || !(alive >> (rr + r) & 1)) w[rb][m][r] = 0.f;
-                            }
+                            for (int r = 0; r < 4; ++r)
+                                if (key[m] - f4[r] < 0 || key[m] - f4[r] > s4[r]) w[rb][m][r] = 0.f;
                         }
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
@@ -497,16 +528,17 @@ __global__ __launch_bounds__(NT, BKV(DP, IO::SIZE)) void attn_bwd_kv(AttnArgs a)
 template <class IO, int DP, bool CAP, bool BIAS>
 hipError_t go(const AttnArgs& a, hipStream_t st)
 {
-    constexpr int BK = 64 * key_blocks<IO, DP>;
+    constexpr int BK = 16 * kv_blocks<IO, DP> * kv_waves<IO, DP>;
+    constexpr int qt = 64 * q_waves<IO, DP>, kt = 64 * kv_waves<IO, DP>;
     const int64_t qb = (int64_t)a.ntile * a.B * a.H, kb = (int64_t)((a.Lk + BK - 1) / BK) * a.nbh;
-    if (!grid_ok(qb, NT) || !grid_ok(kb, NT)) return hipErrorInvalidValue;
+    if (!grid_ok(qb, qt) || !grid_ok(kb, kt)) return hipErrorInvalidValue;
     if (qb > 0) {
-        hipLaunchKernelGGL((attn_bwd_q<IO, DP, CAP, BIAS>), dim3((unsigned)qb), dim3(NT), 0, st, a);
+        hipLaunchKernelGGL((attn_bwd_q<IO, DP, CAP, BIAS>), dim3((unsigned)qb), dim3(qt), 0, st, a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     if (kb == 0) return hipSuccess;
-    hipLaunchKernelGGL((attn_bwd_kv<IO, DP, CAP, BIAS>), dim3((unsigned)kb), dim3(NT), 0, st, a);
+    hipLaunchKernelGGL((attn_bwd_kv<IO, DP, CAP, BIAS>), dim3((unsigned)kb), dim3(kt), 0, st, a);
     return hipGetLastError();
 }
 
@@ -524,7 +556,7 @@ size_t stat_bytes(const AttnArgs& a) { return ((size_t)a.B * a.H * a.Lq * 2 * si
 
 size_t attn_bwd_bytes(const AttnArgs& a)
 {
-    return stat_bytes(a) + (a.doc ? (size_t)a.B * ((a.Lq + BM - 1) / BM) * 4 * sizeof(int4) : 0);
+    return stat_bytes(a) + (a.doc ? (size_t)a.B * ((a.Lq + BM - 1) / BM) * (BM / STRIP) * sizeof(int4) : 0);
 }
 
 hipError_t launch_attn_bwd(Store s, const AttnArgs& a, void* ws, hipStream_t st)
