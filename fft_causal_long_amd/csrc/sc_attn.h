@@ -14,8 +14,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <type_traits>
-
 #include "sc_device.h"
 #include "sc_internal.h"
 
@@ -191,22 +189,6 @@ __device__ __forceinline__ float gmax(float v)
     v = fmaxf(v, __shfl_xor(v, 16));
     return fmaxf(v, __shfl_xor(v, 32));
 }
-// sum over N neighbouring lanes (8, 16 or 32, aligned), by lane permutations in the add itself up
-// to 16: quad swaps, then mirrors of 8 and of 16
-template <int N>
-__device__ __forceinline__ float lane_sum(float v)
-{
-    auto swapped = [](float x, auto ctrl) {
-        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), decltype(ctrl)::value, 0xf, 0xf, true));
-    };
-    using std::integral_constant;
-    v += swapped(v, integral_constant<int, 0xb1>());    // quad_perm 1, 0, 3, 2
-    v += swapped(v, integral_constant<int, 0x4e>());    // quad_perm 2, 3, 0, 1
-    v += swapped(v, integral_constant<int, 0x141>());   // row_half_mirror
-    if constexpr (N >= 16) v += swapped(v, integral_constant<int, 0x140>());   // row_mirror
-    if constexpr (N >= 32) v += __shfl_xor(v, 16);
-    return v;
-}
 __device__ __forceinline__ int wave_min(int v)
 {
 #pragma unroll
@@ -313,24 +295,27 @@ __device__ __forceinline__ RowRange lanes_range(const int (&lo)[NR], const int (
     return {wave_min(x.lo), wave_max(x.hi), wave_max(x.last), wave_min(x.pos)};
 }
 
-// Rows of one stage (keys, or tokens of a head), and how many stages a workgroup's LDS holds:
-// three (48 KB), two in flight while one is used; float32 heads of 128 leave room for one, whose
-// loads are not hidden.  All under 64 KB, the reach of an asynchronous load's LDS offset.
+// Rows of one stage (keys, or tokens of a head) of the workgroups that share one among waves, and
+// how many stages of BN rows LDS holds: three (48 KB and less), two in flight while one is used;
+// float32 heads of 128 leave room for one, whose loads are not hidden.  All under 64 KB, the reach
+// of an asynchronous load's LDS offset.
 template <class IO, int DP>
 constexpr int stage_rows = IO::SIZE == 2 && DP == 64 ? 64 : 32;
-template <class IO, int DP>
-constexpr int stages = IO::SIZE == 4 && DP == 128 ? 1 : 3;
+template <class IO, int DP, int BN>
+constexpr int stages = 3 * 2 * BN * DP * IO::SIZE <= 48 * 1024 ? 3 : 1;
 
 // A ring of stages, each BN rows of two tensors x and y (k and v, or q and dout) and up to three
 // 32-bit values a row.  issue(s, t) starts stage s's loads into place t; rows past the last are
 // read from the last.  ready() waits until they are in LDS for the whole workgroup; after it the
 // place used before is free.
-template <class IO, int DP, int NT>
+template <class IO, int DP, int NT, int BN = stage_rows<IO, DP>>
 struct Ring {
     using E = typename IO::T;
-    static constexpr int BN = stage_rows<IO, DP>, NS = stages<IO, DP>, V = 16 / IO::SIZE, CH = DP / V;
+    static constexpr int NS = stages<IO, DP, BN>, V = 16 / IO::SIZE, CH = DP / V;
     static constexpr int NCH = BN * CH / NT, TILE = BN * DP;   // loads a thread and tensor; elements
     static_assert(BN * CH % NT == 0, "whole rounds of loads");
+    static constexpr int RPR = NT / CH;                        // rows of a round of loads
+    static constexpr int NCOL = RPR >= 8 ? 1 : 8 / RPR;        // rounds until a thread's row repeats mod 8
     struct Shared {
         E x[NS][TILE], y[NS][TILE];
         uint32_t w[3][NS][64];   // a wave writes 64 of them, whatever BN
@@ -341,30 +326,43 @@ struct Ring {
     const uint32_t* wp[3];   // null: not wanted
     int64_t xs, ys;          // row strides
     int rows, vfirst = 0;    // vfirst: the first row that has values
-    int r0, lane, wave;
+    int r0, lane, wave, col[NCOL];
 
     __device__ __forceinline__ Ring(Shared& s, int n, int D, int64_t xs_, int64_t ys_)
         : sh(s), wp{nullptr, nullptr, nullptr}, xs(xs_), ys(ys_), rows(n), r0(threadIdx.x / CH),
-          lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), D_(D)
+          lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6))
     {
+        // this thread's chunk of its row of round i; columns past D take the row's first (they meet
+        // zeros of the other operand, or results that are not stored)
+#pragma unroll
+        for (int i = 0; i < NCOL; ++i) {
+            const int d = (((int)threadIdx.x % CH) ^ ((r0 + RPR * i) & 7)) * V;
+            col[i] = d < D ? d : 0;
+        }
     }
     __device__ __forceinline__ void from(const E* x, const E* y)
     {
-        // this thread's chunk of a row; columns past D take the row's first (they meet zeros of the
-        // other operand, or results that are not stored)
-        const int d = (((int)threadIdx.x % CH) ^ (r0 & 7)) * V;
-        xp = x + (d < D_ ? d : 0);
-        yp = y + (d < D_ ? d : 0);
+        xp = x;
+        yp = y;
     }
     __device__ __forceinline__ void issue(int s, int t) const
     {
-        const int b = s * BN + r0;
+        const int64_t b = s * BN + r0;
         const uint32_t lx = lds_offset(sh.x[t]) + wave * 1024, ly = lds_offset(sh.y[t]) + wave * 1024;
+        if ((s + 1) * BN <= rows) {
+            const E *x = xp + b * xs, *y = yp + b * ys;
 #pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-            const int64_t r = min(b + NT / CH * i, rows - 1);
-            load_lds16(xp + r * xs, __builtin_amdgcn_readfirstlane(lx + i * (NT * 16)));
-            load_lds16(yp + r * ys, __builtin_amdgcn_readfirstlane(ly + i * (NT * 16)));
+            for (int i = 0; i < NCH; ++i) {
+                load_lds16(x + i * RPR * xs + col[i % NCOL], __builtin_amdgcn_readfirstlane(lx + i * (NT * 16)));
+                load_lds16(y + i * RPR * ys + col[i % NCOL], __builtin_amdgcn_readfirstlane(ly + i * (NT * 16)));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) {
+                const int64_t r = min<int64_t>(b + RPR * i, rows - 1);
+                load_lds16(xp + r * xs + col[i % NCOL], __builtin_amdgcn_readfirstlane(lx + i * (NT * 16)));
+                load_lds16(yp + r * ys + col[i % NCOL], __builtin_amdgcn_readfirstlane(ly + i * (NT * 16)));
+            }
         }
         // every wave brings the whole row of values (the same bytes to the same place)
 #pragma unroll
@@ -416,9 +414,6 @@ struct Ring {
             }
         __syncthreads();
     }
-
-  private:
-    int D_;
 };
 
 // four consecutive results of a row

@@ -31,29 +31,25 @@ namespace {
 
 using namespace attn;
 
-constexpr int NT = 256;           // threads of attn_few and attn_join
-constexpr int BM = 128;           // rows of a workgroup of attn_fwd
+constexpr int NT = 256;           // threads of attn_join
 constexpr float SLACK = 8.f;      // a row's base may lag its maximum by this (base 2)
 
-#ifndef FNQ
-#define FNQ(DP, SZ) (SZ == 4 ? 1 : 2)
-#endif
-#ifndef FWV
-#define FWV(DP, SZ) (SZ == 4 ? 2 : DP == 64 ? 3 : 2)
-#endif
-// 16-row blocks of a wave, and its waves
-template <class IO, int DP>
-constexpr int fwd_blocks = FNQ(DP, IO::SIZE);
-template <class IO, int DP>
-constexpr int fwd_waves = BM / 16 / fwd_blocks<IO, DP>;
+// A workgroup's shape: NQ 16-row blocks a wave, NW waves, tiles of BN keys.
+template <int NQ_, int NW_, int BN_>
+struct Shape {
+    static constexpr int NQ = NQ_, NW = NW_, BN = BN_, WM = 16 * NQ, BM = NW * WM;   // rows of a wave, of a workgroup
+};
 
-template <class IO, int DP, bool CAP, bool BIAS>
-__global__ __launch_bounds__((64 * fwd_waves<IO, DP>), FWV(DP, IO::SIZE)) void attn_fwd(AttnArgs a)
+#ifndef FWV
+#define FWV(DP, SZ, NW) (SZ == 4 ? (NW == 1 ? 1 : 2) : DP == 64 ? 3 : 2)
+#endif
+template <class IO, int DP, bool CAP, bool BIAS, class S>
+__global__ __launch_bounds__((64 * S::NW), FWV(DP, IO::SIZE, S::NW)) void attn_fwd(AttnArgs a)
 {
     using E = typename IO::T;
-    constexpr int NQ = fwd_blocks<IO, DP>, NW = fwd_waves<IO, DP>, WM = 16 * NQ;   // WM: rows of a wave
-    using R = Ring<IO, DP, 64 * NW>;
-    constexpr int KK = DP / 32, ND = DP / 16, BN = R::BN, KB = BN / 16;   // 16-key blocks of a tile
+    constexpr int NQ = S::NQ, NW = S::NW, WM = S::WM, BM = S::BM, BN = S::BN;
+    using R = Ring<IO, DP, 64 * NW, BN>;
+    constexpr int KK = DP / 32, ND = DP / 16, KB = BN / 16;   // 16-key blocks of a tile
     __shared__ __attribute__((aligned(1024))) typename R::Shared sh;
     __shared__ int4 range[NW];
 
@@ -268,207 +264,6 @@ __global__ __launch_bounds__((64 * fwd_waves<IO, DP>), FWV(DP, IO::SIZE)) void a
     }
 }
 
-// Few rows (decoding): the rows of one key head are RT at most, and a key is read once and used
-// for them all in vector registers; the matrix instructions would leave 16 - RT of their columns
-// idle and make every key pass through LDS.  LPK lanes hold a key's D values (one 16-byte vector
-// each), a wave reads 64 / LPK keys a load, and every group of LPK lanes keeps running statistics
-// of its own, joined over the wave by shuffles and over the waves through LDS at the end.
-template <class IO, int LPK, int RT, bool CAP>
-__global__ __launch_bounds__(NT) void attn_few(AttnArgs a)
-{
-    using E = typename IO::T;
-    constexpr int V = vec_elems<IO>, KPW = 64 / LPK;   // keys of a load
-#ifndef FEWU
-#define FEWU 4
-#define FEWORDER 1
-#endif
-    constexpr int U = FEWU;                               // loads in flight of k, and of v
-    constexpr int STEP = KPW * U;                      // keys of a wave's turn
-    __shared__ float sm[4][RT], sl[4][RT], so[4][RT][LPK * V];
-
-    const uint32_t id = FEWORDER ? die_order(blockIdx.x, gridDim.x) : blockIdx.x;
-    const int bh = (int)(id % (uint32_t)a.nbh), split = (int)(id / (uint32_t)a.nbh);
-    const int b = bh / a.Hkv, hk = bh % a.Hkv;
-    const int n = seq_len(a, b);
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int grp = lane / LPK, d0 = lane % LPK * V;
-    const bool din = d0 < a.D;
-    const int32_t* doc = a.doc ? a.doc + (int64_t)b * a.Lk : nullptr;
-
-    float q[RT][V], slope[RT], acc[RT][V], mx[RT], sum[RT];
-    int lo[RT], pos[RT], klo = BIG, khi = -1, last = 0, first = BIG;
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        const bool in = r < a.nrow;
-        const int i = in ? r / a.G : 0, h = hk * a.G + (in ? r % a.G : 0);
-        pos[r] = n - a.Lq + i;
-        lo[r] = in ? first_key(a, b, pos[r], n) : BIG;
-        if (lo[r] != BIG) {
-            klo = min(klo, lo[r]);
-            khi = max(khi, pos[r]);
-        }
-        last = max(last, lo[r]);      // BIG for an empty row: its scores are always masked
-        first = min(first, pos[r]);
-        slope[r] = a.slopes ? a.slopes[h] * LOG2E : 0.f;
-        const bool on = lo[r] != BIG && din;
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (on) raw = *(const uint4*)((const E*)a.q + b * a.qs[0] + (int64_t)i * a.qs[1] + h * a.qs[2] + d0);
-        const Lanes<IO> x = widen<IO>(raw);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            q[r][e] = x.x[e];
-            acc[r][e] = 0.f;
-        }
-        mx[r] = -INFINITY;
-        sum[r] = 0.f;
-    }
-    // this split's keys, whole turns of the four waves
-    int k0 = 0, k1 = 0;
-    if (khi >= 0) {
-        const int turns = (khi - klo + 1 + 4 * STEP - 1) / (4 * STEP);
-        const int per = (turns + a.nsplit - 1) / a.nsplit;
-        const int64_t s0 = (int64_t)klo + (int64_t)split * per * 4 * STEP;
-        k0 = (int)min<int64_t>(s0, khi + 1);
-        k1 = (int)min<int64_t>(s0 + (int64_t)per * 4 * STEP, khi + 1);
-    }
-    const float scale2 = CAP ? a.scale / a.cap : a.scale * LOG2E, cap2 = a.cap * LOG2E;
-    const E* kp = (const E*)a.k + b * a.ks[0] + hk * a.ks[2] + (din ? d0 : 0);
-    const E* vp = (const E*)a.v + b * a.vs[0] + hk * a.vs[2] + (din ? d0 : 0);
-    // a turn's loads are issued while the turn before is computed; keys past the last read it again
-    uint4 nk[U], nv[U];
-    int nd[U];
-    auto fetch = [&](int j0) {
-#pragma unroll
-        for (int t = 0; t < U; ++t) {
-            const int64_t j = min(j0 + t * KPW + grp, k1 - 1);
-            nk[t] = *(const uint4*)(kp + j * a.ks[1]);
-            nv[t] = *(const uint4*)(vp + j * a.vs[1]);
-            if (doc) nd[t] = doc[j];
-        }
-    };
-    if (k0 + wave * STEP < k1) fetch(k0 + wave * STEP);
-    for (int j0 = k0 + wave * STEP; j0 < k1; j0 += 4 * STEP) {
-        uint4 rk[U], rv[U];
-        bool on[U];
-#pragma unroll
-        for (int t = 0; t < U; ++t) {
-            const int j = j0 + t * KPW + grp;
-            on[t] = j < k1 && (!doc || nd[t] <= j);
-            rk[t] = nk[t];
-            rv[t] = nv[t];
-        }
-        if (j0 + 4 * STEP < k1) fetch(j0 + 4 * STEP);
-        const bool edge = j0 < last || j0 + STEP - 1 > first || j0 + STEP > k1 || doc;
-        float s[RT][U];
-#pragma unroll
-        for (int t = 0; t < U; ++t) {
-            // padding reads as 0, whatever the memory holds
-            const Lanes<IO> k = widen<IO>(on[t] && din ? rk[t] : make_uint4(0, 0, 0, 0));
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                float x = 0.f;
-#pragma unroll
-                for (int e = 0; e < V; ++e) x = __builtin_fmaf(q[r][e], k.x[e], x);
-                s[r][t] = x;
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int t = 0; t < U; ++t) s[r][t] = lane_sum<LPK>(s[r][t]);
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const float base = mx[r] == -INFINITY ? 0.f : mx[r];
-            float top = -INFINITY;
-#pragma unroll
-            for (int t = 0; t < U; ++t) {
-                const int j = j0 + t * KPW + grp;
-                const float add = __builtin_fmaf(slope[r], (float)(j - pos[r]), -base);
-                float x;
-                if constexpr (CAP) x = __builtin_fmaf(cap2, tanh_of<IO>(s[r][t] * scale2), add);
-                else x = __builtin_fmaf(s[r][t], scale2, add);
-                if (edge && (!on[t] || j < lo[r] || j > pos[r])) x = -INFINITY;
-                s[r][t] = x;
-                top = fmaxf(top, x);
-            }
-            if (__any(top > (mx[r] == -INFINITY ? -INFINITY : SLACK))) {
-                if (top > (mx[r] == -INFINITY ? -INFINITY : SLACK)) {
-                    const float now = base + top, f = exp2_hw(mx[r] - now);
-                    sum[r] *= f;
-#pragma unroll
-                    for (int e = 0; e < V; ++e) acc[r][e] *= f;
-                    mx[r] = now;
-#pragma unroll
-                    for (int t = 0; t < U; ++t) s[r][t] -= top;
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < U; ++t) {
-                s[r][t] = exp2_hw(s[r][t]);
-                sum[r] += s[r][t];
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < U; ++t) {
-            const Lanes<IO> v = widen<IO>(on[t] && din ? rv[t] : make_uint4(0, 0, 0, 0));
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int e = 0; e < V; ++e) acc[r][e] = __builtin_fmaf(s[r][t], v.x[e], acc[r][e]);
-        }
-    }
-    // join the wave's groups, then the waves
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        float top = mx[r];
-#pragma unroll
-        for (int m = LPK; m < 64; m <<= 1) top = fmaxf(top, __shfl_xor(top, m));
-        const float f = mx[r] == -INFINITY ? 0.f : exp2_hw(mx[r] - top);
-        sum[r] *= f;
-#pragma unroll
-        for (int e = 0; e < V; ++e) acc[r][e] *= f;
-#pragma unroll
-        for (int m = LPK; m < 64; m <<= 1) {
-            sum[r] += __shfl_xor(sum[r], m);
-#pragma unroll
-            for (int e = 0; e < V; ++e) acc[r][e] += __shfl_xor(acc[r][e], m);
-        }
-        if (lane < LPK) {
-            if (lane == 0) {
-                sm[wave][r] = top;
-                sl[wave][r] = sum[r];
-            }
-#pragma unroll
-            for (int e = 0; e < V; ++e) so[wave][r][d0 + e] = acc[r][e];
-        }
-    }
-    __syncthreads();
-    for (int x = threadIdx.x; x < RT * LPK * V; x += NT) {
-        const int r = x / (LPK * V), d = x % (LPK * V);
-        if (r >= a.nrow || d >= a.D) continue;
-        const float top = fmaxf(fmaxf(sm[0][r], sm[1][r]), fmaxf(sm[2][r], sm[3][r]));
-        float l = 0.f, o = 0.f;
-        if (top != -INFINITY)
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const float f = exp2_hw(sm[w][r] - top);
-                l = __builtin_fmaf(f, sl[w][r], l);
-                o = __builtin_fmaf(f, so[w][r][d], o);
-            }
-        o = top == -INFINITY ? 0.f : o / l;
-        const float ls = top == -INFINITY ? -INFINITY : top + __builtin_amdgcn_logf(l);
-        const int i = r / a.G, h = hk * a.G + r % a.G;
-        if (a.nsplit > 1) {
-            const int64_t at = ((int64_t)split * a.nbh + bh) * a.nrow + r;
-            a.part[at * a.D + d] = o;
-            if (d == 0) a.part_lse[at] = ls;
-        } else {
-            IO::store((E*)a.o + b * a.os[0] + (int64_t)i * a.os[1] + h * a.os[2], d, o);
-            if (a.lse && d == 0) a.lse[((int64_t)b * a.H + h) * a.Lq + i] = ls * LN2;
-        }
-    }
-}
-
 // Joins the splits of a row: o = sum_s 2^(lse_s - lse) o_s.  One workgroup per row: lane s weighs
 // split s (at most 64), then each wave sums a quarter of the splits for 64 columns at a time.
 template <class IO>
@@ -505,74 +300,77 @@ __global__ __launch_bounds__(NT) void attn_join(AttnArgs a)
         a.lse[((int64_t)b * a.H + h) * a.Lq + i] = sum > 0.f ? (mx + __builtin_amdgcn_logf(sum)) * LN2 : -INFINITY;
 }
 
-#ifndef FEWFILL
-#define FEWFILL 1024
+// Rows of a workgroup: 16 (one wave) for the few rows of decoding; 64 where 128 would give fewer
+// workgroups than ENOUGH.
+constexpr int FEW = 16;
+#ifndef FENOUGH
+#define FENOUGH 256
 #endif
-// Rows of a key head up to this go to attn_few.
-constexpr int FEW = 8;
-// Key splits: as many as fill the GPU when the rows alone do not, each of at least 256 keys.
+constexpr int64_t ENOUGH = FENOUGH;
+int tile_rows(const AttnArgs& a)
+{
+    if (a.nrow <= FEW) return 16;
+    return (a.nrow + 127) / 128 * (int64_t)a.nbh < ENOUGH ? 64 : 128;
+}
+
+// Key splits: as many as fill the GPU when the rows alone do not, each of at least SPLIT_MIN keys.
+#ifndef FEWFILL
+#define FEWFILL 1280
+#endif
+#ifndef SPMIN
+#define SPMIN 256
+#endif
 constexpr int64_t FILL = 512, FILL_FEW = FEWFILL;
-constexpr int64_t SPLIT_MIN = 256;
+constexpr int64_t SPLIT_MIN = SPMIN;
 constexpr int64_t SPLIT_MAX = 64;   // attn_join weighs one split a lane
 
 int splits(const AttnArgs& a)
 {
-    const bool few = a.nrow <= FEW;
-    const int64_t wgs = (few ? 1 : (a.nrow + BM - 1) / BM) * (int64_t)a.nbh, fill = few ? FILL_FEW : FILL;
-    const int64_t keys = std::min<int64_t>(a.Lk, (int64_t)a.window + std::min<int64_t>(a.Lq, BM));
+    const int bm = tile_rows(a);
+    const int64_t wgs = (a.nrow + bm - 1) / bm * (int64_t)a.nbh, fill = a.nrow <= FEW ? FILL_FEW : FILL;
+    const int64_t keys = std::min<int64_t>(a.Lk, (int64_t)a.window + std::min<int64_t>(a.Lq, bm));
     if (wgs <= 0 || 2 * wgs > fill) return 1;
     return (int)std::max<int64_t>(1, std::min<int64_t>({(fill + wgs - 1) / wgs, keys / SPLIT_MIN, SPLIT_MAX}));
 }
 
-template <class IO, int DP, bool CAP, bool BIAS>
-hipError_t go(const AttnArgs& a, int64_t blocks, hipStream_t st)
+template <class IO, int DP, bool CAP, bool BIAS, class S>
+hipError_t go(const AttnArgs& a, hipStream_t st)
 {
-    constexpr int threads = 64 * fwd_waves<IO, DP>;
-    if (!grid_ok(blocks, threads)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((attn_fwd<IO, DP, CAP, BIAS>), dim3((unsigned)blocks), dim3(threads), 0, st, a);
+    const int64_t blocks = (int64_t)a.ntile * a.nbh * a.nsplit;
+    if (!grid_ok(blocks, 64 * S::NW)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((attn_fwd<IO, DP, CAP, BIAS, S>), dim3((unsigned)blocks), dim3(64 * S::NW), 0, st, a);
     return hipGetLastError();
+}
+
+template <class IO, int DP, class S>
+hipError_t pick(AttnArgs a, hipStream_t st)
+{
+    a.ntile = (a.nrow + S::BM - 1) / S::BM;
+    if (a.cap > 0.f)
+        return a.slopes ? go<IO, DP, true, true, S>(a, st) : go<IO, DP, true, false, S>(a, st);
+    return a.slopes ? go<IO, DP, false, true, S>(a, st) : go<IO, DP, false, false, S>(a, st);
 }
 
 template <class IO, int DP>
-hipError_t pick(const AttnArgs& a, int64_t blocks, hipStream_t st)
+hipError_t shape(const AttnArgs& a, hipStream_t st)
 {
-    if (a.cap > 0.f)
-        return a.slopes ? go<IO, DP, true, true>(a, blocks, st) : go<IO, DP, true, false>(a, blocks, st);
-    return a.slopes ? go<IO, DP, false, true>(a, blocks, st) : go<IO, DP, false, false>(a, blocks, st);
-}
-
-template <class IO, int LPK, int RT>
-hipError_t few(const AttnArgs& a, int64_t blocks, hipStream_t st)
-{
-    if (a.cap > 0.f)
-        hipLaunchKernelGGL((attn_few<IO, LPK, RT, true>), dim3((unsigned)blocks), dim3(NT), 0, st, a);
-    else
-        hipLaunchKernelGGL((attn_few<IO, LPK, RT, false>), dim3((unsigned)blocks), dim3(NT), 0, st, a);
-    return hipGetLastError();
-}
-
-template <class IO, int LPK>
-hipError_t few_rows(const AttnArgs& a, int64_t blocks, hipStream_t st)
-{
-    return a.nrow == 1   ? few<IO, LPK, 1>(a, blocks, st)
-           : a.nrow == 2 ? few<IO, LPK, 2>(a, blocks, st)
-           : a.nrow <= 4 ? few<IO, LPK, 4>(a, blocks, st)
-                         : few<IO, LPK, 8>(a, blocks, st);
+    constexpr int BN = stage_rows<IO, DP>;
+    switch (tile_rows(a)) {
+    case 16: return pick<IO, DP, Shape<1, 1, 32>>(a, st);
+    case 64: return pick<IO, DP, Shape<1, 4, BN>>(a, st);
+    default: break;
+    }
+    // float32: one block a wave (the score tile and its operands take twice the registers)
+    constexpr int NQ = IO::SIZE == 4 ? 1 : 2;
+    return pick<IO, DP, Shape<NQ, 8 / NQ, BN>>(a, st);
 }
 
 template <class IO>
 hipError_t run(AttnArgs a, hipStream_t st)
 {
-    constexpr int LPK = 64 / vec_elems<IO>;   // lanes of a key of 64
-    const bool is_few = a.nrow <= FEW;
-    a.ntile = is_few ? 1 : (a.nrow + BM - 1) / BM;
     a.nsplit = splits(a);
-    const int64_t blocks = (int64_t)a.ntile * a.nbh * a.nsplit;
-    if (!grid_ok(blocks, NT)) return hipErrorInvalidValue;
     a.part_lse = a.part + (int64_t)a.nsplit * a.nbh * a.nrow * a.D;
-    hipError_t e;
-    if (is_few) e = a.D <= 64 ? few_rows<IO, LPK>(a, blocks, st) : few_rows<IO, 2 * LPK>(a, blocks, st);
-    else e = a.D <= 64 ? pick<IO, 64>(a, blocks, st) : pick<IO, 128>(a, blocks, st);
+    const hipError_t e = a.D <= 64 ? shape<IO, 64>(a, st) : shape<IO, 128>(a, st);
     if (e != hipSuccess || a.nsplit == 1) return e;
     const int64_t rows = (int64_t)a.nbh * a.nrow;
     if (!grid_ok(rows, NT)) return hipErrorInvalidValue;

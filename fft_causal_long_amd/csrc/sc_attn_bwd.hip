@@ -31,33 +31,20 @@ namespace {
 using namespace attn;
 
 constexpr int STRIP = 32;     // tokens of a strip (half a stage, or a stage)
-constexpr int BM = 128;       // tokens of a workgroup of attn_bwd_q
 
-#ifndef QNQ
-#define QNQ(DP, SZ) (SZ == 4 ? 1 : 2)
-#endif
-#ifndef KNK
-#define KNK(DP, SZ) (SZ == 4 ? 1 : 2)
-#endif
-#ifndef KNW
-#define KNW(DP, SZ) (SZ == 4 ? 8 : 4)
-#endif
+// A workgroup's shape: N 16-row blocks a wave (tokens in attn_bwd_q, keys in attn_bwd_kv), NW waves.
+template <int N_, int NW_>
+struct Shape {
+    static constexpr int N = N_, NW = NW_, W = 16 * N, ROWS = NW * W;   // rows of a wave, of a workgroup
+};
+
+// waves a SIMD the kernels are compiled for
 #ifndef BQV
 #define BQV(DP, SZ) (SZ == 4 ? 2 : DP == 64 ? 3 : 2)
 #endif
 #ifndef BKV
 #define BKV(DP, SZ) (SZ == 4 ? 2 : DP == 64 ? 2 : 1)
 #endif
-// 16-row blocks of a wave of attn_bwd_q, and its waves; 16-key blocks of a wave of attn_bwd_kv,
-// and its waves
-template <class IO, int DP>
-constexpr int q_blocks = QNQ(DP, IO::SIZE);
-template <class IO, int DP>
-constexpr int q_waves = BM / 16 / q_blocks<IO, DP>;
-template <class IO, int DP>
-constexpr int kv_blocks = KNK(DP, IO::SIZE);
-template <class IO, int DP>
-constexpr int kv_waves = KNW(DP, IO::SIZE);
 
 // The score in base 2 of the raw product y plus `add`; dcap: the factor of dS that the cap adds.
 template <class IO, bool CAP>
@@ -72,13 +59,13 @@ __device__ __forceinline__ float score2(float y, float scale2, float cap2, float
     }
 }
 
-template <class IO, int DP, bool CAP, bool BIAS>
-__global__ __launch_bounds__((64 * q_waves<IO, DP>), BQV(DP, IO::SIZE)) void attn_bwd_q(AttnArgs a)
+template <class IO, int DP, bool CAP, bool BIAS, class S>
+__global__ __launch_bounds__((64 * S::NW), BQV(DP, IO::SIZE)) void attn_bwd_q(AttnArgs a)
 {
     using E = typename IO::T;
-    constexpr int NQ = q_blocks<IO, DP>, NW = q_waves<IO, DP>, WM = 16 * NQ;   // WM: tokens of a wave
+    constexpr int NQ = S::N, NW = S::NW, WM = S::W, BM = S::ROWS;
     using R = Ring<IO, DP, 64 * NW>;
-    constexpr int V = vec_elems<IO>, KK = DP / 32, ND = DP / 16, BN = R::BN;
+    constexpr int V = vec_elems<IO>, KK = DP / 32, ND = DP / 16, BN = stage_rows<IO, DP>;
     __shared__ __attribute__((aligned(1024))) typename R::Shared sh;
     __shared__ int4 range[NW];
 
@@ -152,7 +139,7 @@ __global__ __launch_bounds__((64 * q_waves<IO, DP>), BQV(DP, IO::SIZE)) void att
                 const int4 y = range[tid * per + per - 1];
                 x = make_int4(min(x.x, y.x), max(x.y, y.y), max(x.z, y.z), min(x.w, y.w));
             }
-            a.strips[((int64_t)b * a.ntile + tile) * (BM / STRIP) + tid] = x;
+            a.strips[(int64_t)b * a.nstrip + tile * (BM / STRIP) + tid] = x;
         }
     } else {
         const RowRange all = token_range(a, n, tile * BM, BM);
@@ -276,19 +263,21 @@ __global__ __launch_bounds__((64 * q_waves<IO, DP>), BQV(DP, IO::SIZE)) void att
     }
 }
 
-template <class IO, int DP, bool CAP, bool BIAS>
-__global__ __launch_bounds__((64 * kv_waves<IO, DP>), BKV(DP, IO::SIZE)) void attn_bwd_kv(AttnArgs a)
+template <class IO, int DP, bool CAP, bool BIAS, class S>
+__global__ __launch_bounds__((64 * S::NW), BKV(DP, IO::SIZE)) void attn_bwd_kv(AttnArgs a)
 {
     using E = typename IO::T;
-    constexpr int NW = kv_waves<IO, DP>, NK = kv_blocks<IO, DP>, WK = 16 * NK, BK = NW * WK;
+    constexpr int NW = S::NW, NK = S::N, WK = S::W, BK = S::ROWS;
     using R = Ring<IO, DP, 64 * NW>;
-    constexpr int KK = DP / 32, ND = DP / 16, BN = R::BN, SP = BN / STRIP;   // tokens and strips of a stage
+    constexpr int KK = DP / 32, ND = DP / 16, BN = stage_rows<IO, DP>, SP = BN / STRIP;   // tokens and strips of a stage
     __shared__ __attribute__((aligned(1024))) typename R::Shared sh;
     __shared__ __attribute__((aligned(16))) int first[NW][BN], span[NW][BN];   // each wave its own copy
 
     uint32_t id = blockIdx.x;
     const int bh = (int)(id % (uint32_t)a.nbh);
-    const int kt = (int)(id / (uint32_t)a.nbh);   // the first keys are seen by most rows: first
+    id /= (uint32_t)a.nbh;
+    const int part = (int)(id % (uint32_t)a.nparts), kt = (int)(id / (uint32_t)a.nparts);   // the first keys are
+                                                                                      // seen by most rows: first
     const int b = bh / a.Hkv, hk = bh % a.Hkv;
     const int n = seq_len(a, b);
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c = lane & 15;
@@ -334,7 +323,7 @@ __global__ __launch_bounds__((64 * kv_waves<IO, DP>), BKV(DP, IO::SIZE)) void at
             s1 = (int)((phi - off) / BN + 1);
         }
     }
-    const int4* strips = a.strips + (int64_t)b * a.ntile * (BM / STRIP);
+    const int4* strips = a.strips + (int64_t)b * a.nstrip;
     // With documents: which of 64 stages from sbase on see this workgroup's keys, and which of their
     // strips this wave's (hit) and every key of them (full), read together so that the walk itself
     // waits for no load of its own.
@@ -372,7 +361,8 @@ __global__ __launch_bounds__((64 * kv_waves<IO, DP>), BKV(DP, IO::SIZE)) void at
 
     const int32_t* doc = a.doc ? a.doc + (int64_t)b * a.Lk : nullptr;
     R ring(sh, a.Lq, a.D, a.qs[1], a.dos[1]);
-    for (int h = hk * a.G; h < (hk + 1) * a.G; ++h) {
+    const int per = (a.G + a.nparts - 1) / a.nparts;   // heads of a part
+    for (int h = hk * a.G + part * per; h < hk * a.G + min((part + 1) * per, a.G); ++h) {
         ring.from((const E*)a.q + b * a.qs[0] + h * a.qs[2], (const E*)a.dout + b * a.dos[0] + h * a.dos[2]);
         const float* stat = a.rowstat + ((int64_t)b * a.H + h) * a.Lq;
         ring.wp[0] = (const uint32_t*)stat;
@@ -513,6 +503,17 @@ __global__ __launch_bounds__((64 * kv_waves<IO, DP>), BKV(DP, IO::SIZE)) void at
     for (int m = 0; m < NK; ++m) {
         const int j = jw + 16 * m + c;
         if (j >= a.Lk) continue;
+        if (a.nparts > 1) {
+            float* p = a.part + (((int64_t)part * a.nbh + bh) * a.Lk + j) * 2 * a.D;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                const int x = 16 * d + 4 * g;
+                if (x >= a.D) continue;
+                *(f32x4*)(p + x) = dk[d][m] * a.scale;
+                *(f32x4*)(p + a.D + x) = dv[d][m];
+            }
+            continue;
+        }
         E* kp = (E*)a.dk + b * a.dks[0] + (int64_t)j * a.dks[1] + hk * a.dks[2];
         E* vp = (E*)a.dv + b * a.dvs[0] + (int64_t)j * a.dvs[1] + hk * a.dvs[2];
 #pragma unroll
@@ -525,20 +526,77 @@ __global__ __launch_bounds__((64 * kv_waves<IO, DP>), BKV(DP, IO::SIZE)) void at
     }
 }
 
+// dk, dv of a key as the sum of its parts, in order; four values a thread.
+template <class IO>
+__global__ __launch_bounds__(256) void attn_bwd_join(AttnArgs a, int64_t n)
+{
+    using E = typename IO::T;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    const int per = 2 * a.D / 4;   // threads of a key
+    const int64_t row = i / per;
+    const int x = (int)(i % per) * 4;
+    f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int p = 0; p < a.nparts; ++p)
+        sum += *(const f32x4*)(a.part + (((int64_t)p * a.nbh * a.Lk) + row) * 2 * a.D + x);
+    const int bh = (int)(row / a.Lk), j = (int)(row % a.Lk), b = bh / a.Hkv, hk = bh % a.Hkv;
+    E* o = x < a.D ? (E*)a.dk + b * a.dks[0] + (int64_t)j * a.dks[1] + hk * a.dks[2] + x
+                   : (E*)a.dv + b * a.dvs[0] + (int64_t)j * a.dvs[1] + hk * a.dvs[2] + x - a.D;
+    put4<IO>(o, sum);
+}
+
+template <class IO, int DP, bool CAP, bool BIAS, class S>
+hipError_t go_q(AttnArgs a, hipStream_t st)
+{
+    a.ntile = (a.Lq + S::ROWS - 1) / S::ROWS;
+    const int64_t blocks = (int64_t)a.ntile * a.B * a.H;
+    if (!grid_ok(blocks, 64 * S::NW)) return hipErrorInvalidValue;
+    if (blocks == 0) return hipSuccess;
+    hipLaunchKernelGGL((attn_bwd_q<IO, DP, CAP, BIAS, S>), dim3((unsigned)blocks), dim3(64 * S::NW), 0, st, a);
+    return hipGetLastError();
+}
+
+template <class IO, int DP, bool CAP, bool BIAS, class S>
+hipError_t go_kv(const AttnArgs& a, hipStream_t st)
+{
+    const int64_t blocks = (int64_t)((a.Lk + S::ROWS - 1) / S::ROWS) * a.nbh * a.nparts;
+    if (!grid_ok(blocks, 64 * S::NW)) return hipErrorInvalidValue;
+    if (blocks == 0) return hipSuccess;
+    hipLaunchKernelGGL((attn_bwd_kv<IO, DP, CAP, BIAS, S>), dim3((unsigned)blocks), dim3(64 * S::NW), 0, st, a);
+    return hipGetLastError();
+}
+
+// Workgroups of 128 rows or keys below which they take 64; and workgroups below which the heads
+// that share a key head are dealt out to several, whose parts a third kernel adds.
+#ifndef PENOUGH
+#define PENOUGH 1024
+#endif
+constexpr int64_t ENOUGH = 512, PARTS_FILL = PENOUGH;
+
+bool few(int64_t L, int64_t heads) { return (L + 127) / 128 * heads < ENOUGH; }
+
+int parts(const AttnArgs& a)
+{
+    const int64_t bk = few(a.Lk, a.nbh) ? 64 : 128, wgs = (a.Lk + bk - 1) / bk * a.nbh;
+    if (a.G == 1 || wgs == 0 || wgs >= PARTS_FILL || a.Lq == 0) return 1;
+    const int64_t want = std::min<int64_t>(a.G, (PARTS_FILL + wgs - 1) / wgs);
+    const int64_t per = (a.G + want - 1) / want;   // heads of a part
+    return (int)((a.G + per - 1) / per);
+}
+
 template <class IO, int DP, bool CAP, bool BIAS>
 hipError_t go(const AttnArgs& a, hipStream_t st)
 {
-    constexpr int BK = 16 * kv_blocks<IO, DP> * kv_waves<IO, DP>;
-    constexpr int qt = 64 * q_waves<IO, DP>, kt = 64 * kv_waves<IO, DP>;
-    const int64_t qb = (int64_t)a.ntile * a.B * a.H, kb = (int64_t)((a.Lk + BK - 1) / BK) * a.nbh;
-    if (!grid_ok(qb, qt) || !grid_ok(kb, kt)) return hipErrorInvalidValue;
-    if (qb > 0) {
-        hipLaunchKernelGGL((attn_bwd_q<IO, DP, CAP, BIAS>), dim3((unsigned)qb), dim3(qt), 0, st, a);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    if (kb == 0) return hipSuccess;
-    hipLaunchKernelGGL((attn_bwd_kv<IO, DP, CAP, BIAS>), dim3((unsigned)kb), dim3(kt), 0, st, a);
+    // float32: one block a wave (operands and results take twice the registers)
+    constexpr int N = IO::SIZE == 4 ? 1 : 2;
+    hipError_t e = few(a.Lq, (int64_t)a.B * a.H) ? go_q<IO, DP, CAP, BIAS, Shape<1, 4>>(a, st)
+                                                 : go_q<IO, DP, CAP, BIAS, Shape<N, 8 / N>>(a, st);
+    if (e != hipSuccess) return e;
+    e = few(a.Lk, a.nbh) ? go_kv<IO, DP, CAP, BIAS, Shape<1, 4>>(a, st) : go_kv<IO, DP, CAP, BIAS, Shape<N, 8 / N>>(a, st);
+    if (e != hipSuccess || a.nparts == 1) return e;
+    const int64_t n = (int64_t)a.nbh * a.Lk * (2 * a.D / 4), blocks = (n + 255) / 256;
+    if (!grid_ok(blocks, 256)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((attn_bwd_join<IO>), dim3((unsigned)blocks), dim3(256), 0, st, a, n);
     return hipGetLastError();
 }
 
@@ -550,21 +608,31 @@ hipError_t pick(const AttnArgs& a, hipStream_t st)
     return a.slopes ? go<IO, DP, false, true>(a, st) : go<IO, DP, false, false>(a, st);
 }
 
+// strips of a batch row, whole tiles of 128 tokens and whole stages
+int64_t strip_count(const AttnArgs& a) { return (a.Lq + 127) / 128 * (int64_t)(128 / STRIP); }
 size_t stat_bytes(const AttnArgs& a) { return ((size_t)a.B * a.H * a.Lq * 2 * sizeof(float) + 255) / 256 * 256; }
+
+size_t strip_bytes(const AttnArgs& a)
+{
+    return a.doc ? ((size_t)(a.B * strip_count(a)) * sizeof(int4) + 255) / 256 * 256 : 0;
+}
 
 }  // namespace
 
 size_t attn_bwd_bytes(const AttnArgs& a)
 {
-    return stat_bytes(a) + (a.doc ? (size_t)a.B * ((a.Lq + BM - 1) / BM) * (BM / STRIP) * sizeof(int4) : 0);
+    const int np = parts(a);
+    return stat_bytes(a) + strip_bytes(a) + (np > 1 ? (size_t)np * a.nbh * a.Lk * 2 * a.D * sizeof(float) : 0);
 }
 
 hipError_t launch_attn_bwd(Store s, const AttnArgs& a, void* ws, hipStream_t st)
 {
     AttnArgs x = a;
-    x.ntile = (a.Lq + BM - 1) / BM;
+    x.nstrip = (int)strip_count(a);
+    x.nparts = parts(a);
     x.rowstat = (float*)ws;
     x.strips = (int4*)((char*)ws + stat_bytes(a));
+    x.part = (float*)((char*)ws + stat_bytes(a) + strip_bytes(a));
     if (s == Store::F32) return a.D <= 64 ? pick<f32_io, 64>(x, st) : pick<f32_io, 128>(x, st);
     return a.D <= 64 ? pick<bf16_io, 64>(x, st) : pick<bf16_io, 128>(x, st);
 }

@@ -318,8 +318,8 @@ struct AttnArgs {
     float scale, cap;        // cap 0: none
     int nrow, nbh;           // packed rows Lq G and key heads B Hkv of the call
     // set by the launchers
-    int ntile, nsplit;
-    float *part, *part_lse;  // forward: the splits' results
+    int ntile, nsplit, nstrip, nparts;
+    float *part, *part_lse;  // forward: the splits' results; backward: the parts of dk and dv
     float* rowstat;          // backward: lse in base 2 of each row (B, H, Lq), then delta
     int4* strips;            // backward with documents: per 32-token strip the lowest and the
                              // highest key seen, the highest first key and the lowest position
