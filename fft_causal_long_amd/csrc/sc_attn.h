@@ -72,15 +72,6 @@ __device__ __forceinline__ Frag<IO> frag_at(const typename IO::T* p)
     return f;
 }
 
-template <class IO>
-__device__ __forceinline__ Frag<IO> frag_zero()
-{
-    Frag<IO> f;
-    if constexpr (IO::SIZE == 2) f.v = make_uint4(0, 0, 0, 0);
-    else f.a = f.b = make_float4(0, 0, 0, 0);
-    return f;
-}
-
 // LDS tiles hold rows of DP elements without padding (asynchronous loads write 1024 contiguous
 // bytes a wave); the 16-byte chunk k of row r sits at chunk k ^ (r & 7), so that the rows that
 // lanes read together lie in different banks.
@@ -128,6 +119,24 @@ __device__ __forceinline__ Frag<IO> frag_tr(const typename IO::T* tile, int r0, 
         f.b = make_float4(x[4], x[5], x[6], x[7]);
     }
     return f;
+}
+
+// A wave's rows, element d on: read without a branch (a column past D reads column 0) so that
+// nothing waits for a mask, and cleared later where they are not wanted.
+template <class IO>
+__device__ __forceinline__ Frag<IO> frag_load(const typename IO::T* row, int d, int D)
+{
+    return frag_at<IO>(row + (d < D ? d : 0));
+}
+template <class IO>
+__device__ __forceinline__ void frag_keep(Frag<IO>& f, bool on)
+{
+    if constexpr (IO::SIZE == 2) {
+        f.v = on ? f.v : make_uint4(0, 0, 0, 0);
+    } else {
+        f.a = on ? f.a : make_float4(0, 0, 0, 0);
+        f.b = on ? f.b : make_float4(0, 0, 0, 0);
+    }
 }
 
 // ---- asynchronous loads from memory into LDS: every lane's 16 (or 4) bytes go to consecutive

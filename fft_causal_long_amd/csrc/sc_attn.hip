@@ -40,11 +40,12 @@ struct Shape {
     static constexpr int NQ = NQ_, NW = NW_, BN = BN_, WM = 16 * NQ, BM = NW * WM;   // rows of a wave, of a workgroup
 };
 
-#ifndef FWV
-#define FWV(DP, SZ, NW) (SZ == 4 ? (NW == 1 ? 1 : 2) : DP == 64 ? 3 : 2)
-#endif
+// Waves a SIMD the kernel is compiled for: as many as its registers allow without spills.
+template <class IO, int DP, class S>
+constexpr int fwd_occupancy = S::NW == 1 ? 1 : IO::SIZE == 2 && DP == 64 ? 3 : 2;
+
 template <class IO, int DP, bool CAP, bool BIAS, class S>
-__global__ __launch_bounds__((64 * S::NW), FWV(DP, IO::SIZE, S::NW)) void attn_fwd(AttnArgs a)
+__global__ __launch_bounds__((64 * S::NW), (fwd_occupancy<IO, DP, S>)) void attn_fwd(AttnArgs a)
 {
     using E = typename IO::T;
     constexpr int NQ = S::NQ, NW = S::NW, WM = S::WM, BM = S::BM, BN = S::BN;
@@ -82,8 +83,7 @@ __global__ __launch_bounds__((64 * S::NW), FWV(DP, IO::SIZE, S::NW)) void attn_f
         const E* qp = (const E*)a.q + b * a.qs[0] + (int64_t)i * a.qs[1] + h * a.qs[2];
 #pragma unroll
         for (int k = 0; k < KK; ++k) {
-            const int d = 32 * k + 8 * g;
-            q[m][k] = !empty[m] && d < a.D ? frag_at<IO>(qp + d) : frag_zero<IO>();
+            q[m][k] = frag_load<IO>(qp, 32 * k + 8 * g, a.D);
         }
     }
     const RowRange rr = a.doc ? lanes_range(lo, pos) : packed_range(a, n, rw, WM);
@@ -126,6 +126,10 @@ __global__ __launch_bounds__((64 * S::NW), FWV(DP, IO::SIZE, S::NW)) void attn_f
     ring.from((const E*)a.k + b * a.ks[0] + hk * a.ks[2], (const E*)a.v + b * a.vs[0] + hk * a.vs[2]);
     if (a.doc) ring.wp[0] = (const uint32_t*)a.doc + (int64_t)b * a.Lk;
     ring.start(t0, t1);
+#pragma unroll
+    for (int m = 0; m < NQ; ++m)
+#pragma unroll
+        for (int k = 0; k < KK; ++k) frag_keep<IO>(q[m][k], !empty[m] && 32 * k + 8 * g < a.D);
     int place = 0;
     for (int t = t0; t < t1; ++t, place = R::after(place)) {
         const int j0 = t * BN;
@@ -303,10 +307,7 @@ __global__ __launch_bounds__(NT) void attn_join(AttnArgs a)
 // Rows of a workgroup: 16 (one wave) for the few rows of decoding; 64 where 128 would give fewer
 // workgroups than ENOUGH.
 constexpr int FEW = 16;
-#ifndef FENOUGH
-#define FENOUGH 256
-#endif
-constexpr int64_t ENOUGH = FENOUGH;
+constexpr int64_t ENOUGH = 256;
 int tile_rows(const AttnArgs& a)
 {
     if (a.nrow <= FEW) return 16;
@@ -314,14 +315,8 @@ int tile_rows(const AttnArgs& a)
 }
 
 // Key splits: as many as fill the GPU when the rows alone do not, each of at least SPLIT_MIN keys.
-#ifndef FEWFILL
-#define FEWFILL 1280
-#endif
-#ifndef SPMIN
-#define SPMIN 256
-#endif
-constexpr int64_t FILL = 512, FILL_FEW = FEWFILL;
-constexpr int64_t SPLIT_MIN = SPMIN;
+constexpr int64_t FILL = 512, FILL_FEW = 1280;
+constexpr int64_t SPLIT_MIN = 256;
 constexpr int64_t SPLIT_MAX = 64;   // attn_join weighs one split a lane
 
 int splits(const AttnArgs& a)

@@ -38,13 +38,11 @@ struct Shape {
     static constexpr int N = N_, NW = NW_, W = 16 * N, ROWS = NW * W;   // rows of a wave, of a workgroup
 };
 
-// waves a SIMD the kernels are compiled for
-#ifndef BQV
-#define BQV(DP, SZ) (SZ == 4 ? 2 : DP == 64 ? 3 : 2)
-#endif
-#ifndef BKV
-#define BKV(DP, SZ) (SZ == 4 ? 2 : DP == 64 ? 2 : 1)
-#endif
+// Waves a SIMD the kernels are compiled for: as many as their registers allow without spills.
+template <class IO, int DP>
+constexpr int q_occupancy = IO::SIZE == 2 && DP == 64 ? 3 : 2;
+template <class IO, int DP>
+constexpr int kv_occupancy = IO::SIZE == 2 && DP == 128 ? 1 : 2;
 
 // The score in base 2 of the raw product y plus `add`; dcap: the factor of dS that the cap adds.
 template <class IO, bool CAP>
@@ -60,7 +58,7 @@ __device__ __forceinline__ float score2(float y, float scale2, float cap2, float
 }
 
 template <class IO, int DP, bool CAP, bool BIAS, class S>
-__global__ __launch_bounds__((64 * S::NW), BQV(DP, IO::SIZE)) void attn_bwd_q(AttnArgs a)
+__global__ __launch_bounds__((64 * S::NW), (q_occupancy<IO, DP>)) void attn_bwd_q(AttnArgs a)
 {
     using E = typename IO::T;
     constexpr int NQ = S::N, NW = S::NW, WM = S::W, BM = S::ROWS;
@@ -80,52 +78,32 @@ __global__ __launch_bounds__((64 * S::NW), BQV(DP, IO::SIZE)) void attn_bwd_q(At
 
     int pos[NQ], lo[NQ];
     bool empty[NQ];
-    Frag<IO> q[NQ][KK], go[NQ][KK];
+    Frag<IO> q[NQ][KK], go[NQ][KK], of[NQ][KK];
     float lse2[NQ], delta[NQ];
     const int rw = tile * BM + wave * WM;
     const float slope = BIAS ? a.slopes[h] * LOG2E : 0.f;
+    // everything the rows need is asked for at once: their place in the documents, and their data
+    // whether or not they turn out to be empty
 #pragma unroll
     for (int m = 0; m < NQ; ++m) {
-        const int t = rw + 16 * m + c;
-        const bool in = t < a.Lq;
-        const int i = in ? t : 0;
-        pos[m] = n - a.Lq + i;
-        lo[m] = in ? first_key(a, b, pos[m], n) : BIG;
-        empty[m] = lo[m] == BIG;
-        // an empty row's weights are 2^-inf = 0
-        lse2[m] = empty[m] ? INFINITY : a.lse[((int64_t)b * a.H + h) * a.Lq + i] * LOG2E;
+        const int i = min(rw + 16 * m + c, a.Lq - 1);
         const E* qp = (const E*)a.q + b * a.qs[0] + (int64_t)i * a.qs[1] + h * a.qs[2];
         const E* gp = (const E*)a.dout + b * a.dos[0] + (int64_t)i * a.dos[1] + h * a.dos[2];
         const E* op = (const E*)a.o + b * a.os[0] + (int64_t)i * a.os[1] + h * a.os[2];
-        float dl = 0.f;
+        lse2[m] = a.lse[((int64_t)b * a.H + h) * a.Lq + i];
 #pragma unroll
         for (int k = 0; k < KK; ++k) {
-            const int d = 32 * k + 8 * g;
-            const bool on = !empty[m] && d < a.D;
-            q[m][k] = on ? frag_at<IO>(qp + d) : frag_zero<IO>();
-            go[m][k] = on ? frag_at<IO>(gp + d) : frag_zero<IO>();
-            const Frag<IO> of = on ? frag_at<IO>(op + d) : frag_zero<IO>();
-            if constexpr (IO::SIZE == 2) {
-                const Lanes<IO> x = widen<IO>(go[m][k].v), y = widen<IO>(of.v);
+            q[m][k] = frag_load<IO>(qp, 32 * k + 8 * g, a.D);
+            go[m][k] = frag_load<IO>(gp, 32 * k + 8 * g, a.D);
+            of[m][k] = frag_load<IO>(op, 32 * k + 8 * g, a.D);
+        }
+    }
 #pragma unroll
-                for (int e = 0; e < V; ++e) dl = __builtin_fmaf(x.x[e], y.x[e], dl);
-            } else {
-                dl = __builtin_fmaf(go[m][k].a.x, of.a.x, dl);
-                dl = __builtin_fmaf(go[m][k].a.y, of.a.y, dl);
-                dl = __builtin_fmaf(go[m][k].a.z, of.a.z, dl);
-                dl = __builtin_fmaf(go[m][k].a.w, of.a.w, dl);
-                dl = __builtin_fmaf(go[m][k].b.x, of.b.x, dl);
-                dl = __builtin_fmaf(go[m][k].b.y, of.b.y, dl);
-                dl = __builtin_fmaf(go[m][k].b.z, of.b.z, dl);
-                dl = __builtin_fmaf(go[m][k].b.w, of.b.w, dl);
-            }
-        }
-        delta[m] = gsum(dl);
-        if (g == 0 && in) {
-            const int64_t at = (int64_t)bh * a.Lq + i;
-            a.rowstat[at] = lse2[m];
-            a.rowstat[(int64_t)nbh * a.Lq + at] = delta[m];
-        }
+    for (int m = 0; m < NQ; ++m) {
+        const int t = rw + 16 * m + c;
+        pos[m] = n - a.Lq + min(t, a.Lq - 1);
+        lo[m] = t < a.Lq ? first_key(a, b, pos[m], n) : BIG;
+        empty[m] = lo[m] == BIG;
     }
     const RowRange rr = a.doc ? lanes_range(lo, pos) : token_range(a, n, rw, WM);
     int klo, khi;
@@ -148,12 +126,6 @@ __global__ __launch_bounds__((64 * S::NW), BQV(DP, IO::SIZE)) void attn_bwd_q(At
     }
     klo = __builtin_amdgcn_readfirstlane(klo);
     khi = __builtin_amdgcn_readfirstlane(khi);
-#pragma unroll
-    for (int m = 0; m < NQ; ++m)
-        if (empty[m]) {
-            lo[m] = 0;
-            pos[m] = BIG;
-        }
     const int t0 = khi < 0 ? 0 : klo / BN, t1 = khi < 0 ? 0 : khi / BN + 1;
 
     const float scale2 = CAP ? a.scale / a.cap : a.scale * LOG2E, cap2 = a.cap * LOG2E;
@@ -167,6 +139,45 @@ __global__ __launch_bounds__((64 * S::NW), BQV(DP, IO::SIZE)) void attn_bwd_q(At
     ring.from((const E*)a.k + b * a.ks[0] + hk * a.ks[2], (const E*)a.v + b * a.vs[0] + hk * a.vs[2]);
     if (a.doc) ring.wp[0] = (const uint32_t*)a.doc + (int64_t)b * a.Lk;
     ring.start(t0, t1);
+#pragma unroll
+    for (int m = 0; m < NQ; ++m) {
+        float dl = 0.f;
+#pragma unroll
+        for (int k = 0; k < KK; ++k) {
+            const bool on = !empty[m] && 32 * k + 8 * g < a.D;
+            frag_keep<IO>(q[m][k], on);
+            frag_keep<IO>(go[m][k], on);
+            frag_keep<IO>(of[m][k], on);
+            if constexpr (IO::SIZE == 2) {
+                const Lanes<IO> x = widen<IO>(go[m][k].v), y = widen<IO>(of[m][k].v);
+#pragma unroll
+                for (int e = 0; e < V; ++e) dl = __builtin_fmaf(x.x[e], y.x[e], dl);
+            } else {
+                const Frag<IO>&x = go[m][k], &y = of[m][k];
+                dl = __builtin_fmaf(x.a.x, y.a.x, dl);
+                dl = __builtin_fmaf(x.a.y, y.a.y, dl);
+                dl = __builtin_fmaf(x.a.z, y.a.z, dl);
+                dl = __builtin_fmaf(x.a.w, y.a.w, dl);
+                dl = __builtin_fmaf(x.b.x, y.b.x, dl);
+                dl = __builtin_fmaf(x.b.y, y.b.y, dl);
+                dl = __builtin_fmaf(x.b.z, y.b.z, dl);
+                dl = __builtin_fmaf(x.b.w, y.b.w, dl);
+            }
+        }
+        delta[m] = gsum(dl);
+        // an empty row's weights are 2^-inf = 0, with nothing masked
+        lse2[m] = empty[m] ? INFINITY : lse2[m] * LOG2E;
+        if (empty[m]) {
+            lo[m] = 0;
+            pos[m] = BIG;
+        }
+        const int t = rw + 16 * m + c;
+        if (g == 0 && t < a.Lq) {
+            const int64_t at = (int64_t)bh * a.Lq + t;
+            a.rowstat[at] = lse2[m];
+            a.rowstat[(int64_t)nbh * a.Lq + at] = delta[m];
+        }
+    }
     int place = 0;
     for (int t = t0; t < t1; ++t, place = R::after(place)) {
         const int j0 = t * BN;
@@ -264,7 +275,7 @@ __global__ __launch_bounds__((64 * S::NW), BQV(DP, IO::SIZE)) void attn_bwd_q(At
 }
 
 template <class IO, int DP, bool CAP, bool BIAS, class S>
-__global__ __launch_bounds__((64 * S::NW), BKV(DP, IO::SIZE)) void attn_bwd_kv(AttnArgs a)
+__global__ __launch_bounds__((64 * S::NW), (kv_occupancy<IO, DP>)) void attn_bwd_kv(AttnArgs a)
 {
     using E = typename IO::T;
     constexpr int NW = S::NW, NK = S::N, WK = S::W, BK = S::ROWS;
@@ -284,26 +295,19 @@ __global__ __launch_bounds__((64 * S::NW), BKV(DP, IO::SIZE)) void attn_bwd_kv(A
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);   // uniform, so that branches on it are
     const int jb = kt * BK, jw = jb + wave * WK;   // first key of the workgroup, of the wave
 
+    // this wave's keys, asked for whether or not they turn out to be padding; cleared below
     Frag<IO> k[NK][KK], v[NK][KK];
-    int key[NK];
-    bool dead = false;
 #pragma unroll
     for (int m = 0; m < NK; ++m) {
-        const int j = jw + 16 * m + c;
-        const bool live = key_live(a, b, j, n);
-        key[m] = live ? j : -1;   // a dead key lies before every row's first
-        dead |= !live;
-        const E* kp = (const E*)a.k + b * a.ks[0] + (int64_t)j * a.ks[1] + hk * a.ks[2];
-        const E* vp = (const E*)a.v + b * a.vs[0] + (int64_t)j * a.vs[1] + hk * a.vs[2];
+        const int64_t j = min(jw + 16 * m + c, a.Lk - 1);
+        const E* kp = (const E*)a.k + b * a.ks[0] + j * a.ks[1] + hk * a.ks[2];
+        const E* vp = (const E*)a.v + b * a.vs[0] + j * a.vs[1] + hk * a.vs[2];
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
-            const int d = 32 * kk + 8 * g;
-            const bool on = live && d < a.D;
-            k[m][kk] = on ? frag_at<IO>(kp + d) : frag_zero<IO>();
-            v[m][kk] = on ? frag_at<IO>(vp + d) : frag_zero<IO>();
+            k[m][kk] = frag_load<IO>(kp, 32 * kk + 8 * g, a.D);
+            v[m][kk] = frag_load<IO>(vp, 32 * kk + 8 * g, a.D);
         }
     }
-    dead = __any(dead);
 
     f32x4 dk[ND][NK], dv[ND][NK];
 #pragma unroll
@@ -361,6 +365,8 @@ __global__ __launch_bounds__((64 * S::NW), BKV(DP, IO::SIZE)) void attn_bwd_kv(A
 
     const int32_t* doc = a.doc ? a.doc + (int64_t)b * a.Lk : nullptr;
     R ring(sh, a.Lq, a.D, a.qs[1], a.dos[1]);
+    int key[NK];
+    bool dead = false;
     const int per = (a.G + a.nparts - 1) / a.nparts;   // heads of a part
     for (int h = hk * a.G + part * per; h < hk * a.G + min((part + 1) * per, a.G); ++h) {
         ring.from((const E*)a.q + b * a.qs[0] + h * a.qs[2], (const E*)a.dout + b * a.dos[0] + h * a.dos[2]);
@@ -377,6 +383,22 @@ __global__ __launch_bounds__((64 * S::NW), BKV(DP, IO::SIZE)) void attn_bwd_kv(A
         int q0 = seek(s0), q1 = q0 < s1 ? seek(q0 + 1) : s1;
         if (R::NS > 1 && q0 < s1) ring.issue(q0, 0);
         if (R::NS > 1 && q1 < s1) ring.issue(q1, 1);
+        if (h == hk * a.G + part * per) {
+            // the keys that are padding read as 0 and lie before every row's first
+#pragma unroll
+            for (int m = 0; m < NK; ++m) {
+                const int j = jw + 16 * m + c;
+                const bool live = key_live(a, b, j, n);
+                key[m] = live ? j : -1;
+                dead |= !live;
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk) {
+                    frag_keep<IO>(k[m][kk], live && 32 * kk + 8 * g < a.D);
+                    frag_keep<IO>(v[m][kk], live && 32 * kk + 8 * g < a.D);
+                }
+            }
+            dead = __any(dead);
+        }
         int place = 0;
         for (; q0 < s1; place = R::after(place)) {
             const int tb = q0 * BN, pb = off + tb, here = q0;
@@ -568,10 +590,7 @@ hipError_t go_kv(const AttnArgs& a, hipStream_t st)
 
 // Workgroups of 128 rows or keys below which they take 64; and workgroups below which the heads
 // that share a key head are dealt out to several, whose parts a third kernel adds.
-#ifndef PENOUGH
-#define PENOUGH 1024
-#endif
-constexpr int64_t ENOUGH = 512, PARTS_FILL = PENOUGH;
+constexpr int64_t ENOUGH = 512, PARTS_FILL = 1024;
 
 bool few(int64_t L, int64_t heads) { return (L + 127) / 128 * heads < ENOUGH; }
 
