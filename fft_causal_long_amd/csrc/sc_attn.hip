@@ -304,17 +304,22 @@ __global__ __launch_bounds__(NT) void attn_join(AttnArgs a)
         a.lse[((int64_t)b * a.H + h) * a.Lq + i] = sum > 0.f ? (mx + __builtin_amdgcn_logf(sum)) * LN2 : -INFINITY;
 }
 
-// Rows of a workgroup: 16 (one wave) for the few rows of decoding; 64 where 128 would give fewer
-// workgroups than ENOUGH.
+// Rows of a workgroup: 16 (one wave) for the few rows of decoding, where waves without rows would
+// only share the loads (8 sequences over caches of 65536 keys, 4 key heads of 64: 88.1 us, 90.9
+// with 64 rows); 64 where 128 would give no more than 512 workgroups, two a CU (12 heads of 64,
+// L 1024: 384 workgroups 23.0 us, 768 of half the rows 17.8; 16 heads of 128, 4 key heads, L 4096:
+// 512 135 us, 1024 112; but 768 29.0 us, 1536 30.5 and 4096 104 us, 8192 111).
 constexpr int FEW = 16;
-constexpr int64_t ENOUGH = 256;
+constexpr int64_t TWO_A_CU = 512;
 int tile_rows(const AttnArgs& a)
 {
     if (a.nrow <= FEW) return 16;
-    return (a.nrow + 127) / 128 * (int64_t)a.nbh < ENOUGH ? 64 : 128;
+    return (a.nrow + 127) / 128 * (int64_t)a.nbh <= TWO_A_CU ? 64 : 128;
 }
 
 // Key splits: as many as fill the GPU when the rows alone do not, each of at least SPLIT_MIN keys.
+// The caches above take 88 us in 1280 parts (40 a sequence and key head), 1544 us unsplit; 768 and
+// 2048 parts are 3% and more slower.  Four sequences of 16384 keys, 2 key heads: 18.7 and 330 us.
 constexpr int64_t FILL = 512, FILL_FEW = 1280;
 constexpr int64_t SPLIT_MIN = 256;
 constexpr int64_t SPLIT_MAX = 64;   // attn_join weighs one split a lane
