@@ -9,14 +9,29 @@
 //
 // One pass over the keys with a running maximum and sum, in base 2.  The heads that share a key
 // head are packed into one row axis (row r = token r / G, head r % G), so a key tile is read
-// once for all of them.  A workgroup takes 128 rows, 32 per wave, and walks tiles of 64 keys
-// staged through LDS with the next tile's loads in flight.  Scores are made transposed
-// (keys x rows): a lane then holds 16 keys of one row per 16-row block, the row's statistics
-// are the lane's own but for two shuffles, and the weights are the B operand of the second
-// product as they stand (sc_attn.h).  A wave skips tiles none of its rows sees and masks only
-// tiles that an edge crosses.
-// What bounds it: with a window of 256 the bytes of q, k, v, o; without one the vector
-// instructions per score (scale, max, exponential, sum, rounding), not the matrix products.
+// once for all of them.  A workgroup takes 16, 64 or 128 rows (tile_rows), 16 or 32 a wave, and
+// walks tiles of 64 keys (32 for float32, heads over 64 and single waves) that asynchronous loads
+// bring into a ring of three LDS places, two tiles ahead.  Scores are made transposed (keys x
+// rows): a lane then holds a quarter of the tile's keys of one row per 16-row block, the row's
+// statistics are the lane's own but for two shuffles, and the weights are the B operand of the
+// second product as they stand (sc_attn.h).  A wave skips tiles none of its rows sees and masks
+// only tiles that an edge crosses.  When the rows do not fill the GPU the keys are split over
+// workgroups, whose parts attn_join adds.
+//
+// Measured (MI355X; a large copy moves 5.4 TB/s, reads alone 6.3, a bfloat16 product of 8192^3
+// reaches 1135 TFLOP/s), bfloat16:
+//  * B 8, L 4096, 16 heads of 64, window 256, bias: 104 us, 2.6 TB/s of q, k, v, o read and written
+//    once, where 51 us would be a copy's rate.  The loads and stores alone take 65 us; the vector
+//    instructions of the scores (scale, bias, edges, maximum, exponential, sum, rounding: 13 each
+//    with what a wave spends outside the tiles) keep a SIMD busy 60% of the time, the matrix
+//    products 16%.
+//  * B 1, L 8192, 16 heads of 128 on 4 key heads, no window: 331 us, 830 TFLOP/s of the products
+//    that the mask leaves: bound by the same vector instructions beside the products.
+//  * 8 sequences over ragged caches of up to 65536, one query, 16 heads of 64 on 4 key heads: 88 us,
+//    4.8 TB/s, 5 us of it the join: bound by the cache's bytes.
+// 32 rows a wave and 4 waves against 16 x 8: 104 and 107 us, 335 and 356; 32 x 8: 161 (fewer
+// workgroups a CU, and they wait for each other's barriers).  float32 takes 16 a wave: the operands
+// are twice as large.
 
 #include <hip/hip_runtime.h>
 

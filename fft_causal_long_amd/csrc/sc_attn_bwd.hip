@@ -7,15 +7,27 @@
 //     dx_ij = dS_ij (1 - tanh^2),   dq_i = scale sum_j dx_ij k_j,   dk_j = scale sum_i dx_ij q_i
 //
 // Two kernels, neither with atomics, so the sums have a fixed order:
-//  * attn_bwd_q: a workgroup owns 128 tokens of one head and walks key tiles; it makes delta on
-//    the way in and leaves (lse, delta) of each row for the second kernel, and with documents
+//  * attn_bwd_q: a workgroup owns 64 or 128 tokens of one head and walks key tiles; it makes delta
+//    on the way in and leaves (lse, delta) of each row for the second kernel, and with documents
 //    the key range of each 32-token strip.
-//  * attn_bwd_kv: a workgroup owns 128 keys of a key head and walks the tokens that see them, all
-//    heads of the group in turn, so the gradients of shared heads are plain sums.
-// Both keep their own side's operands in registers (B operands), stage the other side through
-// LDS with the next stage's loads in flight, and feed the score-shaped products to the next
-// product from registers (sc_attn.h).  Seven products instead of the five of a single kernel
-// that would add dq with atomics.
+//  * attn_bwd_kv: a workgroup owns 64 or 128 keys of a key head and walks the tokens that see them,
+//    all heads of the group in turn (or its part of them), so the gradients of shared heads are
+//    plain sums.
+// Both keep their own side's operands in registers (B operands), bring the other side into an LDS
+// ring by asynchronous loads, and feed the score-shaped products to the next product from
+// registers (sc_attn.h).  Seven products instead of the five of a single kernel that would add dq
+// with atomics.
+//
+// Measured (MI355X; a large copy moves 5.4 TB/s): bfloat16, B 8, L 4096, 16 heads of 64, window
+// 256, bias, documents of about 700: 306 us, 130 of them attn_bwd_q and 179 attn_bwd_kv, where a
+// copy of the tensors takes 102.  The loads and stores alone are 103 and 86 us.  Vector instructions
+// keep a SIMD busy 46 and 34% of the time and the matrix products 14%: what is left are waits, for
+// the first tiles of short walks (6 stages a workgroup) and for the waves that still have work.
+// 16 tokens a wave and 8 waves: 146 us against 135, 32 x 8 187; keys: 16 x 8 180, as 32 x 4, at
+// two waves a SIMD 243, 32 x 8 235; three waves a SIMD spill (552 us in all).
+// float32, B 2, L 1001, 12 heads of 64, cap 30, bias, documents: 136 us (60 and 82).  384 workgroups
+// of 64 rows are one and a half a CU: 0.7 waves a SIMD on average, each alone with its latencies
+// (matrix products 19% of the time, vector instructions 10%).
 
 #include <hip/hip_runtime.h>
 
@@ -588,8 +600,11 @@ hipError_t go_kv(const AttnArgs& a, hipStream_t st)
     return hipGetLastError();
 }
 
-// Workgroups of 128 rows or keys below which they take 64; and workgroups below which the heads
-// that share a key head are dealt out to several, whose parts a third kernel adds.
+// Workgroups of 128 rows or keys below which they take 64 (12 heads of 64, L 1024, bfloat16: 384
+// workgroups 69 us, 768 of half the size 55; 768 83, 1536 84; 4096 and 8192 305 and 307 us); and
+// workgroups below which the heads that share a key head are dealt out to several, whose parts a
+// third kernel adds (B 2, L 1500, 8 heads of 128 on 2: 138 us, 343 in one part; L 2048, 16 heads of
+// 64 on one: 105 and 848; 512 and 2048 instead of 1024 are 4% and more slower).
 constexpr int64_t ENOUGH = 512, PARTS_FILL = 1024;
 
 bool few(int64_t L, int64_t heads) { return (L + 127) / 128 * heads < ENOUGH; }

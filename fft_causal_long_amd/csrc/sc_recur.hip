@@ -22,8 +22,8 @@
 //
 // Measured (MI355X): B 8, L 4096, C 1024 bfloat16 forward 50.6 us (4.0 TB/s of the bytes it
 // cannot do without; a large copy reaches 5.4), backward 111 us (3.6); B 8, L 1024, C 768
-// float32 backward 34 us (4.4); B 1, L 65536, C 1536 float32 forward 437 us, where the fold
-// reads z and u a second time (2.0 GB in all, 4.6 TB/s).  NC, R and the waves were chosen there:
+// float32 backward 34 us (4.4); B 1, L 65536, C 1536 float32 forward 428 us, where the fold
+// reads z and u a second time (2.0 GB in all, 4.7 TB/s); its three kernels take 184, 5 and 242 us.  NC, R and the waves were chosen there:
 // for bfloat16 forward, 2 channels and 8 tokens a lane took 50.6 us, 4 x 8 54.2, 8 x 4 55.2
 // (more shuffles a value); 4 waves a workgroup 61, and loads two tiles ahead 60; for float32
 // 4 x 4 and 2 x 8 are within 2%.
@@ -351,7 +351,8 @@ __global__ __launch_bounds__(64 * NW) void recur_tiles(Args a)
 }
 
 // The segments' pairs chained in walk order (segment nseg-1 first for the backward pass): each
-// pair's first half becomes the state before its segment; the last state goes to s1.
+// pair's first half becomes the state before its segment; the last state goes to s1.  Eight pairs
+// are read at a time, so that their loads overlap.
 __global__ __launch_bounds__(NT) void recur_chain(float* seg, const float* s0, float* s1,
                                                   int64_t n, int C, int nseg, int down)
 {
@@ -359,11 +360,21 @@ __global__ __launch_bounds__(NT) void recur_chain(float* seg, const float* s0, f
     if (i >= n) return;
     const int64_t b = i / C, c = i % C;
     float s = s0 ? s0[i] : 0.f;
-    for (int k = 0; k < nseg; ++k) {
-        float* p = seg + (b * nseg + (down ? nseg - 1 - k : k)) * 2 * C + c;
-        const float fa = p[0], fb = p[C];
-        p[0] = s;
-        s = __builtin_fmaf(fa, s, fb);
+    for (int k0 = 0; k0 < nseg; k0 += 8) {
+        float *p[8], fa[8], fb[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int k = min(k0 + e, nseg - 1);
+            p[e] = seg + (b * nseg + (down ? nseg - 1 - k : k)) * 2 * C + c;
+            fa[e] = p[e][0];
+            fb[e] = p[e][C];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (k0 + e < nseg) {
+                p[e][0] = s;
+                s = __builtin_fmaf(fa[e], s, fb[e]);
+            }
     }
     if (s1) s1[i] = s;
 }
@@ -420,11 +431,13 @@ __global__ __launch_bounds__(64) void recur_walk(Args a, int64_t n, int nvec)
         if (c0 + e < C) a.s1[b * C + c0 + e] = s[e];
 }
 
-// Lengths up to this are walked by single threads.
+// Lengths up to this are walked by single threads: one token of 8 sequences, C 1024, bfloat16, takes
+// 4.4 us and 5.4 by tiles; 32 tokens 17 us and under 11.
 constexpr int64_t WALK_MAX_L = 16;
 // With fewer than ENOUGH workgroups (one per CU) the tokens are cut into segments of at least
-// SEG_MIN tokens, FILL workgroups in all.  The long case: 1024 workgroups 437 us, 512 469, 256
-// 569; the medium case has 256 and takes 50.6 us whole, 97 in two segments.
+// SEG_MIN tokens, FILL workgroups in all.  The long case above: 1024 workgroups 437 us (with a
+// slower chain kernel), 512 469, 256 569, unsplit 719; the first case has 256 and takes 50.6 us whole,
+// 97 in two segments.
 constexpr int64_t ENOUGH = 256, FILL = 1024;
 constexpr int64_t SEG_MIN = 1024;
 
