@@ -73,20 +73,24 @@ __device__ __forceinline__ Frag<IO> frag_at(const typename IO::T* p)
 }
 
 // LDS tiles hold rows of DP elements without padding (asynchronous loads write 1024 contiguous
-// bytes a wave); the 16-byte chunk k of row r sits at chunk k ^ (r & 7), so that the rows that
-// lanes read together lie in different banks.
+// bytes a wave); the 16-byte chunk k of row r sits at chunk k ^ (r mod SW), so that the rows that
+// lanes read together lie in different banks: SW = 8 for rows of 128 bytes, of which two span the
+// banks, 16 for longer ones.
+template <class IO, int DP>
+constexpr int SW = DP * IO::SIZE > 128 ? 16 : 8;
 
-// A operand: row r0 + c, elements 32 k + 8 g .. + 7.  r0 a multiple of 8.
+// A operand: row r0 + c, elements 32 k + 8 g .. + 7.  r0 a multiple of 16.
 template <class IO, int DP>
 __device__ __forceinline__ Frag<IO> frag_row(const typename IO::T* tile, int r0, int k, int g, int c)
 {
     const typename IO::T* row = tile + (r0 + c) * DP;
+    const int x = c & (SW<IO, DP> - 1);
     Frag<IO> f;
     if constexpr (IO::SIZE == 2) {
-        f.v = *(const uint4*)(row + ((4 * k + g) ^ (c & 7)) * 8);
+        f.v = *(const uint4*)(row + ((4 * k + g) ^ x) * 8);
     } else {
-        f.a = *(const float4*)(row + ((8 * k + 2 * g) ^ (c & 7)) * 4);
-        f.b = *(const float4*)(row + ((8 * k + 2 * g + 1) ^ (c & 7)) * 4);
+        f.a = *(const float4*)(row + ((8 * k + 2 * g) ^ x) * 4);
+        f.b = *(const float4*)(row + ((8 * k + 2 * g + 1) ^ x) * 4);
     }
     return f;
 }
@@ -100,7 +104,7 @@ __device__ __forceinline__ Frag<IO> frag_tr(const typename IO::T* tile, int r0, 
     if constexpr (IO::SIZE == 2) {
         // lane c of a 16-lane group addresses row c / 4, columns 4 (c % 4) .. + 3, and receives
         // column c of the group's four rows
-        const int r = 4 * g + (c >> 2), k = (d0 / 8 + ((c & 3) >> 1)) ^ (r & 7);
+        const int r = 4 * g + (c >> 2), k = (d0 / 8 + ((c & 3) >> 1)) ^ (r & (SW<IO, DP> - 1));
         const uint16_t* p = tile + (r0 + r) * DP + 8 * k + 4 * (c & 1);
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
         const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 16 * DP));
@@ -110,7 +114,7 @@ __device__ __forceinline__ Frag<IO> frag_tr(const typename IO::T* tile, int r0, 
         float x[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int r = 4 * g + e, k = (d0 / 4 + (c >> 2)) ^ (r & 7);
+            const int r = 4 * g + e, k = (d0 / 4 + (c >> 2)) ^ (r & (SW<IO, DP> - 1));
             const float* p = tile + (r0 + r) * DP + 4 * k + (c & 3);
             x[e] = p[0];
             x[4 + e] = p[16 * DP];
@@ -324,7 +328,7 @@ struct Ring {
     static constexpr int NCH = BN * CH / NT, TILE = BN * DP;   // loads a thread and tensor; elements
     static_assert(BN * CH % NT == 0, "whole rounds of loads");
     static constexpr int RPR = NT / CH;                        // rows of a round of loads
-    static constexpr int NCOL = RPR >= 8 ? 1 : 8 / RPR;        // rounds until a thread's row repeats mod 8
+    static constexpr int NCOL = RPR >= SW<IO, DP> ? 1 : SW<IO, DP> / RPR;   // rounds until its row repeats mod SW
     struct Shared {
         E x[NS][TILE], y[NS][TILE];
         uint32_t w[3][NS][64];   // a wave writes 64 of them, whatever BN
@@ -345,7 +349,7 @@ struct Ring {
         // zeros of the other operand, or results that are not stored)
 #pragma unroll
         for (int i = 0; i < NCOL; ++i) {
-            const int d = (((int)threadIdx.x % CH) ^ ((r0 + RPR * i) & 7)) * V;
+            const int d = (((int)threadIdx.x % CH) ^ ((r0 + RPR * i) & (SW<IO, DP> - 1))) * V;
             col[i] = d < D ? d : 0;
         }
     }
