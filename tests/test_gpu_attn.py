@@ -207,3 +207,28 @@ def test_empty(sc):
     assert o.shape == e.shape
     _, dk, dv = sc.causal_attention_bwd(e, e, q, q, o, lse)
     assert not dk.any() and not dv.any()
+
+
+# enough heads for the workgroups of 128 rows and keys, which fewer never reach
+MANY = [dict(L=200, H=16, Hkv=16, D=64, window=70, bias=True),
+        dict(L=200, H=16, Hkv=16, D=40, docs=50, pad=3, bias=True),
+        dict(L=129, H=32, Hkv=16, D=128, cap=5.0),
+        dict(L=160, H=32, Hkv=16, D=64, cap=5.0, docs=60, window=90, bias=True),
+        dict(L=190, H=16, Hkv=16, D=96)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", MANY, ids=lambda c: "L%d-H%d-D%d" % (c["L"], c["H"], c["D"]))
+def test_many_heads(sc, dtype, case):
+    print("case attn many heads %s %s" % (dtype, case), flush=True)
+    c = dict(case)
+    L = c.pop("L")
+    run(sc, 40, L, L, c.pop("H"), c.pop("Hkv"), c.pop("D"), dtype, **c)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_heads_over_a_cache(sc, dtype, D):
+    print("case attn many heads cache %s D=%d" % (dtype, D), flush=True)
+    kv_len = [(37 * b) % 300 for b in range(40)]   # also rows of length 0 and shorter than the queries
+    run(sc, 40, 140, 299, 16, 16, D, dtype, kv_len=kv_len, window=120, bias=True)
