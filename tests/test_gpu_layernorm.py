@@ -134,3 +134,11 @@ def test_workspace_and_stream(sc):
     assert all(torch.equal(p, q) for p, q in zip(a, b))
     with pytest.raises(sc.SpecConvError):
         sc.layer_norm_bwd(dy, x, mean, rstd, workspace=ws[:n - 256])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,C", [(9001, 64), (8300, 61), (2500, 768), (2051, 1001), (700, 5000), (530, 4099),
+                                    (150, 16384)])
+def test_more_rows_than_workgroups(sc, dtype, rows, C):
+    # backward workgroups that take several rows, and their shares of dw and db
+    test_both_directions(sc, dtype, rows, C)
