@@ -22,7 +22,8 @@
 // 32768 x 2048 bfloat16 57 us (4.7); 8 x 768 bfloat16, one decoding step, 3.5 us, less than a
 // launch costs.  Backward, 32768 x 1024 bfloat16, 39 us with the sums of dw and db (5.2).  Rows of
 // 16384 float32, read twice: forward 2048 of them 90 us (3.0), backward 160 us (2.5).  Rows that are
-// not whole vectors (C = 1023) go element by element: 32768 bfloat16 rows forward 121 us (1.1).
+// not whole vectors go element by element: 16384 of 767 float32 forward 19 us (5.3) and backward 36
+// (4.2); 32768 of 1023 bfloat16, two bytes a load, 57 (2.3) and 48 (4.2).
 
 #include <hip/hip_runtime.h>
 
@@ -54,6 +55,15 @@ __device__ __forceinline__ float row_sum(float v, float* red)
     return v;
 }
 
+// A thread's columns of its row's vector i: V neighbours, or (rows that are not whole vectors, read
+// element by element) V that lie TPR apart, so that each load of the TPR threads takes TPR neighbours:
+// 16384 rows of 767 float32 take 20 us forward, 48 with neighbours a thread.
+template <int TPR, int V, bool WHOLE>
+struct Columns {
+    static constexpr int STEP = WHOLE ? 1 : TPR;
+    __device__ __forceinline__ static int first(int i, int lt) { return WHOLE ? (i * TPR + lt) * V : i * TPR * V + lt; }
+};
+
 template <class IO, int TPR, int NV, bool WHOLE>
 __global__ __launch_bounds__(NT) void ln_fwd(const typename IO::T* __restrict__ x,
                                              const typename IO::T* __restrict__ w,
@@ -64,15 +74,16 @@ __global__ __launch_bounds__(NT) void ln_fwd(const typename IO::T* __restrict__ 
                                              float eps)
 {
     constexpr int V = vec_elems<IO>, RPB = NT / TPR;
+    using R = Columns<TPR, V, WHOLE>;
     __shared__ float red[2][2][4];   // double-buffered over the row loop
     const int lt = threadIdx.x % TPR;
     const float n = (float)C;
     uint4 wr[NV], br[NV];   // read before the first row's sums, not after them
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPR + lt) * V, cc = c < C ? c : 0;
-        if (w) wr[i] = load_raw<IO, WHOLE>(w, cc, C);
-        if (b) br[i] = load_raw<IO, WHOLE>(b, cc, C);
+        const int c = R::first(i, lt), cc = c < C ? c : 0;
+        if (w) wr[i] = load_raw<IO, WHOLE, R::STEP>(w, cc, C);
+        if (b) br[i] = load_raw<IO, WHOLE, R::STEP>(b, cc, C);
     }
     int buf = 0;
     // every thread of a workgroup makes the same number of turns (the barriers of TPR = 256)
@@ -84,8 +95,8 @@ __global__ __launch_bounds__(NT) void ln_fwd(const typename IO::T* __restrict__ 
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * TPR + lt) * V;
-            const uint4 raw = load_raw<IO, WHOLE>(xr, c < C ? c : 0, C);
+            const int c = R::first(i, lt);
+            const uint4 raw = load_raw<IO, WHOLE, R::STEP>(xr, c < C ? c : 0, C);
             v[i] = widen<IO>(c < C ? raw : make_uint4(0, 0, 0, 0));
 #pragma unroll
             for (int e = 0; e < V; ++e) s += v[i].x[e];
@@ -94,11 +105,11 @@ __global__ __launch_bounds__(NT) void ln_fwd(const typename IO::T* __restrict__ 
         float q = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * TPR + lt) * V;
+            const int c = R::first(i, lt);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 v[i].x[e] -= mu;
-                q += c + e < C ? v[i].x[e] * v[i].x[e] : 0.f;
+                q += c + e * R::STEP < C ? v[i].x[e] * v[i].x[e] : 0.f;
             }
         }
         const float var = row_sum<TPR>(q, red[buf][1]) / n;
@@ -111,7 +122,7 @@ __global__ __launch_bounds__(NT) void ln_fwd(const typename IO::T* __restrict__ 
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * TPR + lt) * V;
+            const int c = R::first(i, lt);
             if (c >= C) continue;
             Lanes<IO> o;
             Lanes<IO> wv, bv;
@@ -123,7 +134,7 @@ __global__ __launch_bounds__(NT) void ln_fwd(const typename IO::T* __restrict__ 
                 if (w) t *= wv.x[e];
                 o.x[e] = b ? t + bv.x[e] : t;
             }
-            store_raw<IO, WHOLE>(y + row * ys, c, C, o);
+            store_raw<IO, WHOLE, R::STEP>(y + row * ys, c, C, o);
         }
     }
 }
@@ -139,6 +150,7 @@ __global__ __launch_bounds__(NT) void ln_bwd(const typename IO::T* __restrict__ 
                                              int64_t dys, int64_t xs, int64_t dxs)
 {
     constexpr int V = vec_elems<IO>, RPB = NT / TPR;
+    using R = Columns<TPR, V, WHOLE>;
     __shared__ float red[2][2][4];
     __shared__ float acc[RPB > 1 ? TPR * NV * V * 2 : 1];
     const int lt = threadIdx.x % TPR, grp = threadIdx.x / TPR;
@@ -146,8 +158,8 @@ __global__ __launch_bounds__(NT) void ln_bwd(const typename IO::T* __restrict__ 
     Lanes<IO> wv[NV], aw[NV], ab[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPR + lt) * V;
-        if (w) wv[i] = widen<IO>(load_raw<IO, WHOLE>(w, c < C ? c : 0, C));
+        const int c = R::first(i, lt);
+        if (w) wv[i] = widen<IO>(load_raw<IO, WHOLE, R::STEP>(w, c < C ? c : 0, C));
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             if (!w) wv[i].x[e] = 1.f;
@@ -162,11 +174,11 @@ __global__ __launch_bounds__(NT) void ln_bwd(const typename IO::T* __restrict__ 
         const int64_t r = row < rows ? row : rows - 1;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * TPR + lt) * V;
+            const int c = R::first(i, lt);
             // past the row or the last row: some valid address, zeroed where dy is used
             const int cc = c < C ? c : 0;
-            nx[i] = load_raw<IO, WHOLE>(x + r * xs, cc, C);
-            ny[i] = load_raw<IO, WHOLE>(dy + r * dys, cc, C);
+            nx[i] = load_raw<IO, WHOLE, R::STEP>(x + r * xs, cc, C);
+            ny[i] = load_raw<IO, WHOLE, R::STEP>(dy + r * dys, cc, C);
         }
         nmu = mean[r];
         nrs = rstd[r];
@@ -178,7 +190,7 @@ __global__ __launch_bounds__(NT) void ln_bwd(const typename IO::T* __restrict__ 
         const float mu = nmu, rs = nrs;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * TPR + lt) * V;
+            const int c = R::first(i, lt);
             xh[i] = widen<IO>(nx[i]);
             g[i] = widen<IO>(row < rows && c < C ? ny[i] : make_uint4(0, 0, 0, 0));
         }
@@ -186,7 +198,7 @@ __global__ __launch_bounds__(NT) void ln_bwd(const typename IO::T* __restrict__ 
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * TPR + lt) * V;
+            const int c = R::first(i, lt);
             if (c < C && row < rows) {
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
@@ -206,12 +218,12 @@ __global__ __launch_bounds__(NT) void ln_bwd(const typename IO::T* __restrict__ 
         if (row >= rows) continue;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * TPR + lt) * V;
+            const int c = R::first(i, lt);
             if (c >= C) continue;
             Lanes<IO> o;
 #pragma unroll
             for (int e = 0; e < V; ++e) o.x[e] = rs * (g[i].x[e] - m1 - xh[i].x[e] * m2);
-            store_raw<IO, WHOLE>(dx + row * dxs, c, C, o);
+            store_raw<IO, WHOLE, R::STEP>(dx + row * dxs, c, C, o);
         }
     }
     if (!part) return;
@@ -221,7 +233,7 @@ __global__ __launch_bounds__(NT) void ln_bwd(const typename IO::T* __restrict__ 
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const int c = (i * TPR + lt) * V + e;
+                const int c = R::first(i, lt) + e * R::STEP;
                 if (c < C) {
                     mine[c] = aw[i].x[e];
                     mine[C + c] = ab[i].x[e];
@@ -237,7 +249,7 @@ __global__ __launch_bounds__(NT) void ln_bwd(const typename IO::T* __restrict__ 
                 for (int i = 0; i < NV; ++i)
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
-                        const int c = (i * TPR + lt) * V + e;
+                        const int c = R::first(i, lt) + e * R::STEP;
                         acc[c] = k ? acc[c] + aw[i].x[e] : aw[i].x[e];
                         acc[W + c] = k ? acc[W + c] + ab[i].x[e] : ab[i].x[e];
                     }
@@ -297,23 +309,24 @@ __global__ __launch_bounds__(NT) void lnl_fwd(const typename IO::T* __restrict__
                                               float eps)
 {
     constexpr int V = vec_elems<IO>;
+    using R = Columns<NT, V, WHOLE>;
     __shared__ float red[2][2][4];
     int buf = 0;
     const float n = (float)C;
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
         const typename IO::T* xr = x + row * xs;
         float s = 0.f;
-        for (int64_t c = threadIdx.x * V; c < C; c += NT * V) {
-            const Lanes<IO> v = widen<IO>(load_raw<IO, WHOLE>(xr, (int)c, C));
+        for (int64_t c = R::first(0, threadIdx.x); c < C; c += NT * V) {
+            const Lanes<IO> v = widen<IO>(load_raw<IO, WHOLE, R::STEP>(xr, (int)c, C));
 #pragma unroll
             for (int e = 0; e < V; ++e) s += v.x[e];
         }
         const float mu = row_sum<NT>(s, red[buf][0]) / n;
         float q = 0.f;
-        for (int64_t c = threadIdx.x * V; c < C; c += NT * V) {
-            const Lanes<IO> v = widen<IO>(load_raw<IO, WHOLE>(xr, (int)c, C));
+        for (int64_t c = R::first(0, threadIdx.x); c < C; c += NT * V) {
+            const Lanes<IO> v = widen<IO>(load_raw<IO, WHOLE, R::STEP>(xr, (int)c, C));
 #pragma unroll
-            for (int e = 0; e < V; ++e) q += c + e < C ? (v.x[e] - mu) * (v.x[e] - mu) : 0.f;
+            for (int e = 0; e < V; ++e) q += c + e * R::STEP < C ? (v.x[e] - mu) * (v.x[e] - mu) : 0.f;
         }
         const float rs = 1.0f / sqrtf(row_sum<NT>(q, red[buf][1]) / n + eps);
         buf ^= 1;
@@ -321,18 +334,18 @@ __global__ __launch_bounds__(NT) void lnl_fwd(const typename IO::T* __restrict__
             if (mean) mean[row] = mu;
             if (rstd) rstd[row] = rs;
         }
-        for (int64_t c = threadIdx.x * V; c < C; c += NT * V) {
-            Lanes<IO> v = widen<IO>(load_raw<IO, WHOLE>(xr, (int)c, C));
+        for (int64_t c = R::first(0, threadIdx.x); c < C; c += NT * V) {
+            Lanes<IO> v = widen<IO>(load_raw<IO, WHOLE, R::STEP>(xr, (int)c, C));
             Lanes<IO> wv, bv;
-            if (w) wv = widen<IO>(load_raw<IO, WHOLE>(w, (int)c, C));
-            if (b) bv = widen<IO>(load_raw<IO, WHOLE>(b, (int)c, C));
+            if (w) wv = widen<IO>(load_raw<IO, WHOLE, R::STEP>(w, (int)c, C));
+            if (b) bv = widen<IO>(load_raw<IO, WHOLE, R::STEP>(b, (int)c, C));
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 float t = (v.x[e] - mu) * rs;
                 if (w) t *= wv.x[e];
                 v.x[e] = b ? t + bv.x[e] : t;
             }
-            store_raw<IO, WHOLE>(y + row * ys, (int)c, C, v);
+            store_raw<IO, WHOLE, R::STEP>(y + row * ys, (int)c, C, v);
         }
     }
 }
@@ -347,16 +360,17 @@ __global__ __launch_bounds__(NT) void lnl_bwd(const typename IO::T* __restrict__
                                               int64_t dys, int64_t xs, int64_t dxs)
 {
     constexpr int V = vec_elems<IO>;
+    using R = Columns<NT, V, WHOLE>;
     __shared__ float red[2][2][4];
     int buf = 0;
     const float n = (float)C;
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
         const float mu = mean[row], rs = rstd[row];
         auto terms = [&](int c, Lanes<IO>& e, Lanes<IO>& xh) {
-            e = widen<IO>(load_raw<IO, WHOLE>(dy + row * dys, c, C));
-            xh = widen<IO>(load_raw<IO, WHOLE>(x + row * xs, c, C));
+            e = widen<IO>(load_raw<IO, WHOLE, R::STEP>(dy + row * dys, c, C));
+            xh = widen<IO>(load_raw<IO, WHOLE, R::STEP>(x + row * xs, c, C));
             Lanes<IO> wv;
-            if (w) wv = widen<IO>(load_raw<IO, WHOLE>(w, c, C));
+            if (w) wv = widen<IO>(load_raw<IO, WHOLE, R::STEP>(w, c, C));
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 xh.x[i] = (xh.x[i] - mu) * rs;
@@ -364,7 +378,7 @@ __global__ __launch_bounds__(NT) void lnl_bwd(const typename IO::T* __restrict__
             }
         };
         float s1 = 0.f, s2 = 0.f;
-        for (int64_t c = threadIdx.x * V; c < C; c += NT * V) {
+        for (int64_t c = R::first(0, threadIdx.x); c < C; c += NT * V) {
             Lanes<IO> e, xh;
             terms((int)c, e, xh);
 #pragma unroll
@@ -376,12 +390,12 @@ __global__ __launch_bounds__(NT) void lnl_bwd(const typename IO::T* __restrict__
         const float m1 = row_sum<NT>(s1, red[buf][0]) / n;
         const float m2 = row_sum<NT>(s2, red[buf][1]) / n;
         buf ^= 1;
-        for (int64_t c = threadIdx.x * V; c < C; c += NT * V) {
+        for (int64_t c = R::first(0, threadIdx.x); c < C; c += NT * V) {
             Lanes<IO> e, xh;
             terms((int)c, e, xh);
 #pragma unroll
             for (int i = 0; i < V; ++i) e.x[i] = rs * (e.x[i] - m1 - xh.x[i] * m2);
-            store_raw<IO, WHOLE>(dx + row * dxs, (int)c, C, e);
+            store_raw<IO, WHOLE, R::STEP>(dx + row * dxs, (int)c, C, e);
         }
     }
 }
@@ -466,8 +480,10 @@ hipError_t fwd(const void* x, const void* w, const void* b, void* y, float* mean
 {
     using E = typename IO::T;
     const RowPlan p = row_plan(C, vec_elems<IO>);
-    // the row loop covers what a grid of this many workgroups leaves
-    const int64_t rpb = NT / p.tpr, blocks = std::min<int64_t>((rows + rpb - 1) / rpb, 1 << 20);
+    // the row loop covers what a grid of this many workgroups leaves; element by element w and b cost
+    // as many loads as a row, so a workgroup then keeps them for several rows (32768 of 1023 bfloat16
+    // 57 us, 70 with a workgroup for each four rows, 66 with 1024 workgroups and 61 with 4096)
+    const int64_t rpb = NT / p.tpr, blocks = std::min<int64_t>((rows + rpb - 1) / rpb, WHOLE ? 1 << 20 : 2048);
     if (p.nv == 0) {
         hipLaunchKernelGGL((lnl_fwd<IO, WHOLE>), dim3((unsigned)blocks), dim3(NT), 0, st, (const E*)x,
                            (const E*)w, (const E*)b, (E*)y, mean, rstd, rows, C, xs, ys, eps);

@@ -60,27 +60,38 @@ __device__ __forceinline__ uint4 narrow(const Lanes<IO>& v)
 // Elements c .. c+V-1 (c < n) of the row p of n elements.  WHOLE: every row starts 16-byte
 // aligned and n is a multiple of V, so the vector is one load; a kernel takes one form or the
 // other, since a choice at each load would make every load wait for the one before.  Otherwise
-// the elements are read one by one, those at n and beyond as 0.
-template <class IO, bool WHOLE>
+// the elements are read one by one, those at n and beyond as 0; STEP apart, so that with STEP lanes
+// beside each other every load takes neighbouring elements.
+template <class IO, bool WHOLE, int STEP = 1>
 __device__ __forceinline__ uint4 load_raw(const typename IO::T* p, int c, int n)
 {
     constexpr int V = vec_elems<IO>;
     if constexpr (WHOLE) {
         return *(const uint4*)(p + c);
     } else {
-        uint32_t w[4] = {0, 0, 0, 0};
+        // each element's own address or the row's last: no branch
+        uint32_t w[4];
+        if constexpr (IO::SIZE == 2) {
+            typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            // the element's own address or the row's last: no branch
-            const int at = c + i < n ? c + i : n - 1;
-            if constexpr (IO::SIZE == 2) w[i / 2] |= (c + i < n ? (uint32_t)p[at] : 0u) << (16 * (i & 1));
-            else w[i] = c + i < n ? __float_as_uint(p[at]) : 0u;
+            for (int i = 0; i < 4; ++i) {
+                const int c0 = c + 2 * i * STEP, c1 = c0 + STEP;
+                const u16x2 v = {p[c0 < n ? c0 : n - 1], p[c1 < n ? c1 : n - 1]};
+                w[i] = __builtin_bit_cast(uint32_t, v) & (c1 < n ? 0xffffffffu : c0 < n ? 0xffffu : 0u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool in = c + i * STEP < n;
+                const float v = p[in ? c + i * STEP : n - 1];
+                w[i] = in ? __float_as_uint(v) : 0u;
+            }
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
-template <class IO, bool WHOLE>
+template <class IO, bool WHOLE, int STEP = 1>
 __device__ __forceinline__ void store_raw(typename IO::T* p, int c, int n, const Lanes<IO>& v)
 {
     constexpr int V = vec_elems<IO>;
@@ -89,7 +100,7 @@ __device__ __forceinline__ void store_raw(typename IO::T* p, int c, int n, const
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (c + i < n) IO::store(p, c + i, v.x[i]);
+            if (c + i * STEP < n) IO::store(p, c + i * STEP, v.x[i]);
     }
 }
 
