@@ -14,6 +14,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "sc_device.h"
 #include "sc_internal.h"
 
@@ -221,27 +223,59 @@ __device__ __forceinline__ void keep_branch() { asm volatile(""); }
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// tanh(y).  1 - 2 / (1 + e^2y) is off by about 1e-7 whatever y: below the rounding of bfloat16
-// weights even times a cap of 100, so 16-bit storage takes it for every y.  float32 storage
-// wants the relative error small too: below 1/2 the odd Taylor series to y^15 (the next term is
-// under 1e-8 of the sum).
+// A kernel's form for the call's cap (cap_of).  tanh(y) as 1 - 2 / (1 + e^2y) is off by up to 4 units
+// of 2^-24 whatever y, and the cap multiplies that.  With SERIES the odd Taylor series takes over near
+// 0, so that the error is relative to tanh(y) everywhere: float32 storage always, below 1/2 and to y^15
+// (the next term is under 1e-8 of the sum), about 7 units in all; 16-bit storage for caps over 64,
+// below 1/8 and to y^5, about 31 units (2e-6).  Smaller caps leave 16-bit storage a score off by no
+// more than 1.5e-5, which its weights, rounded to 2^-8, do not show, and the series costs time and
+// registers: B 8, L 4096, 16 heads of 64, window 256: forward 121 us with it and 117 without, backward
+// 364 and 331; L 8192, 16 heads of 128 on 4: 464 and 434, 1606 and 1526.
+enum Cap { UNCAPPED, CAPPED, SERIES };
+constexpr float SERIES_CAP = 64.f;
 template <class IO>
+constexpr Cap cap_of(float cap)
+{
+    return !(cap > 0.f) ? UNCAPPED : IO::SIZE == 4 || cap > SERIES_CAP ? SERIES : CAPPED;
+}
+
+template <class IO, Cap CAP>
 __device__ __forceinline__ float tanh_of(float y)
 {
     const float t = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + exp2_hw(2.0f * LOG2E * y));
-    if constexpr (IO::SIZE == 2) {
+    if constexpr (CAP != SERIES) {
         return t;
     } else {
         const float z = y * y;
-        float p = -929569.0f / 638512875.0f;
-        p = __builtin_fmaf(p, z, 21844.0f / 6081075.0f);
-        p = __builtin_fmaf(p, z, -1382.0f / 155925.0f);
-        p = __builtin_fmaf(p, z, 62.0f / 2835.0f);
-        p = __builtin_fmaf(p, z, -17.0f / 315.0f);
-        p = __builtin_fmaf(p, z, 2.0f / 15.0f);
-        p = __builtin_fmaf(p, z, -1.0f / 3.0f);
-        return z < 0.25f ? __builtin_fmaf(p * z, y, y) : t;
+        float p;
+        if constexpr (IO::SIZE == 2) {
+            p = __builtin_fmaf(2.0f / 15.0f, z, -1.0f / 3.0f);
+        } else {
+            p = -929569.0f / 638512875.0f;
+            p = __builtin_fmaf(p, z, 21844.0f / 6081075.0f);
+            p = __builtin_fmaf(p, z, -1382.0f / 155925.0f);
+            p = __builtin_fmaf(p, z, 62.0f / 2835.0f);
+            p = __builtin_fmaf(p, z, -17.0f / 315.0f);
+            p = __builtin_fmaf(p, z, 2.0f / 15.0f);
+            p = __builtin_fmaf(p, z, -1.0f / 3.0f);
+        }
+        return z < (IO::SIZE == 2 ? 1.0f / 64.0f : 0.25f) ? __builtin_fmaf(p * z, y, y) : t;
     }
+}
+
+// Calls f(Cap, BIAS) as constants for the call's options.  (float32 has no CAPPED form.)
+template <class IO, class F>
+hipError_t with_options(const AttnArgs& a, F&& f)
+{
+    using std::integral_constant;
+    auto bias = [&](auto cap) { return a.slopes ? f(cap, std::true_type()) : f(cap, std::false_type()); };
+    switch (cap_of<IO>(a.cap)) {
+    case UNCAPPED: return bias(integral_constant<Cap, UNCAPPED>());
+    case SERIES: return bias(integral_constant<Cap, SERIES>());
+    default: break;
+    }
+    if constexpr (IO::SIZE == 2) return bias(integral_constant<Cap, CAPPED>());
+    return hipErrorInvalidValue;
 }
 
 // The batch row's length, and a query row's place in it.

@@ -59,7 +59,7 @@ struct Shape {
 template <class IO, int DP, class S>
 constexpr int fwd_occupancy = S::NW == 1 ? 1 : IO::SIZE == 2 && DP == 64 ? 3 : 2;
 
-template <class IO, int DP, bool CAP, bool BIAS, class S>
+template <class IO, int DP, Cap CAP, bool BIAS, class S>
 __global__ __launch_bounds__((64 * S::NW), (fwd_occupancy<IO, DP, S>)) void attn_fwd(AttnArgs a)
 {
     using E = typename IO::T;
@@ -126,7 +126,7 @@ __global__ __launch_bounds__((64 * S::NW), (fwd_occupancy<IO, DP, S>)) void attn
         t1 = min(t1, t0 + per);
     }
 
-    const float scale2 = CAP ? a.scale / a.cap : a.scale * LOG2E, cap2 = a.cap * LOG2E;
+    const float scale2 = CAP != UNCAPPED ? a.scale / a.cap : a.scale * LOG2E, cap2 = a.cap * LOG2E;
     f32x4 o[ND][NQ];
     float mx[NQ], sum[NQ];
 #pragma unroll
@@ -187,7 +187,7 @@ __global__ __launch_bounds__((64 * S::NW), (fwd_occupancy<IO, DP, S>)) void attn
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float add = BIAS ? __builtin_fmaf(slope[m], (float)(16 * kb + r), shift) : shift;
-                    if constexpr (CAP) s[kb][m][r] = __builtin_fmaf(cap2, tanh_of<IO>(s[kb][m][r] * scale2), add);
+                    if constexpr (CAP != UNCAPPED) s[kb][m][r] = __builtin_fmaf(cap2, tanh_of<IO, CAP>(s[kb][m][r] * scale2), add);
                     else s[kb][m][r] = __builtin_fmaf(s[kb][m][r], scale2, add);
                 }
             if (edge) {
@@ -348,7 +348,7 @@ int splits(const AttnArgs& a)
     return (int)std::max<int64_t>(1, std::min<int64_t>({(fill + wgs - 1) / wgs, keys / SPLIT_MIN, SPLIT_MAX}));
 }
 
-template <class IO, int DP, bool CAP, bool BIAS, class S>
+template <class IO, int DP, Cap CAP, bool BIAS, class S>
 hipError_t go(const AttnArgs& a, hipStream_t st)
 {
     const int64_t blocks = (int64_t)a.ntile * a.nbh * a.nsplit;
@@ -361,9 +361,9 @@ template <class IO, int DP, class S>
 hipError_t pick(AttnArgs a, hipStream_t st)
 {
     a.ntile = (a.nrow + S::BM - 1) / S::BM;
-    if (a.cap > 0.f)
-        return a.slopes ? go<IO, DP, true, true, S>(a, st) : go<IO, DP, true, false, S>(a, st);
-    return a.slopes ? go<IO, DP, false, true, S>(a, st) : go<IO, DP, false, false, S>(a, st);
+    return with_options<IO>(a, [&](auto cap, auto bias) {
+        return go<IO, DP, decltype(cap)::value, decltype(bias)::value, S>(a, st);
+    });
 }
 
 template <class IO, int DP>

@@ -57,11 +57,11 @@ template <class IO, int DP>
 constexpr int kv_occupancy = IO::SIZE == 2 && DP == 128 ? 1 : 2;
 
 // The score in base 2 of the raw product y plus `add`; dcap: the factor of dS that the cap adds.
-template <class IO, bool CAP>
+template <class IO, Cap CAP>
 __device__ __forceinline__ float score2(float y, float scale2, float cap2, float add, float& dcap)
 {
-    if constexpr (CAP) {
-        const float t = tanh_of<IO>(y * scale2);
+    if constexpr (CAP != UNCAPPED) {
+        const float t = tanh_of<IO, CAP>(y * scale2);
         dcap = 1.0f - t * t;
         return __builtin_fmaf(cap2, t, add);
     } else {
@@ -69,7 +69,7 @@ __device__ __forceinline__ float score2(float y, float scale2, float cap2, float
     }
 }
 
-template <class IO, int DP, bool CAP, bool BIAS, class S>
+template <class IO, int DP, Cap CAP, bool BIAS, class S>
 __global__ __launch_bounds__((64 * S::NW), (q_occupancy<IO, DP>)) void attn_bwd_q(AttnArgs a)
 {
     using E = typename IO::T;
@@ -140,7 +140,7 @@ __global__ __launch_bounds__((64 * S::NW), (q_occupancy<IO, DP>)) void attn_bwd_
     khi = __builtin_amdgcn_readfirstlane(khi);
     const int t0 = khi < 0 ? 0 : klo / BN, t1 = khi < 0 ? 0 : khi / BN + 1;
 
-    const float scale2 = CAP ? a.scale / a.cap : a.scale * LOG2E, cap2 = a.cap * LOG2E;
+    const float scale2 = CAP != UNCAPPED ? a.scale / a.cap : a.scale * LOG2E, cap2 = a.cap * LOG2E;
     f32x4 acc[ND][NQ];
 #pragma unroll
     for (int d = 0; d < ND; ++d)
@@ -261,7 +261,7 @@ __global__ __launch_bounds__((64 * S::NW), (q_occupancy<IO, DP>)) void attn_bwd_
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         s[kb][m][r] *= dp[kb][m][r] - delta[m];
-                        if constexpr (CAP) s[kb][m][r] *= cf[kb][r];
+                        if constexpr (CAP != UNCAPPED) s[kb][m][r] *= cf[kb][r];
                     }
                 w[m] = frag_of<IO>(s[0][m], s[1][m]);
             }
@@ -286,7 +286,7 @@ __global__ __launch_bounds__((64 * S::NW), (q_occupancy<IO, DP>)) void attn_bwd_
     }
 }
 
-template <class IO, int DP, bool CAP, bool BIAS, class S>
+template <class IO, int DP, Cap CAP, bool BIAS, class S>
 __global__ __launch_bounds__((64 * S::NW), (kv_occupancy<IO, DP>)) void attn_bwd_kv(AttnArgs a)
 {
     using E = typename IO::T;
@@ -327,7 +327,7 @@ __global__ __launch_bounds__((64 * S::NW), (kv_occupancy<IO, DP>)) void attn_bwd
 #pragma unroll
         for (int m = 0; m < NK; ++m) dk[d][m] = dv[d][m] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const float scale2 = CAP ? a.scale / a.cap : a.scale * LOG2E, cap2 = a.cap * LOG2E;
+    const float scale2 = CAP != UNCAPPED ? a.scale / a.cap : a.scale * LOG2E, cap2 = a.cap * LOG2E;
     const int off = n - a.Lq;   // position of token 0
     // stages of tokens at positions jb .. jb + BK - 1 + window - 1
     int s0 = 0, s1 = 0;
@@ -510,7 +510,7 @@ __global__ __launch_bounds__((64 * S::NW), (kv_occupancy<IO, DP>)) void attn_bwd
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
                             dp[rb][m][r] = w[rb][m][r] * (dp[rb][m][r] - dl[r]);
-                            if constexpr (CAP) dp[rb][m][r] *= cf[r];
+                            if constexpr (CAP != UNCAPPED) dp[rb][m][r] *= cf[r];
                         }
                     }
                 }
@@ -579,7 +579,7 @@ __global__ __launch_bounds__(256) void attn_bwd_join(AttnArgs a, int64_t n)
     put4<IO>(o, sum);
 }
 
-template <class IO, int DP, bool CAP, bool BIAS, class S>
+template <class IO, int DP, Cap CAP, bool BIAS, class S>
 hipError_t go_q(AttnArgs a, hipStream_t st)
 {
     a.ntile = (a.Lq + S::ROWS - 1) / S::ROWS;
@@ -590,7 +590,7 @@ hipError_t go_q(AttnArgs a, hipStream_t st)
     return hipGetLastError();
 }
 
-template <class IO, int DP, bool CAP, bool BIAS, class S>
+template <class IO, int DP, Cap CAP, bool BIAS, class S>
 hipError_t go_kv(const AttnArgs& a, hipStream_t st)
 {
     const int64_t blocks = (int64_t)((a.Lk + S::ROWS - 1) / S::ROWS) * a.nbh * a.nparts;
@@ -618,7 +618,7 @@ int parts(const AttnArgs& a)
     return (int)((a.G + per - 1) / per);
 }
 
-template <class IO, int DP, bool CAP, bool BIAS>
+template <class IO, int DP, Cap CAP, bool BIAS>
 hipError_t go(const AttnArgs& a, hipStream_t st)
 {
     // float32: one block a wave (operands and results take twice the registers)
@@ -637,9 +637,9 @@ hipError_t go(const AttnArgs& a, hipStream_t st)
 template <class IO, int DP>
 hipError_t pick(const AttnArgs& a, hipStream_t st)
 {
-    if (a.cap > 0.f)
-        return a.slopes ? go<IO, DP, true, true>(a, st) : go<IO, DP, true, false>(a, st);
-    return a.slopes ? go<IO, DP, false, true>(a, st) : go<IO, DP, false, false>(a, st);
+    return with_options<IO>(a, [&](auto cap, auto bias) {
+        return go<IO, DP, decltype(cap)::value, decltype(bias)::value>(a, st);
+    });
 }
 
 // strips of a batch row, whole tiles of 128 tokens and whole stages
