@@ -612,7 +612,7 @@ bool few(int64_t L, int64_t heads) { return (L + 127) / 128 * heads < ENOUGH; }
 int parts(const AttnArgs& a)
 {
     const int64_t bk = few(a.Lk, a.nbh) ? 64 : 128, wgs = (a.Lk + bk - 1) / bk * a.nbh;
-    if (a.G == 1 || wgs == 0 || wgs >= PARTS_FILL || a.Lq == 0) return 1;
+    if (a.G <= 1 || wgs == 0 || wgs >= PARTS_FILL || a.Lq == 0) return 1;
     const int64_t want = std::min<int64_t>(a.G, (PARTS_FILL + wgs - 1) / wgs);
     const int64_t per = (a.G + want - 1) / want;   // heads of a part
     return (int)((a.G + per - 1) / per);

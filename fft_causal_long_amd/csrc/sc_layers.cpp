@@ -297,8 +297,9 @@ struct Tensor {
     }
 };
 
-// Shape checks; *args receives everything but the pointers.  *empty: nothing to compute.
-sc_status attn_shape(sc_kind kind, const sc_attn* a, sc::AttnArgs* x, bool* empty)
+// Shape checks; *x receives everything but the pointers.  *empty: no output to write (the backward
+// call without query heads still writes dk and dv).
+sc_status attn_shape(sc_kind kind, const sc_attn* a, bool backward, sc::AttnArgs* x, bool* empty)
 {
     if (!a || !float_kind(kind)) return SC_ERR_INVALID_ARGUMENT;
     if (a->B < 0 || a->Lq < 0 || a->Lk < 0 || a->H < 0 || a->Hkv < 0 || a->D < 0 || a->window < 0)
@@ -307,12 +308,12 @@ sc_status attn_shape(sc_kind kind, const sc_attn* a, sc::AttnArgs* x, bool* empt
         return SC_ERR_INVALID_ARGUMENT;
     if (((uintptr_t)a->slopes | (uintptr_t)a->kv_len | (uintptr_t)a->doc_start) % 4)
         return SC_ERR_INVALID_ARGUMENT;
-    *empty = a->B == 0 || a->H == 0 || a->D == 0;
+    *empty = a->B == 0 || a->D == 0 || (a->H == 0 && (!backward || a->Hkv == 0));
     if (*empty) return SC_OK;
     if (a->Hkv == 0 || a->H % a->Hkv) return SC_ERR_UNSUPPORTED;
     if (a->D % 8 || a->D > 128) return SC_ERR_UNSUPPORTED;
     const int64_t G = a->H / a->Hkv;
-    if (a->Lk > kMaxDim || a->Lq > kMaxDim / G || G > kMaxDim) return SC_ERR_UNSUPPORTED;
+    if (a->Lk > kMaxDim || a->Lq > kMaxDim / std::max<int64_t>(G, 1) || G > kMaxDim) return SC_ERR_UNSUPPORTED;
     if ((__int128)a->B * a->Hkv > (__int128)INT32_MAX) return SC_ERR_UNSUPPORTED;
     *x = sc::AttnArgs{};
     x->B = (int)a->B;
@@ -348,7 +349,7 @@ sc_status attn_run(sc_kind kind, const sc_attn* a, const void* q, const void* k,
 {
     sc::AttnArgs x;
     bool empty;
-    sc_status st = attn_shape(kind, a, &x, &empty);
+    sc_status st = attn_shape(kind, a, false, &x, &empty);
     if (st != SC_OK) return st;
     if (empty || a->Lq == 0) return SC_OK;
     const int64_t es = elt(kind);
@@ -380,22 +381,22 @@ sc_status attn_bwd_run(sc_kind kind, const sc_attn* a, const void* dout, const v
 {
     sc::AttnArgs x;
     bool empty;
-    sc_status st = attn_shape(kind, a, &x, &empty);
+    sc_status st = attn_shape(kind, a, true, &x, &empty);
     if (st != SC_OK) return st;
-    if (empty || (a->Lq == 0 && a->Lk == 0)) return SC_OK;
+    if (empty || ((a->Lq == 0 || a->H == 0) && a->Lk == 0)) return SC_OK;
     const int64_t es = elt(kind);
     const Tensor tq{q, a->q, a->B, a->Lq, a->H, a->D, es}, to{o, a->o, a->B, a->Lq, a->H, a->D, es};
     const Tensor tg{dout, a->dout, a->B, a->Lq, a->H, a->D, es}, tdq{dq, a->dq, a->B, a->Lq, a->H, a->D, es};
     const Tensor tk{k, a->k, a->B, a->Lk, a->Hkv, a->D, es}, tv{v, a->v, a->B, a->Lk, a->Hkv, a->D, es};
     const Tensor tdk{dk, a->dk, a->B, a->Lk, a->Hkv, a->D, es}, tdv{dv, a->dv, a->B, a->Lk, a->Hkv, a->D, es};
-    if (a->Lq > 0 && (!tq.ok() || !to.ok() || !tg.ok() || !tdq.ok() || !tdq.distinct() || !lse || (uintptr_t)lse % 4))
+    const bool nq = a->Lq == 0 || a->H == 0, nk = a->Lk == 0;
+    if (!nq && (!tq.ok() || !to.ok() || !tg.ok() || !tdq.ok() || !tdq.distinct() || !lse || (uintptr_t)lse % 4))
         return SC_ERR_INVALID_ARGUMENT;
-    if (a->Lk > 0 && (!tk.ok() || !tv.ok() || !tdk.ok() || !tdv.ok() || !tdk.distinct() || !tdv.distinct()))
+    if (!nk && (!tk.ok() || !tv.ok() || !tdk.ok() || !tdv.ok() || !tdk.distinct() || !tdv.distinct()))
         return SC_ERR_INVALID_ARGUMENT;
     const size_t need = sc::attn_bwd_bytes(x);
     const int64_t nl = a->B * a->H * a->Lq;
     const Array none = rows_of(nullptr, 0, 0, 0, 1);
-    const bool nq = a->Lq == 0, nk = a->Lk == 0;
     const Array in[] = {nq ? none : tq.array(), nq ? none : to.array(), nq ? none : tg.array(),
                         nk ? none : tk.array(), nk ? none : tv.array(),
                         rows_of(lse, 1, nl, nl, 4), rows_of(a->slopes, 1, a->H, a->H, 4),
@@ -476,7 +477,7 @@ size_t sc_attn_workspace_bytes(sc_kind kind, const sc_attn* a, int backward)
 {
     sc::AttnArgs x;
     bool empty;
-    if (attn_shape(kind, a, &x, &empty) != SC_OK || empty) return 0;
+    if (attn_shape(kind, a, backward, &x, &empty) != SC_OK || empty) return 0;
     return backward ? sc::attn_bwd_bytes(x) : sc::attn_fwd_bytes(x);
 }
 
