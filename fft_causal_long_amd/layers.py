@@ -197,7 +197,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
                out: torch.Tensor | None = None, *, stats: bool = False):
     """y = (x - mean) rstd weight + bias over the last axis (sc_layernorm); x (..., C) with evenly
     spaced contiguous rows.  ``stats``: returns (y, mean, rstd), the statistics float32 of x's
-    leading shape, as :func:`layer_norm_bwd` takes them."""
+    leading shape, as :func:`layer_norm_bwd` takes them (NaN for rows of no values)."""
     kind = _check(x, weight, bias)
     if x.dim() < 1:
         raise ValueError("x must be (..., C)")
@@ -209,6 +209,9 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
     if stats:
         mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
         rstd = torch.empty_like(mean)
+        if C == 0:   # the mean of no values, 0 / 0; the call itself has nothing to do then
+            mean.fill_(math.nan)
+            rstd.fill_(math.nan)
     _run("layer_norm", _lib.sc_layernorm, x.device, kind, x.data_ptr(), _ptr(weight), _ptr(bias),
          y.data_ptr(), _ptr(mean), _ptr(rstd), rows, C, _row_stride(x), _row_stride(y), eps)
     return (y, mean, rstd) if stats else y

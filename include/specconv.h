@@ -434,7 +434,8 @@ sc_status sc_causal_conv_shared_bwd_bf16(const uint16_t* dr, const uint16_t* v, 
  * sc_layernorm -- y = (x - mean) rstd w + b per row of C values, mean = sum x / C,
  *   rstd = (sum (x - mean)^2 / C + eps)^-1/2 (the sum is taken about the mean).  w, b: C
  *   values or null (1, 0); mean, rstd: rows float32 values or null (not wanted).  eps >= 0.
- *   A row of NaN or infinity affects itself only.  C <= 2^30.
+ *   A row of NaN or infinity affects itself only.  C <= 2^30.  With rows = 0 or C = 0 nothing is
+ *   written (a row of no values has no mean).
  * sc_layernorm_bwd -- for the output gradient dy, with xh = (x - mean) rstd and e = dy w:
  *     dx = rstd (e - mean(e) - xh mean(e xh)),  dw = sum_rows dy xh,  db = sum_rows dy
  *   mean, rstd as the forward call returned them; dw, db null: not wanted (no ws then).  With

@@ -29,3 +29,13 @@ def test_no_query_heads(sc, dtype, Lq, Lk, D):
         dq, a, b = sc.causal_attention_bwd(q, q, k, v, q, lse, dk=dk, dv=dv, **opt)
         assert dq.shape == q.shape and a is dk and b is dv
         assert not dk.any() and not dv.any()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_statistics_of_rows_without_values(sc, dtype):
+    # a mean over no values is 0 / 0
+    print("case layernorm C=0 %s" % dtype, flush=True)
+    x = torch.empty(3, 5, 0, dtype=dtype, device=DEV)
+    y, mean, rstd = sc.layer_norm(x, stats=True)
+    assert y.shape == x.shape and mean.shape == rstd.shape == (3, 5)
+    assert torch.isnan(mean).all() and torch.isnan(rstd).all()
