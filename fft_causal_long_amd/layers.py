@@ -13,7 +13,7 @@ import math
 
 import torch
 
-from . import (KIND_BF16, KIND_F32, SC_OK, SpecConvError, _lib, _ws_args)
+from . import (KIND_BF16, KIND_F32, SC_ERR_UNSUPPORTED, SC_OK, SpecConvError, _lib, _ws_args)
 
 __all__ = [
     "layer_norm", "layer_norm_bwd", "gated_recurrence", "gated_recurrence_bwd",
@@ -345,13 +345,16 @@ def causal_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, windo
     positions of each sequence of kv_len[b] (default Lk) keys attend to the ``window`` (0: all)
     keys up to their own, within their document (doc_start (B, Lk) int32).  ``scale`` defaults to
     D^-1/2; ``cap`` > 0 caps scores by a tanh; ``slopes`` (H) float32 subtract slope * distance.
-    ``lse``: returns (o, lse), lse (B, H, Lq) float32."""
+    ``lse``: returns (o, lse), lse (B, H, Lq) float32; heads of no values (D = 0) have none
+    (SC_ERR_UNSUPPORTED)."""
     kind = _check(q, k, v, out)
     _typed(q, torch.float32, slopes)
     _typed(q, torch.int32, doc_start, kv_len)
     a = _attn(q, k, v, window, scale, cap, slopes, doc_start, kv_len)
     o = _out(out, q, "out")
     a.o = _strides(o)
+    if lse and a.D == 0 and a.B * a.H * a.Lq:   # the call has no result to write then, and no lse
+        raise SpecConvError(SC_ERR_UNSUPPORTED, "causal_attention: lse of heads of no values")
     L = torch.empty((a.B, a.H, a.Lq), dtype=torch.float32, device=q.device) if lse else None
     pa = ctypes.byref(a)
     keep, ws, n = _scratch(_lib.sc_attn_workspace_bytes(kind, pa, 0), workspace, q.device)

@@ -494,6 +494,7 @@ sc_status sc_recur_bwd(sc_kind kind, const void* dh, const void* z, const void* 
  * Lq H / Hkv at most 2^30 (else SC_ERR_UNSUPPORTED); pointers and strides that matter are
  * multiples of 16 bytes, scale > 0 and finite, cap >= 0 and finite, window >= 0
  * (0: no window) (else SC_ERR_INVALID_ARGUMENT).
+ * With B = 0, D = 0 or no heads there is no result and nothing is written, lse included.
  *
  *  sc_causal_attn -- o and, if lse is not null, lse (B, H, Lq) float32.  bfloat16 storage: the
  *      weights are rounded to bfloat16 for the second product, sums stay float32.  When the

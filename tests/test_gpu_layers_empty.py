@@ -39,3 +39,18 @@ def test_statistics_of_rows_without_values(sc, dtype):
     y, mean, rstd = sc.layer_norm(x, stats=True)
     assert y.shape == x.shape and mean.shape == rstd.shape == (3, 5)
     assert torch.isnan(mean).all() and torch.isnan(rstd).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_heads_without_values(sc, dtype):
+    # heads of no values: an empty result, but no log-sum is made up for them
+    print("case attn D=0 %s" % dtype, flush=True)
+    q = torch.empty(2, 5, 3, 0, dtype=dtype, device=DEV)
+    assert sc.causal_attention(q, q, q).shape == q.shape
+    with pytest.raises(sc.SpecConvError) as e:
+        sc.causal_attention(q, q, q, lse=True)
+    assert e.value.status == sc.SC_ERR_UNSUPPORTED
+    o, lse = sc.causal_attention(q[:0], q[:0], q[:0], lse=True)     # nothing to make up
+    assert o.shape == (0, 5, 3, 0) and lse.shape == (0, 3, 5)
+    g = sc.causal_attention_bwd(q, q, q, q, q, torch.empty(2, 3, 5, device=DEV))
+    assert all(t.shape == q.shape for t in g)
