@@ -267,6 +267,7 @@ __global__ __launch_bounds__(NT) void ln_bwd(const typename IO::T* __restrict__ 
 // eight loads in flight a thread (512 shares of C = 1024: 4 us; 11 us for twice the shares with one
 // load at a time).  16 and 8 columns give more workgroups and are 2-4% slower over the whole call.
 constexpr int PCOL = 32;
+constexpr int64_t PARAM_BLOCKS = 1 << 20;   // a launch holds fewer than 2^32 threads
 
 template <class IO>
 __global__ __launch_bounds__(1024) void ln_params(const float* __restrict__ part, int n, int C,
@@ -276,24 +277,29 @@ __global__ __launch_bounds__(1024) void ln_params(const float* __restrict__ part
     constexpr int PL = 1024 / PCOL;
     __shared__ float s[16][PCOL];
     const int cl = threadIdx.x % PCOL, pl = threadIdx.x / PCOL, wave = threadIdx.x >> 6;
-    const int64_t col = (int64_t)blockIdx.x * PCOL + cl;   // of the 2 C columns
-    const bool in = col < 2 * (int64_t)C;
-    float v = 0.f;
+    const int64_t cols = 2 * (int64_t)C;
+    // more than one turn only past PARAM_BLOCKS workgroups
+    for (int64_t c0 = (int64_t)blockIdx.x * PCOL; c0 < cols; c0 += (int64_t)gridDim.x * PCOL) {
+        const int64_t col = c0 + cl;
+        const bool in = col < cols;
+        float v = 0.f;
 #pragma unroll 8
-    for (int p = pl; p < n; p += PL) v += part[(int64_t)p * 2 * C + (in ? col : 0)];
+        for (int p = pl; p < n; p += PL) v += part[(int64_t)p * cols + (in ? col : 0)];
 #pragma unroll
-    for (int m = PCOL; m < 64; m <<= 1) v += __shfl_xor(v, m);
-    if ((threadIdx.x & 63) < PCOL) s[wave][cl] = v;
-    __syncthreads();
-    if (threadIdx.x < PCOL && in) {
-        float t = 0.f;
+        for (int m = PCOL; m < 64; m <<= 1) v += __shfl_xor(v, m);
+        if ((threadIdx.x & 63) < PCOL) s[wave][cl] = v;
+        __syncthreads();
+        if (threadIdx.x < PCOL && in) {
+            float t = 0.f;
 #pragma unroll
-        for (int w = 0; w < 16; ++w) t += s[w][cl];
-        if (col < C) {
-            if (dw) IO::store(dw, col, t);
-        } else if (db) {
-            IO::store(db, col - C, t);
+            for (int w = 0; w < 16; ++w) t += s[w][cl];
+            if (col < C) {
+                if (dw) IO::store(dw, col, t);
+            } else if (db) {
+                IO::store(db, col - C, t);
+            }
         }
+        __syncthreads();
     }
 }
 
@@ -539,8 +545,9 @@ hipError_t bwd(const void* dy, const void* x, const void* w, const float* mean, 
         });
     }
     if (e != hipSuccess || !params) return e;
-    hipLaunchKernelGGL((ln_params<IO>), dim3((unsigned)((2 * (int64_t)C + PCOL - 1) / PCOL)), dim3(1024), 0,
-                       st, part, (int)shares, C, (E*)dw, (E*)db);
+    const int64_t blocks = std::min<int64_t>((2 * (int64_t)C + PCOL - 1) / PCOL, PARAM_BLOCKS);
+    hipLaunchKernelGGL((ln_params<IO>), dim3((unsigned)blocks), dim3(1024), 0, st, part, (int)shares, C, (E*)dw,
+                       (E*)db);
     return hipGetLastError();
 }
 
