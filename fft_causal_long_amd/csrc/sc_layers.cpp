@@ -32,43 +32,98 @@ sc_status guarded(F&& f)
     }
 }
 
-// An array of `outer` x `rows` rows of `width` contiguous elements (sizes in bytes below): what
-// the overlap checks need to know.  width covers every element of a row (or of a token's heads).
+// What the overlap checks know of an array: runs of `width` elements of es bytes, one for each index
+// of the axes (n[i] places s[i] elements apart).
 struct Array {
     const void* p;
-    int64_t outer, rows, ostride, stride, width, es;
-    bool used() const { return p && outer > 0 && rows > 0 && width > 0; }
-    // one past the last byte; false if it does not fit 63 bits
-    bool end(__int128* out) const
+    int64_t n[3], s[3], width, es;
+    bool used() const { return p && n[0] > 0 && n[1] > 0 && n[2] > 0 && width > 0; }
+    // bytes from the first to past the last; false if they do not fit 63 bits
+    bool span(__int128* out) const
     {
-        const __int128 n = (__int128)(outer - 1) * ostride + (__int128)(rows - 1) * stride + width;
-        *out = (__int128)(uintptr_t)p + n * es;
-        return n * es <= (__int128)INT64_MAX;
+        __int128 k = width;
+        for (int i = 0; i < 3; ++i) k += (__int128)(n[i] - 1) * s[i];
+        *out = k * es;
+        return *out <= (__int128)INT64_MAX;
     }
 };
 
 Array rows_of(const void* p, int64_t rows, int64_t stride, int64_t width, int64_t es)
 {
-    return {p, 1, rows, 0, stride, width, es};
+    return {p, {rows, 1, 1}, {stride, 0, 0}, width, es};
 }
 
-// May two arrays share a byte?  Extents first; arrays whose extents meet but whose rows repeat
-// with the same period are columns of one array: they share nothing if their columns do not.
-bool share(const Array& a, const Array& b)
+// An array in bytes from `at` on, the axes that have more than one place by descending stride.
+struct Runs {
+    __int128 at;
+    int axes;
+    __int128 n[3], s[3], width;
+    explicit Runs(const Array& a) : at((uintptr_t)a.p), axes(0), width((__int128)a.width * a.es)
+    {
+        for (int i = 0; i < 3; ++i) {
+            if (a.n[i] < 2) continue;
+            int k = axes++;
+            for (; k > 0 && s[k - 1] < (__int128)a.s[i] * a.es; --k) {
+                n[k] = n[k - 1];
+                s[k] = s[k - 1];
+            }
+            n[k] = a.n[i];
+            s[k] = (__int128)a.s[i] * a.es;
+        }
+    }
+    __int128 span(int from) const
+    {
+        __int128 k = width;
+        for (int i = from; i < axes; ++i) k += (n[i] - 1) * s[i];
+        return k;
+    }
+};
+
+// May a from `pa` on with its axes ia.. share a byte with b from `pb` on with its axes ib..?  Not if
+// their extents do not meet.  Else the larger of the two leading strides is taken as a period that
+// both repeat with (the other array, if its stride is smaller, once); as long as what repeats is no
+// longer than the period, repetitions i of a and j of b meet for at most two values of i - j, and what
+// repeats is compared there.  Exact for axes that nest, as the parts of one dense array do; where they
+// do not, the arrays count as sharing.
+bool meet(const Runs& a, __int128 pa, int ia, const Runs& b, __int128 pb, int ib)
 {
-    if (!a.used() || !b.used()) return false;
-    __int128 ea, eb;
-    if (!a.end(&ea) || !b.end(&eb)) return true;
-    const __int128 pa = (uintptr_t)a.p, pb = (uintptr_t)b.p;
-    if (pa >= eb || pb >= ea) return false;
-    const int64_t period = a.stride * a.es;
-    if (period <= 0 || period != b.stride * b.es) return true;
-    if ((a.outer > 1 && a.ostride * a.es % period) || (b.outer > 1 && b.ostride * b.es % period))
-        return true;
-    const int64_t wa = a.width * a.es, wb = b.width * b.es;
-    if (wa > period || wb > period) return true;
-    const int64_t d = (int64_t)((pb - pa) % period + period) % period;   // b's first column - a's
-    return d < wa || d + wb > period;
+    if (pa >= pb + b.span(ib) || pb >= pa + a.span(ia)) return false;
+    const __int128 sa = ia < a.axes ? a.s[ia] : 0, sb = ib < b.axes ? b.s[ib] : 0, period = std::max(sa, sb);
+    if (period == 0) return true;
+    const bool ta = sa == period, tb = sb == period;   // whose leading axis is taken
+    const __int128 na = ta ? a.n[ia] : 1, nb = tb ? b.n[ib] : 1;
+    ia += ta;
+    ib += tb;
+    if (a.span(ia) > period || b.span(ib) > period) return true;
+    // a's repetition i begins at pa + i period, b's j at pb + j period: i - j = k
+    const __int128 d = pb - pa, low = d >= 0 ? d / period : -((-d + period - 1) / period);
+    for (__int128 k = low; k <= low + 1; ++k)
+        if (k > -nb && k < na && meet(a, pa + k * period, ia, b, pb, ib)) return true;
+    return false;
+}
+
+// May two arrays share a byte?  Rows of one period whose other axes are multiples of it are columns of
+// one array, whatever those axes are: they share nothing if their columns do not.
+bool share(const Array& x, const Array& y)
+{
+    if (!x.used() || !y.used()) return false;
+    __int128 ex, ey;
+    if (!x.span(&ex) || !y.span(&ey)) return true;
+    const __int128 px = (uintptr_t)x.p, py = (uintptr_t)y.p;
+    if (px >= py + ey || py >= px + ex) return false;   // almost always
+    const Runs a(x), b(y);
+    for (int ka = 0; ka < a.axes; ++ka)
+        for (int kb = 0; kb < b.axes; ++kb) {
+            const __int128 period = a.s[ka], wa = a.span(ka + 1), wb = b.span(kb + 1);
+            if (period <= 0 || period != b.s[kb] || wa > period || wb > period) continue;
+            bool multiples = true;
+            for (int i = 0; i < ka; ++i) multiples &= a.s[i] % period == 0;
+            for (int i = 0; i < kb; ++i) multiples &= b.s[i] % period == 0;
+            if (!multiples) continue;
+            const __int128 d = ((b.at - a.at) % period + period) % period;   // b's first column - a's
+            if (d >= wa && d + wb <= period) return false;
+        }
+    return meet(a, a.at, 0, b, b.at, 0);
 }
 
 // Every output apart from every input and from the other outputs.
@@ -87,7 +142,7 @@ bool apart(const Array (&in)[NI], const Array (&out)[NO])
 bool fits(const Array& a)
 {
     __int128 e;
-    return !a.used() || a.end(&e);
+    return !a.used() || a.span(&e);
 }
 
 bool aligned(const void* p, int64_t stride, int64_t es)
@@ -255,21 +310,12 @@ sc_status recur_bwd_run(sc_kind kind, const void* dh, const void* z, const void*
 
 // ------------------------------------------------------------------ attention
 
-// A (batch, token, head) tensor; token footprints as Array rows where heads lie inside a token.
+// A (batch, token, head) tensor.
 struct Tensor {
     const void* p;
     const int64_t* s;
     int64_t B, L, H, D, es;
-    Array array() const
-    {
-        const int64_t hs = H > 1 ? s[2] : 0, ts = L > 1 ? s[1] : 0, bs = B > 1 ? s[0] : 0;
-        const int64_t tok = (H - 1) * hs + D;   // one token's span
-        if (L > 1 && tok > ts) {   // heads outside tokens: one extent
-            const int64_t all = (B - 1) * bs + (L - 1) * ts + tok;
-            return {p, 1, 1, 0, all, all, es};
-        }
-        return {p, B, L, bs, L > 1 ? ts : (B > 1 ? bs : tok), tok, es};
-    }
+    Array array() const { return {p, {B, L, H}, {s[0], s[1], s[2]}, D, es}; }
     // sizes times strides in range, 16-byte steps
     bool ok() const
     {

@@ -424,7 +424,8 @@ sc_status sc_causal_conv_shared_bwd_bf16(const uint16_t* dr, const uint16_t* v, 
  *    of a wider array can be passed; the row itself is contiguous.  Inputs take any stride
  *    >= 0, outputs one of at least the row's length.
  *  - An output may share no element with an input or another output (SC_ERR_INVALID_ARGUMENT);
- *    interleaved columns of one array are told apart when the row strides are equal.
+ *    Told apart are parts of one dense array along any of its axes, and interleaved columns
+ *    whose row strides are equal; other layouts whose extents meet count as sharing.
  *  - Rows that all start 16-byte aligned are moved in 16-byte vectors; others work, slower.
  *  - ws: scratch of the call's *_workspace_bytes (256-byte aligned, overlapping nothing else),
  *    or null with ws_bytes 0: the call then allocates it stream-ordered.
