@@ -99,10 +99,11 @@ def sc_causal_attn_bwd(kind, a, dout, q, k, v, o, lse, dq, dk, dv, ws, ws_bytes,
 # ---------------------------------------------------------------- tensor front end
 
 _KIND = {torch.float32: KIND_F32, torch.bfloat16: KIND_BF16}
-# the current stream's handle without building a Stream object: a decoding step is a handful of
-# microseconds, most of them spent here
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_get_device = torch._C._cuda_getDevice
+# The current stream's handle without building a Stream object: a decoding step is a handful of
+# microseconds, most of them spent here.  A torch without these entry points (one built without GPU
+# support has none) takes the public calls.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _check(x, *others):
