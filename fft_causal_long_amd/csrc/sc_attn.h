@@ -177,6 +177,16 @@ __device__ __forceinline__ void stage_barrier()
     asm volatile("" ::: "memory");
 }
 
+// What this wave's lanes wrote to LDS comes before what its lanes read next.  The hardware keeps a
+// wave's LDS order by itself; this keeps the compiler's, which need not see that a vector read meets
+// another lane's scalar write.
+__device__ __forceinline__ void wave_lds_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // B operand from two result blocks (the halves of a 32-row strip), rounded to the storage type:
 // bfloat16 weights carry a relative error of up to 2^-8 each, as the values they multiply do.
 template <class IO>

@@ -453,6 +453,7 @@ __global__ __launch_bounds__((64 * S::NW), (kv_occupancy<IO, DP>)) void attn_bwd
                 const bool some = tb + r < a.Lq && p >= 0 && lo <= p;
                 first[wave][r] = some ? lo : BIG;
                 span[wave][r] = some ? p - lo : -1;
+                wave_lds_order();
                 // rows that see nothing, or lie past the last: 0, whatever the memory holds
                 alive = __ballot(some);
                 if (BN < 64) alive |= ~0ull << (BN & 63);
