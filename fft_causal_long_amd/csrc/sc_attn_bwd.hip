@@ -15,7 +15,8 @@
 //    plain sums.
 // Both keep their own side's operands in registers (B operands), bring the other side into an LDS
 // ring by asynchronous loads, and feed the score-shaped products to the next product from
-// registers (sc_attn.h).  Seven products instead of the five of a single kernel that would add dq
+// registers (sc_attn.h), P and dS rounded to the storage type on the way, as the forward pass rounds its
+// weights.  Seven products instead of the five of a single kernel that would add dq
 // with atomics.
 //
 // Measured (MI355X; a large copy moves 5.4 TB/s): bfloat16, B 8, L 4096, 16 heads of 64, window
@@ -50,7 +51,10 @@ struct Shape {
     static constexpr int N = N_, NW = NW_, W = 16 * N, ROWS = NW * W;   // rows of a wave, of a workgroup
 };
 
-// Waves a SIMD the kernels are compiled for: as many as their registers allow without spills.
+// Waves a SIMD the kernels are compiled for: as many as their registers allow without spills but for
+// three capped forms with a bias (of attn_bwd_kv, float32 heads over 64 in workgroups of 64 keys, and
+// bfloat16 heads up to 64 with the tanh series in workgroups of 128: two registers; of attn_bwd_q, the
+// latter's: five).
 template <class IO, int DP>
 constexpr int q_occupancy = IO::SIZE == 2 && DP == 64 ? 3 : 2;
 template <class IO, int DP>

@@ -23,10 +23,10 @@
 // Measured (MI355X): B 8, L 4096, C 1024 bfloat16 forward 50.6 us (4.0 TB/s of the bytes it
 // cannot do without; a large copy reaches 5.4), backward 111 us (3.6); B 8, L 1024, C 768
 // float32 backward 34 us (4.4); B 1, L 65536, C 1536 float32 forward 428 us, where the fold
-// reads z and u a second time (2.0 GB in all, 4.7 TB/s); its three kernels take 184, 5 and 242 us.  NC, R and the waves were chosen there:
-// for bfloat16 forward, 2 channels and 8 tokens a lane took 50.6 us, 4 x 8 54.2, 8 x 4 55.2
-// (more shuffles a value); 4 waves a workgroup 61, and loads two tiles ahead 60; for float32
-// 4 x 4 and 2 x 8 are within 2%.
+// reads z and u a second time (2.0 GB in all, 4.7 TB/s); its three kernels take 184, 5 and 240 us.
+// NC, R and the waves were chosen there: for bfloat16 forward, 2 channels and 8 tokens a lane took
+// 50.6 us, 4 x 8 54.2, 8 x 4 55.2 (more shuffles a value); 4 waves a workgroup 61, and loads two tiles
+// ahead 60; for float32 4 x 4 and 2 x 8 are within 2%.
 
 #include <hip/hip_runtime.h>
 
@@ -43,9 +43,11 @@ namespace {
 constexpr int NT = 256;    // threads of the small kernels
 constexpr int CG = 32;     // channels of a workgroup
 
-// f = 1 / (1 + e), 1 - f = e f with e = exp(-z): each exact to a few ulp where the other
-// saturates.  The exponent stops at 2^125, below which the reciprocal is a normal number (past
-// 2^126 it is flushed to 0, and e f with it); a comparison, not a minimum, so a NaN in z stays.
+// f = 1 / (1 + e), 1 - f = e f with e = exp(-z): neither loses its relative precision where the other
+// saturates.  The rounding of the exponent moves e, and the smaller gate with it, by about |z| units
+// of 2^-24 (31 at |z| = 40); beside it a few ulp.  The exponent stops at 2^125, below which the
+// reciprocal is a normal number (past 2^126 it is flushed to 0, and e f with it), so f stays at 2^-125
+// for z below -86.6; a comparison, not a minimum, so a NaN in z stays.
 __device__ __forceinline__ void gates(float z, float& f, float& k)
 {
     const float t = z * -1.44269504088896340736f;

@@ -419,7 +419,8 @@ sc_status sc_causal_conv_shared_bwd_bf16(const uint16_t* dr, const uint16_t* v, 
  * Architecture via Spectral Mixing", key designs 1 and 3); a gated recurrence is the mixing
  * layer of the models it is compared with.  These calls take SC_KIND_F32 or SC_KIND_BF16 (else
  * SC_ERR_INVALID_ARGUMENT), token-major activations, and keep every sum, statistic and state
- * in float32; bfloat16 results are rounded once, nearest, ties to even.  Shared conventions:
+ * in float32; bfloat16 results are rounded once, nearest, ties to even (attention rounds the factors
+ * of its second products too, see there).  Shared conventions:
  *  - A "row stride" is the distance in elements between consecutive rows (tokens), so columns
  *    of a wider array can be passed; the row itself is contiguous.  Inputs take any stride
  *    >= 0, outputs one of at least the row's length.
@@ -457,8 +458,9 @@ sc_status sc_layernorm_bwd(sc_kind kind, const void* dy, const void* x, const vo
  *   z, u, h: token t of batch row b starts (b L + t) * stride elements in.  h0: the state
  *   before token 0, (B, C) float32, or null (zero); hT: the state after the last token, or
  *   null.  hT may be h0 itself (the state of a decoding loop).  Both gates are computed from
- *   exp(-|z|), so neither loses precision where the other saturates.  L = 1 is the step of a
- *   decoding loop.  An empty sequence (L = 0) copies h0 (or zero) to hT.
+ *   e = exp(-z), as 1 / (1 + e) and e / (1 + e), so neither loses its relative precision where the
+ *   other saturates: the smaller one is off by about |z| units of 2^-24.  e is kept to 2^125, so f is
+ *   2^-125 for every z below -86.6.  L = 1 is the step of a decoding loop.  An empty sequence (L = 0) copies h0 (or zero) to hT.
  * sc_recur_bwd -- for the output gradient dh and that of hT, dhT (null: zero):
  *     g_t = dh_t + f_{t+1} g_{t+1}  (dhT after the last),   du_t = (1 - f_t) g_t,
  *     dz_t = g_t (h_{t-1} - u_t) f_t (1 - f_t),             dh0 = f_0 g_0
@@ -504,7 +506,8 @@ sc_status sc_recur_bwd(sc_kind kind, const void* dh, const void* z, const void* 
  *  sc_causal_attn_bwd -- dq (strides dq), dk, dv (of key heads: summed over the heads that
  *      share them) for the output gradient dout (strides dout), from the forward call's o and
  *      lse; sc_attn_workspace_bytes(kind, a, 1) bytes of ws.  dk, dv are written for every key,
- *      0 where no row sees it.
+ *      0 where no row sees it.  bfloat16 storage: the weights and the gradients of the scores are
+ *      rounded to bfloat16 for the products that make dq, dk and dv; the sums stay float32.
  */
 typedef struct sc_attn {
     int64_t B, Lq, Lk, H, Hkv, D;
