@@ -249,6 +249,15 @@ constexpr Cap cap_of(float cap)
     return !(cap > 0.f) ? UNCAPPED : IO::SIZE == 4 || cap > SERIES_CAP ? SERIES : CAPPED;
 }
 
+// What a raw product is multiplied by: for tanh's argument, no more than the largest float32 where the
+// quotient passes it (a 0 stays 0 and everything else saturates, as it does with the quotient), or for
+// the score in base 2.
+template <Cap CAP>
+__device__ __forceinline__ float score_scale(const AttnArgs& a)
+{
+    return CAP != UNCAPPED ? fminf(a.scale / a.cap, 3.402823466e38f) : a.scale * LOG2E;
+}
+
 template <class IO, Cap CAP>
 __device__ __forceinline__ float tanh_of(float y)
 {

@@ -126,7 +126,7 @@ __global__ __launch_bounds__((64 * S::NW), (fwd_occupancy<IO, DP, S>)) void attn
         t1 = min(t1, t0 + per);
     }
 
-    const float scale2 = CAP != UNCAPPED ? a.scale / a.cap : a.scale * LOG2E, cap2 = a.cap * LOG2E;
+    const float scale2 = score_scale<CAP>(a), cap2 = a.cap * LOG2E;
     f32x4 o[ND][NQ];
     float mx[NQ], sum[NQ];
 #pragma unroll

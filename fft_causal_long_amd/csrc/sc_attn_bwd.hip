@@ -144,7 +144,7 @@ __global__ __launch_bounds__((64 * S::NW), (q_occupancy<IO, DP>)) void attn_bwd_
     khi = __builtin_amdgcn_readfirstlane(khi);
     const int t0 = khi < 0 ? 0 : klo / BN, t1 = khi < 0 ? 0 : khi / BN + 1;
 
-    const float scale2 = CAP != UNCAPPED ? a.scale / a.cap : a.scale * LOG2E, cap2 = a.cap * LOG2E;
+    const float scale2 = score_scale<CAP>(a), cap2 = a.cap * LOG2E;
     f32x4 acc[ND][NQ];
 #pragma unroll
     for (int d = 0; d < ND; ++d)
@@ -331,7 +331,7 @@ __global__ __launch_bounds__((64 * S::NW), (kv_occupancy<IO, DP>)) void attn_bwd
 #pragma unroll
         for (int m = 0; m < NK; ++m) dk[d][m] = dv[d][m] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const float scale2 = CAP != UNCAPPED ? a.scale / a.cap : a.scale * LOG2E, cap2 = a.cap * LOG2E;
+    const float scale2 = score_scale<CAP>(a), cap2 = a.cap * LOG2E;
     const int off = n - a.Lq;   // position of token 0
     // stages of tokens at positions jb .. jb + BK - 1 + window - 1
     int s0 = 0, s1 = 0;

@@ -28,3 +28,11 @@ def test_caps(sc, dtype, cap):
 def test_caps_over_a_cache(sc, dtype, cap):
     print("case attn cap cache %s cap=%g" % (dtype, cap), flush=True)
     run(sc, 2, 1, 1500, 4, 2, 64, dtype, cap=cap, kv_len=[1500, 3], qmul=3.0, bwd=False)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_smallest_caps(sc, dtype):
+    # scale / cap past the largest float32: every score is the cap, with its sign
+    print("case attn smallest cap %s" % dtype, flush=True)
+    run(sc, 2, 70, 70, 2, 1, 64, dtype, cap=1e-42)
+    run(sc, 1, 1, 600, 2, 1, 128, dtype, cap=1e-42, bias=True, bwd=False)
