@@ -233,31 +233,20 @@ __device__ __forceinline__ void keep_branch() { asm volatile(""); }
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// A kernel's form for the call's cap (cap_of).  tanh(y) as 1 - 2 / (1 + e^2y) is off by up to 4 units
-// of 2^-24 whatever y, and the cap multiplies that.  With SERIES the odd Taylor series takes over near
-// 0, so that the error is relative to tanh(y) everywhere: float32 storage always, below 1/2 and to y^15
-// (the next term is under 1e-8 of the sum), about 7 units in all; 16-bit storage for caps over 64,
-// below 1/8 and to y^5, about 31 units (2e-6).  Smaller caps leave 16-bit storage a score off by no
-// more than 1.5e-5, which its weights, rounded to 2^-8, do not show, and the series costs time and
-// registers: B 8, L 4096, 16 heads of 64, window 256: forward 121 us with it and 117 without, backward
-// 364 and 331; L 8192, 16 heads of 128 on 4: 464 and 434, 1606 and 1526.
+// A kernel's form for the call's cap.  tanh(y) as 1 - 2 / (1 + e^2y) is off by up to 4 units of 2^-24
+// whatever y, and the cap multiplies that.  With SERIES a polynomial takes over near 0, so that the
+// error is relative to tanh(y) everywhere, no more than 9 units.  float32 storage always takes it, and
+// so does the forward pass, whose lse is float32 whatever the storage.  The backward pass of 16-bit
+// storage does without for caps up to 64: a score is then off by no more than 1.5e-5, which results
+// rounded to 2^-8 do not show.  There it costs time and registers: B 8, L 4096, 16 heads of 64, window
+// 256: 364 us with it, 331 without; L 8192, 16 heads of 128 on 4: 1606 and 1526.  (The forward pass: 122
+// and 116, 470 and 432.)
 enum Cap { UNCAPPED, CAPPED, SERIES };
 constexpr float SERIES_CAP = 64.f;
-template <class IO>
-constexpr Cap cap_of(float cap)
-{
-    return !(cap > 0.f) ? UNCAPPED : IO::SIZE == 4 || cap > SERIES_CAP ? SERIES : CAPPED;
-}
 
-// What a raw product is multiplied by: for tanh's argument, no more than the largest float32 where the
-// quotient passes it (a 0 stays 0 and everything else saturates, as it does with the quotient), or for
-// the score in base 2.
-template <Cap CAP>
-__device__ __forceinline__ float score_scale(const AttnArgs& a)
-{
-    return CAP != UNCAPPED ? fminf(a.scale / a.cap, 3.402823466e38f) : a.scale * LOG2E;
-}
-
+// float32 storage, below 1/2: the Taylor series to y^15 (the next term is under 1e-8 of the sum).
+// 16-bit storage, y^2 below 0.2: y + y^3 (c0 + c1 y^2 + c2 y^4), c fitted for the least maximum of the
+// relative error there (5 units).
 template <class IO, Cap CAP>
 __device__ __forceinline__ float tanh_of(float y)
 {
@@ -268,7 +257,8 @@ __device__ __forceinline__ float tanh_of(float y)
         const float z = y * y;
         float p;
         if constexpr (IO::SIZE == 2) {
-            p = __builtin_fmaf(2.0f / 15.0f, z, -1.0f / 3.0f);
+            p = __builtin_fmaf(-0.046406733f, z, 0.13248634f);
+            p = __builtin_fmaf(p, z, -0.333305836f);
         } else {
             p = -929569.0f / 638512875.0f;
             p = __builtin_fmaf(p, z, 21844.0f / 6081075.0f);
@@ -278,23 +268,29 @@ __device__ __forceinline__ float tanh_of(float y)
             p = __builtin_fmaf(p, z, 2.0f / 15.0f);
             p = __builtin_fmaf(p, z, -1.0f / 3.0f);
         }
-        return z < (IO::SIZE == 2 ? 1.0f / 64.0f : 0.25f) ? __builtin_fmaf(p * z, y, y) : t;
+        return z < (IO::SIZE == 2 ? 0.2f : 0.25f) ? __builtin_fmaf(p * z, y, y) : t;
     }
 }
 
-// Calls f(Cap, BIAS) as constants for the call's options.  (float32 has no CAPPED form.)
-template <class IO, class F>
+// Calls f(Cap, BIAS) as constants for the call's options.
+template <class IO, bool BWD, class F>
 hipError_t with_options(const AttnArgs& a, F&& f)
 {
     using std::integral_constant;
     auto bias = [&](auto cap) { return a.slopes ? f(cap, std::true_type()) : f(cap, std::false_type()); };
-    switch (cap_of<IO>(a.cap)) {
-    case UNCAPPED: return bias(integral_constant<Cap, UNCAPPED>());
-    case SERIES: return bias(integral_constant<Cap, SERIES>());
-    default: break;
-    }
-    if constexpr (IO::SIZE == 2) return bias(integral_constant<Cap, CAPPED>());
-    return hipErrorInvalidValue;
+    if (!(a.cap > 0.f)) return bias(integral_constant<Cap, UNCAPPED>());
+    if constexpr (BWD && IO::SIZE == 2)
+        if (a.cap <= SERIES_CAP) return bias(integral_constant<Cap, CAPPED>());
+    return bias(integral_constant<Cap, SERIES>());
+}
+
+// What a raw product is multiplied by: for tanh's argument, no more than the largest float32 where the
+// quotient passes it (a 0 stays 0 and everything else saturates, as it does with the quotient), or for
+// the score in base 2.
+template <Cap CAP>
+__device__ __forceinline__ float score_scale(const AttnArgs& a)
+{
+    return CAP != UNCAPPED ? fminf(a.scale / a.cap, 3.402823466e38f) : a.scale * LOG2E;
 }
 
 // The batch row's length, and a query row's place in it.

@@ -361,7 +361,7 @@ template <class IO, int DP, class S>
 hipError_t pick(AttnArgs a, hipStream_t st)
 {
     a.ntile = (a.nrow + S::BM - 1) / S::BM;
-    return with_options<IO>(a, [&](auto cap, auto bias) {
+    return with_options<IO, false>(a, [&](auto cap, auto bias) {
         return go<IO, DP, decltype(cap)::value, decltype(bias)::value, S>(a, st);
     });
 }

@@ -642,7 +642,7 @@ hipError_t go(const AttnArgs& a, hipStream_t st)
 template <class IO, int DP>
 hipError_t pick(const AttnArgs& a, hipStream_t st)
 {
-    return with_options<IO>(a, [&](auto cap, auto bias) {
+    return with_options<IO, true>(a, [&](auto cap, auto bias) {
         return go<IO, DP, decltype(cap)::value, decltype(bias)::value>(a, st);
     });
 }

@@ -122,18 +122,18 @@ def visible(Lq, Lk, window, n, doc):
     return see, p - j
 
 
-def _cap_err(s, cap, bf16):
+def _cap_err(s, cap, plain):
     """Error of s = cap tanh(x / cap) beside the argument's.  From t = 1 - 2 r, r = 1 / (1 + e^2y):
     e is off by (4 y + 2) U (its argument's two roundings; an ulp), r by that times e / (1 + e) and 3
-    more: 4 U of t at most.  A series near 0 makes it relative: 2 r / t is 1.2 at y = 1/2, where float32
-    goes over to it: 7 U; 7.0 at y = 1/8, where bfloat16 with a cap over 64 does: 31 U, and its series
-    leaves out 3.5 U there.  The products with cap and cap's conversion add 3 U."""
-    if bf16 and cap <= 64:
+    more: 4 U of t at most, which is what a plain evaluation has.  A series near 0 makes it relative: 2 r
+    / t is 1.4 at y = 0.45, where the last of them gives way: 9 U.  The products with cap and cap's
+    conversion add 3 U."""
+    if plain:
         return 4 * U * cap + 3 * U * np.abs(s)
-    return (40 if bf16 else 12) * U * np.abs(s)
+    return 12 * U * np.abs(s)
 
 
-def _scores(q, k, see, far, scale, cap, slope, bf16):
+def _scores(q, k, see, far, scale, cap, slope, plain=False):
     x = scale * (q @ k.T)
     mag = scale * (np.abs(q) @ np.abs(k).T)
     t = None
@@ -142,7 +142,7 @@ def _scores(q, k, see, far, scale, cap, slope, bf16):
     if cap:
         t = np.tanh(x / cap)
         s = cap * t
-        err = err + _cap_err(s, cap, bf16)   # tanh passes on no more than its argument's error
+        err = err + _cap_err(s, cap, plain)   # tanh passes on no more than its argument's error
     s = s - slope * far
     err = err + 8 * U * (np.abs(s) + np.abs(slope * far)) + 4 * U
     return np.where(see, s, -np.inf), t, np.where(see, err, 0.0)
@@ -167,8 +167,7 @@ def attention(q, k, v, scale, window=0, cap=0.0, slopes=None, kv_len=None, doc=N
     o, bo = np.zeros(q.shape), np.zeros(q.shape)
     lse, bl = np.full((B, H, Lq), -np.inf), np.zeros((B, H, Lq))
     for b, h, g, see, far, qq, kk, vv, rows in _each(q, k, v, Lk, H, Hkv, window, kv_len, doc):
-        s, _, err = _scores(qq, kk, see, far, scale, cap, 0.0 if slopes is None else float(slopes[h]),
-                            bf16)
+        s, _, err = _scores(qq, kk, see, far, scale, cap, 0.0 if slopes is None else float(slopes[h]))
         m = np.where(rows, s.max(1, initial=-np.inf), 0.0)
         e = np.exp(s - m[:, None])
         l = e.sum(1)
@@ -193,7 +192,7 @@ def attention_bwd(do, q, k, v, o, lse, scale, window=0, cap=0.0, slopes=None, kv
     r = UB if bf16 else 0.0
     for b, h, g, see, far, qq, kk, vv, rows in _each(q, k, v, Lk, H, Hkv, window, kv_len, doc):
         s, t, err = _scores(qq, kk, see, far, scale, cap, 0.0 if slopes is None else float(slopes[h]),
-                            bf16)
+                            plain=bf16 and cap <= 64)
         dd, oo = (np.where(rows[:, None], x[b, :, h], 0.0) for x in (do, o))
         L = np.where(rows, lse[b, h], 0.0)
         p = np.exp(s - L[:, None])
