@@ -59,6 +59,14 @@ struct Shape {
 template <class IO, int DP, class S>
 constexpr int fwd_occupancy = S::NW == 1 ? 1 : IO::SIZE == 2 && DP == 64 ? 3 : 2;
 
+// Weights of bfloat16 storage as the sum of two bfloat16 values, which takes the second product twice:
+// for the few rows of decoding, where the cache's bytes leave the arithmetic time, so that o is off by
+// its own rounding only (0.0017 of it; 0.0024 with weights of one).  The caches of tile_rows: 99.4 us
+// with one, 99.8 with two; 64 sequences over 2048 keys, 16 heads of 128 on 2: 35.1 and 36.4.  More rows
+// take one: window 256 as above 91 us, 108 with two; L 8192 332 and 421.
+template <class IO, class S>
+constexpr bool two_weights = IO::SIZE == 2 && S::NW == 1;
+
 template <class IO, int DP, Cap CAP, bool BIAS, class S>
 __global__ __launch_bounds__((64 * S::NW), (fwd_occupancy<IO, DP, S>)) void attn_fwd(AttnArgs a)
 {
@@ -66,6 +74,7 @@ __global__ __launch_bounds__((64 * S::NW), (fwd_occupancy<IO, DP, S>)) void attn
     constexpr int NQ = S::NQ, NW = S::NW, WM = S::WM, BM = S::BM, BN = S::BN;
     using R = Ring<IO, DP, 64 * NW, BN>;
     constexpr int KK = DP / 32, ND = DP / 16, KB = BN / 16;   // 16-key blocks of a tile
+    constexpr bool TWO = two_weights<IO, S>;
     __shared__ __attribute__((aligned(1024))) typename R::Shared sh;
     __shared__ int4 range[NW];
 
@@ -173,7 +182,7 @@ __global__ __launch_bounds__((64 * S::NW), (fwd_occupancy<IO, DP, S>)) void attn
             }
         }
         const bool edge = j0 < rr.last || j0 + BN - 1 > rr.pos;
-        Frag<IO> w[KB / 2][NQ];
+        Frag<IO> w[KB / 2][NQ], rest[KB / 2][NQ];
 #pragma unroll
         for (int m = 0; m < NQ; ++m) {
             // scores in base 2, less the row's base: the running maximum as it was when a score
@@ -237,7 +246,10 @@ __global__ __launch_bounds__((64 * S::NW), (fwd_occupancy<IO, DP, S>)) void attn
                     sum[m] += e;
                 }
 #pragma unroll
-            for (int hf = 0; hf < KB / 2; ++hf) w[hf][m] = frag_of<IO>(s[2 * hf][m], s[2 * hf + 1][m]);
+            for (int hf = 0; hf < KB / 2; ++hf) {
+                w[hf][m] = frag_of<IO>(s[2 * hf][m], s[2 * hf + 1][m]);
+                if constexpr (TWO) rest[hf][m] = frag_rest(s[2 * hf][m], s[2 * hf + 1][m], w[hf][m]);
+            }
         }
         // o^T += v^T w
 #pragma unroll
@@ -246,7 +258,10 @@ __global__ __launch_bounds__((64 * S::NW), (fwd_occupancy<IO, DP, S>)) void attn
             for (int hf = 0; hf < KB / 2; ++hf) {
                 const Frag<IO> f = frag_tr<IO, DP>(Vt, 32 * hf, 16 * d, g, c);
 #pragma unroll
-                for (int m = 0; m < NQ; ++m) o[d][m] = mma(f, w[hf][m], o[d][m]);
+                for (int m = 0; m < NQ; ++m) {
+                    o[d][m] = mma(f, w[hf][m], o[d][m]);
+                    if constexpr (TWO) o[d][m] = mma(f, rest[hf][m], o[d][m]);
+                }
             }
     }
 

@@ -500,7 +500,8 @@ sc_status sc_recur_bwd(sc_kind kind, const void* dh, const void* z, const void* 
  * With B = 0, D = 0 or no heads there is no result and nothing is written, lse included.
  *
  *  sc_causal_attn -- o and, if lse is not null, lse (B, H, Lq) float32.  bfloat16 storage: the
- *      weights are rounded to bfloat16 for the second product, sums stay float32.  When the
+ *      weights are rounded to bfloat16 for the second product (up to 16 rows Lq H / Hkv: to the sum
+ *      of two bfloat16 values, (2^-8)^2 of each), sums stay float32.  When the
  *      rows alone do not fill the GPU (decoding) the keys are split over workgroups and the
  *      parts joined, through sc_attn_workspace_bytes(kind, a, 0) bytes of ws.
  *  sc_causal_attn_bwd -- dq (strides dq), dk, dv (of key heads: summed over the heads that
