@@ -61,9 +61,10 @@ constexpr int fwd_occupancy = S::NW == 1 ? 1 : IO::SIZE == 2 && DP == 64 ? 3 : 2
 
 // Weights of bfloat16 storage as the sum of two bfloat16 values, which takes the second product twice:
 // for the few rows of decoding, where the cache's bytes leave the arithmetic time, so that o is off by
-// its own rounding only (0.0017 of it; 0.0024 with weights of one).  The caches of tile_rows: 99.4 us
-// with one, 99.8 with two; 64 sequences over 2048 keys, 16 heads of 128 on 2: 35.1 and 36.4.  More rows
-// take one: window 256 as above 91 us, 108 with two; L 8192 332 and 421.
+// its own rounding only (0.0017 of it; 0.0024 with weights of one).  8 sequences over 65536 keys each,
+// 16 heads of 64 on 4: 99.4 us with one, 99.8 with two; 64 sequences over 2048 keys, 16 heads of 128 on
+// 2: 35.1 and 36.4.  More rows take one: B 8, L 4096, 16 heads of 64, window 256, no bias: 91 us, 108
+// with two; L 8192 as above 332 and 421.
 template <class IO, class S>
 constexpr bool two_weights = IO::SIZE == 2 && S::NW == 1;
 
