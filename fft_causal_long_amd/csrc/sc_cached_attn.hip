@@ -1,0 +1,537 @@
+// Causal attention over a cache of 8-bit codes (layout in sc_cache.h), with a window, first tokens that
+// stay visible (sinks), a distance bias and a tanh cap (gfx950).
+//
+// Query row i of batch row b stands at p = len_b - Lq + i and sees j <= p with j > p - window or
+// j < sinks.  With codes K, V and block scales ks, vs:
+//
+//     x = scale ks q.K,  s = cap tanh(x / cap)  (cap > 0),  s -= slope_h (p - j)
+//     o = sum_j softmax(s)_j vs V_j,   lse = log sum_j exp(s_j)
+//
+// One pass with a running base and sum, in base 2.  Codes are exact in half precision, so both products
+// run on the half-precision matrix instruction: a query row is multiplied by the power of two that
+// brings its largest value to 2^14 .. 2^15 (bfloat16 values then are exact down to 2^-29 of it; float32
+// ones are the sum of two halves, 2^-22 of each), and a weight carries 11 bits (float32: two halves).  A
+// block's vs goes into the weights' exponent, w = 2^(s + log2 vs - base), so that every weight is
+// relative to the row's largest contribution to o, whatever the scales; the sum takes w / vs.
+// The heads that share a key head are packed into one row axis, scores are made transposed (keys x
+// rows) and the blocks' byte order is that of the operands (sc_cache.h), so a score block, rounded, is
+// the operand of the second product and codes go from memory to the products without an exchange.
+//
+// Few rows (decoding): the four waves of a workgroup share 16 rows and take blocks in turn, each with
+// its next block on its way in registers, and join their results through LDS; keys are split over
+// workgroups to fill the GPU.  More rows: a wave has rows of its own and the workgroup's blocks come by
+// asynchronous loads into a ring of three LDS places.
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "sc_attn.h"
+#include "sc_cache.h"
+
+namespace sc {
+
+namespace {
+
+using namespace attn;
+using namespace cache;
+
+constexpr float SLACK = 8.f;   // a row's base may lag its maximum by this (base 2)
+constexpr float HEAD = 7.f;    // weights are 2^HEAD at the base: up to 2^15 in half precision
+
+// q times this brings a row's largest magnitude to 2^14 .. 2^15.
+constexpr int Q_TOP = 14;
+
+// A workgroup's shape: NQ 16-row blocks a wave, NW waves; KEYS: the waves share the rows and take the
+// blocks in turn.
+template <int NQ_, int NW_, bool KEYS_>
+struct Shape {
+    static constexpr int NQ = NQ_, NW = NW_, WM = 16 * NQ, BM = KEYS_ ? WM : NW * WM;
+    static constexpr bool KEYS = KEYS_;
+};
+
+__device__ __forceinline__ f32x4 mma(const half8_t& a, const half8_t& b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// Eight float32 values as halves, and what that left of them.
+__device__ __forceinline__ half8_t halves_of(const float (&x)[8])
+{
+    half8_t h;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = (_Float16)x[e];
+    return h;
+}
+__device__ __forceinline__ half8_t rest_of(const float (&x)[8], const half8_t& h)
+{
+    half8_t r;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = (_Float16)(x[e] - (float)h[e]);
+    return r;
+}
+
+// The 64-token blocks a strip of rows sees, [0, sink) and [t0, t1), newest first: with a distance bias
+// the first base is then near the last one.  (A base that rises by x leaves the scores it rose for with
+// the roundings of x: from the first tokens on, 4096 keys of slope 1 / sqrt 2 cost lse 5e-6.)
+struct Blocks {
+    int sink, t0, t1;
+    __device__ __forceinline__ int count() const { return sink + t1 - t0; }
+    __device__ __forceinline__ int at(int u) const { return u < t1 - t0 ? t1 - 1 - u : sink - 1 - (u - (t1 - t0)); }
+};
+
+// Positions p0 .. p1 of the tokens t .. t + count - 1 that exist (p0 > p1: none).
+__device__ __forceinline__ void positions(const AttnArgs& a, int64_t off, int t, int count, int& p0, int& p1)
+{
+    p0 = (int)min<int64_t>(max<int64_t>(off + t, 0), INT_MAX);
+    p1 = (int)max<int64_t>(min<int64_t>(off + t + count - 1, a.Lk - 1), -1);
+}
+
+// One block's bytes of a wave: the operands of lane (g, c), 16 bytes each.
+template <int J>
+struct Bytes {
+    uint4 k[4][J], v[4 * J];
+    // `chunk` 16-value chunks of D; a lane past them reads the first (its query values are 0)
+    __device__ __forceinline__ void from(const uint8_t* kp, const uint8_t* vp, int chunks, int g, int lane)
+    {
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int ch = 4 * j + g < chunks ? 4 * j + g : 0;
+                k[kb][j] = *(const uint4*)(kp + ((kb * chunks + ch) * 16 + (lane & 15)) * 16);
+            }
+#pragma unroll
+        for (int d = 0; d < 4 * J; ++d) v[d] = *(const uint4*)(vp + ((d < chunks ? d : 0) * 64 + lane) * 16);
+    }
+};
+
+template <class IO, Code CODE, int J, Cap CAP, bool BIAS, class S>
+__global__ __launch_bounds__((64 * S::NW), 2) void cached_attn(AttnArgs a, CacheArgs cc, int sinks)
+{
+    using E = typename IO::T;
+    constexpr int NQ = S::NQ, NW = S::NW, WM = S::WM, BM = S::BM, ND = 4 * J, P = IO::SIZE == 4 ? 2 : 1;
+    constexpr int DP = 64 * J, NS = 3, STAGE = 2 * T * DP;
+    // the ring of blocks, or what the waves join
+    constexpr int LDS = S::KEYS ? NW * WM * (DP + 2) * 4 : NS * STAGE;
+    __shared__ __attribute__((aligned(1024))) uint8_t sh[LDS];
+
+    uint32_t id = blockIdx.x;
+    const int bh = (int)(id % (uint32_t)a.nbh);
+    id /= (uint32_t)a.nbh;
+    const int split = (int)(id % (uint32_t)a.nsplit);
+    const int tile = a.ntile - 1 - (int)(id / (uint32_t)a.nsplit);   // the last rows see most keys: first
+    const int b = bh / a.Hkv, hk = bh % a.Hkv, chunks = a.D / 16;
+    const int64_t off = (int64_t)a.kv_len[b] - a.Lq;   // position of token 0
+    const int n = (int)min<int64_t>(max<int64_t>(off + a.Lq, 0), a.Lk);
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+    // this lane's rows
+    int row[NQ], pos[NQ], lo[NQ];
+    bool empty[NQ];
+    half8_t q[NQ][J][2][P];
+    float slope[NQ], back[NQ];   // back: what undoes the row's power of two, with the score's scale
+    const int rw = tile * BM + (S::KEYS ? 0 : wave * WM);   // the wave's first row
+    const float scale2 = score_scale<CAP>(a), cap2 = a.cap * LOG2E;
+#pragma unroll
+    for (int m = 0; m < NQ; ++m) {
+        row[m] = rw + 16 * m + c;
+        const bool in = row[m] < a.nrow;
+        const int i = in ? token_of(a, row[m]) : 0, h = in ? hk * a.G + row[m] - i * a.G : hk * a.G;
+        const int64_t p = off + i;
+        empty[m] = !in || p < 0 || p >= a.Lk;
+        // an empty row takes part with q = 0 and nothing masked; its result is dropped
+        pos[m] = empty[m] ? BIG : (int)p;
+        lo[m] = empty[m] ? 0 : max(0, (int)p - a.window + 1);
+        slope[m] = BIAS ? a.slopes[h] * LOG2E : 0.f;
+        const E* qp = (const E*)a.q + b * a.qs[0] + (int64_t)i * a.qs[1] + h * a.qs[2];
+        float x[J][2][8], top = 0.f;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int d = 16 * (4 * j + g) + 8 * k;
+                const bool on = !empty[m] && d < a.D;
+                const Frag<IO> f = frag_at<IO>(qp + (d < a.D ? d : 0));
+                if constexpr (IO::SIZE == 2) {
+                    const uint32_t w[4] = {f.v.x, f.v.y, f.v.z, f.v.w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[j][k][e] = __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+                } else {
+                    const float w[8] = {f.a.x, f.a.y, f.a.z, f.a.w, f.b.x, f.b.y, f.b.z, f.b.w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[j][k][e] = w[e];
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[j][k][e] = on ? x[j][k][e] : 0.f;
+                    top = fmaxf(top, fabsf(x[j][k][e]));
+                }
+            }
+        top = gmax(top);
+        const int ex = min((int)(__float_as_uint(top) >> 23), 254) - 127;
+        back[m] = __builtin_amdgcn_ldexpf(scale2, ex - Q_TOP);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[j][k][e] = __builtin_amdgcn_ldexpf(x[j][k][e], Q_TOP - ex);
+                q[m][j][k][0] = halves_of(x[j][k]);
+                if constexpr (P == 2) q[m][j][k][1] = rest_of(x[j][k], q[m][j][k][0]);
+            }
+    }
+    // what the wave's rows and the workgroup's see
+    int p0, p1, w0, w1;
+    {
+        const int t = token_of(a, min(tile * BM, a.nrow - 1));
+        positions(a, off, t, token_of(a, min(tile * BM + BM, a.nrow) - 1) - t + 1, p0, p1);
+        const int tw = token_of(a, min(rw, a.nrow - 1));
+        positions(a, off, tw, rw < a.nrow ? token_of(a, min(rw + WM, a.nrow) - 1) - tw + 1 : 0, w0, w1);
+    }
+    const int wlo = max(0, w0 - a.window + 1), wlast = max(0, w1 - a.window + 1);   // first keys of the wave's rows
+    Blocks bl = {0, 0, 0};
+    if (p0 <= p1) {
+        const int klo = max(0, p0 - a.window + 1);
+        bl.t0 = klo / T;
+        bl.t1 = p1 / T + 1;
+        bl.sink = min((min(sinks, klo) + T - 1) / T, bl.t0);
+    }
+    int u0 = 0, u1 = bl.count();
+    if (a.nsplit > 1) {
+        const int per = (u1 + a.nsplit - 1) / a.nsplit;
+        u0 = min(u1, split * per);
+        u1 = min(u1, u0 + per);
+    }
+
+    f32x4 o[ND][NQ];
+    float mx[NQ], sum[NQ];
+#pragma unroll
+    for (int m = 0; m < NQ; ++m) {
+        mx[m] = -INFINITY;
+        sum[m] = 0.f;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) o[d][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    const int64_t step = (int64_t)T * a.D;   // bytes of a block and head
+
+    // one block, its operands given by kf(kb, j) and vf(d)
+    auto block = [&](int j0, float ks, int ve, auto&& kf, auto&& vf) {
+        f32x4 s[4][NQ];
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {
+#pragma unroll
+            for (int m = 0; m < NQ; ++m) s[kb][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const uint4 u = kf(kb, j);
+                const half8_t f[2] = {halves8<CODE>(u.x, u.y), halves8<CODE>(u.z, u.w)};
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int m = 0; m < NQ; ++m)
+#pragma unroll
+                        for (int p = 0; p < P; ++p) s[kb][m] = mma(f[k], q[m][j][k][p], s[kb][m]);
+            }
+        }
+        const bool edge = j0 + T - 1 > w0 || (j0 < wlast && j0 + T > sinks);
+        const float vexp = (float)ve, vback = power(-ve);
+        half8_t w[NQ][2][P];
+#pragma unroll
+        for (int m = 0; m < NQ; ++m) {
+            // Scores in base 2 with the block's vs, less the row's base: the running maximum as it was
+            // when a score last passed it by SLACK.
+            const float base = mx[m] == -INFINITY ? 0.f : mx[m];
+            const float by = back[m] * ks;
+            const float shift = (BIAS ? slope[m] * (float)(j0 + 16 * g - pos[m]) : 0.f) + (vexp + HEAD - base);
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float add = BIAS ? __builtin_fmaf(slope[m], (float)(4 * kb + r), shift) : shift;
+                    if constexpr (CAP != UNCAPPED) s[kb][m][r] = __builtin_fmaf(cap2, tanh_of<IO, CAP>(s[kb][m][r] * by), add);
+                    else s[kb][m][r] = __builtin_fmaf(s[kb][m][r], by, add);
+                }
+            if (edge) {
+                keep_branch();
+                const int j = j0 + 16 * g;
+#pragma unroll
+                for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int key = j + 4 * kb + r;
+                        if (key > pos[m] || (key < lo[m] && key >= sinks)) s[kb][m][r] = -INFINITY;
+                    }
+            }
+            float top = s[0][m][0];
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) top = fmaxf(top, s[kb][m][r]);
+            const float limit = mx[m] == -INFINITY ? -INFINITY : HEAD + SLACK;
+            if (__any(top > limit)) {
+                top = gmax(top);
+                if (top > limit) {
+                    const float now = base + (top - HEAD), f = exp2_hw(mx[m] - now);
+                    sum[m] *= f;
+#pragma unroll
+                    for (int d = 0; d < ND; ++d) o[d][m] *= f;
+                    mx[m] = now;
+#pragma unroll
+                    for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) s[kb][m][r] -= top - HEAD;
+                }
+            }
+            float part = 0.f;
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float e = exp2_hw(s[kb][m][r]);
+                    s[kb][m][r] = e;
+                    part += e;
+                }
+            sum[m] = __builtin_fmaf(part, vback, sum[m]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float x[8] = {s[2 * k][m][0], s[2 * k][m][1], s[2 * k][m][2], s[2 * k][m][3],
+                                    s[2 * k + 1][m][0], s[2 * k + 1][m][1], s[2 * k + 1][m][2], s[2 * k + 1][m][3]};
+                w[m][k][0] = halves_of(x);
+                if constexpr (P == 2) w[m][k][1] = rest_of(x, w[m][k][0]);
+            }
+        }
+        // e4m3 bytes behind the sequence's last token may stand for NaN: weight 0 does not hide it
+        const int left = n - j0 - 16 * g;
+        const bool tail = CODE == Code::E4M3 && j0 + T > n;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+            if (16 * d >= a.D) break;
+            uint4 u = vf(d);
+            if (tail) {
+                keep_branch();
+                uint32_t* x = (uint32_t*)&u;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int keep = left - 4 * k;
+                    x[k] &= keep >= 4 ? ~0u : keep <= 0 ? 0u : (1u << (8 * keep)) - 1;
+                }
+            }
+            const half8_t f[2] = {halves8<CODE>(u.x, u.y), halves8<CODE>(u.z, u.w)};
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int m = 0; m < NQ; ++m)
+#pragma unroll
+                    for (int p = 0; p < P; ++p) o[d][m] = mma(f[k], w[m][k][p], o[d][m]);
+        }
+    };
+
+    if constexpr (S::KEYS) {
+        // this wave's blocks: u0 + wave, + NW, ...
+        Bytes<J> now, next;
+        auto fetch = [&](int u, Bytes<J>& to) -> int {
+            const int p = block_of(cc, b, bl.at(u));
+            const int64_t at = ((int64_t)max(p, 0) * a.Hkv + hk) * step;
+            to.from((const uint8_t*)cc.k + at, (const uint8_t*)cc.v + at, chunks, g, lane);
+            return p;
+        };
+        int u = u0 + wave, p = -1;
+        if (u < u1) p = fetch(u, now);
+        for (; u < u1; u += NW) {
+            int pn = -1;
+            if (u + NW < u1) pn = fetch(u + NW, next);
+            if (p >= 0) {
+                const int64_t at = (int64_t)p * a.Hkv + hk;
+                block(bl.at(u) * T, power(exponent_at(cc.ks + at)), exponent_at(cc.vs + at),
+                      [&](int kb, int j) { return now.k[kb][j]; }, [&](int d) { return now.v[d]; });
+            }
+            now = next;
+            p = pn;
+        }
+        // join the waves: their rows' base, sum and o
+        float* st = (float*)sh;                  // [wave][2][16]
+        float* ow = st + NW * 2 * 16;            // [wave][16 rows][DP]
+        const float l = gsum(sum[0]);
+        if (g == 0) {
+            st[(wave * 2) * 16 + c] = mx[0];
+            st[(wave * 2 + 1) * 16 + c] = l;
+        }
+#pragma unroll
+        for (int d = 0; d < ND; ++d) *(float4*)(ow + (wave * 16 + c) * DP + 16 * d + 4 * g) = make_float4(o[d][0][0], o[d][0][1], o[d][0][2], o[d][0][3]);
+        __syncthreads();
+        // wave w writes a quarter of each row's values
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) top = fmaxf(top, st[(w * 2) * 16 + c]);
+        float f[NW], all = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float x = st[(w * 2) * 16 + c];
+            f[w] = x == -INFINITY ? 0.f : exp2_hw(x - top);
+            all = __builtin_fmaf(f[w], st[(w * 2 + 1) * 16 + c], all);
+        }
+        const bool none = empty[0] || all == 0.f;
+        const float inv = none ? 0.f : 1.0f / all;
+        const float ls = none ? -INFINITY : top - HEAD + __builtin_amdgcn_logf(all);
+        if (row[0] >= a.nrow) return;
+        const int i = token_of(a, row[0]), h = hk * a.G + row[0] - i * a.G;
+        const int64_t at = ((int64_t)split * a.nbh + bh) * a.nrow + row[0];
+#pragma unroll
+        for (int d = 0; d < DP; d += 16 * NW) {
+            const int d0 = d + 16 * wave + 4 * g;
+            if (d0 >= a.D) continue;
+            f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float4 y = *(const float4*)(ow + (w * 16 + c) * DP + d0);
+                x += f32x4{y.x, y.y, y.z, y.w} * f[w];
+            }
+            x = none ? f32x4{0.f, 0.f, 0.f, 0.f} : x * inv;
+            if (a.nsplit > 1) *(float4*)(a.part + at * a.D + d0) = make_float4(x[0], x[1], x[2], x[3]);
+            else put4<IO>((E*)a.o + b * a.os[0] + (int64_t)i * a.os[1] + h * a.os[2] + d0, x);
+        }
+        if (wave == 0 && g == 0) {
+            if (a.nsplit > 1) a.part_lse[at] = ls;
+            else if (a.lse) a.lse[((int64_t)b * a.H + h) * a.Lq + i] = ls * LN2;
+        }
+    } else {
+        // D / 8 kilobytes a block (k, then v): every wave brings the same number, the last ones twice
+        const int kilo = a.D / 8, rounds = (kilo + NW - 1) / NW;
+        int blk[NS];   // the pool's block in each place
+        auto issue = [&](int u, int place) {
+            const int p = block_of(cc, b, bl.at(u));
+            const int64_t at = ((int64_t)max(p, 0) * a.Hkv + hk) * step;
+#pragma unroll
+            for (int i = 0; i < DP / 8 / NW; ++i) {
+                if (i >= rounds) break;
+                const int k = min(i * NW + wave, kilo - 1), half = kilo / 2;
+                const uint8_t* src = (k < half ? (const uint8_t*)cc.k + at + k * 1024 : (const uint8_t*)cc.v + at + (k - half) * 1024) + lane * 16;
+                load_lds16(src, __builtin_amdgcn_readfirstlane(lds_offset(sh) + place * STAGE + k * 1024));
+            }
+            return p;
+        };
+        auto wait_but = [&](int stages) {   // all but the last `stages` stages' loads have arrived
+            if (stages == 0) wait_loads<0>();
+            else if (rounds == 1) wait_loads<1>();
+            else if (rounds == 2) wait_loads<2>();
+            else if (rounds == 3) wait_loads<3>();
+            else wait_loads<4>();
+        };
+        for (int s = 0; s < NS - 1; ++s) blk[s] = u0 + s < u1 ? issue(u0 + s, s) : -1;
+        int place = 0;
+        for (int u = u0; u < u1; ++u) {
+            wait_but(u + 1 < u1 ? 1 : 0);
+            stage_barrier();
+            const int j0 = bl.at(u) * T, p = blk[0];
+            blk[0] = blk[1];
+            if (u + NS - 1 < u1) blk[1] = issue(u + NS - 1, place == 0 ? NS - 1 : place - 1);
+            const uint8_t* kt = sh + place * STAGE;
+            const uint8_t* vt = kt + T * a.D;
+            place = place + 1 == NS ? 0 : place + 1;
+            if (p < 0 || w0 > w1 || j0 > w1 || (j0 + T - 1 < wlo && j0 >= sinks)) continue;
+            const int64_t at = (int64_t)p * a.Hkv + hk;
+            block(j0, power(exponent_at(cc.ks + at)), exponent_at(cc.vs + at),
+                  [&](int kb, int j) {
+                      const int ch = 4 * j + g < chunks ? 4 * j + g : 0;
+                      return *(const uint4*)(kt + ((kb * chunks + ch) * 16 + c) * 16);
+                  },
+                  [&](int d) { return *(const uint4*)(vt + (d * 64 + lane) * 16); });
+        }
+#pragma unroll
+        for (int m = 0; m < NQ; ++m) {
+            const float l = gsum(sum[m]);
+            if (row[m] >= a.nrow) continue;
+            const bool none = empty[m] || l == 0.f;
+            const float inv = none ? 0.f : 1.0f / l;
+            const float ls = none ? -INFINITY : mx[m] - HEAD + __builtin_amdgcn_logf(l);
+            const int i = token_of(a, row[m]), h = hk * a.G + row[m] - i * a.G;
+            const int64_t at = ((int64_t)split * a.nbh + bh) * a.nrow + row[m];
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                const int d0 = 16 * d + 4 * g;
+                if (d0 >= a.D) continue;
+                const f32x4 x = none ? f32x4{0.f, 0.f, 0.f, 0.f} : o[d][m] * inv;
+                if (a.nsplit > 1) *(float4*)(a.part + at * a.D + d0) = make_float4(x[0], x[1], x[2], x[3]);
+                else put4<IO>((E*)a.o + b * a.os[0] + (int64_t)i * a.os[1] + h * a.os[2] + d0, x);
+            }
+            if (g != 0) continue;
+            if (a.nsplit > 1) a.part_lse[at] = ls;
+            else if (a.lse) a.lse[((int64_t)b * a.H + h) * a.Lq + i] = ls * LN2;
+        }
+    }
+}
+
+// Rows of a workgroup: 16 shared by four waves for the few rows of decoding, else 64 or 128.
+constexpr int FEW = 16;
+constexpr int64_t TWO_A_CU = 512;
+int tile_rows(const AttnArgs& a)
+{
+    if (a.nrow <= FEW) return 16;
+    return (a.nrow + 127) / 128 * (int64_t)a.nbh <= TWO_A_CU ? 64 : 128;
+}
+
+// Key splits while the rows do not fill the GPU, each of at least SPLIT_MIN keys.
+constexpr int64_t FILL = 512, FILL_FEW = 768, SPLIT_MIN = 512;
+constexpr int64_t SPLIT_MAX = 64;   // the join weighs one split a lane
+
+int splits(const AttnArgs& a, int sinks)
+{
+    const int bm = tile_rows(a);
+    const int64_t wgs = (a.nrow + bm - 1) / bm * (int64_t)a.nbh, fill = a.nrow <= FEW ? FILL_FEW : FILL;
+    const int64_t keys = std::min<int64_t>(a.Lk, (int64_t)a.window + sinks + std::min<int64_t>(a.Lq, bm));
+    if (wgs <= 0 || 2 * wgs > fill) return 1;
+    return (int)std::max<int64_t>(1, std::min<int64_t>({(fill + wgs - 1) / wgs, keys / SPLIT_MIN, SPLIT_MAX}));
+}
+
+template <class IO, Code CODE, int J, class S>
+hipError_t go(AttnArgs a, const CacheArgs& c, int sinks, hipStream_t st)
+{
+    a.ntile = (a.nrow + S::BM - 1) / S::BM;
+    const int64_t blocks = (int64_t)a.ntile * a.nbh * a.nsplit;
+    if (!grid_ok(blocks, 64 * S::NW)) return hipErrorInvalidValue;
+    return with_options<IO, false>(a, [&](auto cap, auto bias) {
+        hipLaunchKernelGGL((cached_attn<IO, CODE, J, decltype(cap)::value, decltype(bias)::value, S>), dim3((unsigned)blocks),
+                           dim3(64 * S::NW), 0, st, a, c, sinks);
+        return hipGetLastError();
+    });
+}
+
+template <class IO, Code CODE, int J>
+hipError_t shape(const AttnArgs& a, const CacheArgs& c, int sinks, hipStream_t st)
+{
+    switch (tile_rows(a)) {
+    case 16: return go<IO, CODE, J, Shape<1, 4, true>>(a, c, sinks, st);
+    case 64: return go<IO, CODE, J, Shape<1, 4, false>>(a, c, sinks, st);
+    default: return go<IO, CODE, J, Shape<2, 4, false>>(a, c, sinks, st);
+    }
+}
+
+template <class IO, Code CODE>
+hipError_t run(AttnArgs a, const CacheArgs& c, int sinks, Store s, hipStream_t st)
+{
+    a.nsplit = splits(a, sinks);
+    a.part_lse = a.part + (int64_t)a.nsplit * a.nbh * a.nrow * a.D;
+    const hipError_t e = a.D <= 64 ? shape<IO, CODE, 1>(a, c, sinks, st) : shape<IO, CODE, 2>(a, c, sinks, st);
+    return e != hipSuccess || a.nsplit == 1 ? e : launch_attn_join(s, a, st);
+}
+
+}  // namespace
+
+size_t cached_attn_bytes(const AttnArgs& a, int sinks)
+{
+    const int ns = splits(a, sinks);
+    return ns > 1 ? (size_t)ns * a.nbh * a.nrow * (a.D + 1) * sizeof(float) : 0;
+}
+
+hipError_t launch_cached_attn(Store s, Code code, const AttnArgs& a, const CacheArgs& c, int sinks, void* ws, hipStream_t st)
+{
+    AttnArgs x = a;
+    x.part = (float*)ws;
+    if (s == Store::F32)
+        return code == Code::I8 ? run<f32_io, Code::I8>(x, c, sinks, s, st) : run<f32_io, Code::E4M3>(x, c, sinks, s, st);
+    return code == Code::I8 ? run<bf16_io, Code::I8>(x, c, sinks, s, st) : run<bf16_io, Code::E4M3>(x, c, sinks, s, st);
+}
+
+}  // namespace sc

@@ -328,5 +328,58 @@ size_t attn_fwd_bytes(const AttnArgs& a);
 hipError_t launch_attn(Store st, const AttnArgs& a, void* ws, hipStream_t stream);
 size_t attn_bwd_bytes(const AttnArgs& a);
 hipError_t launch_attn_bwd(Store st, const AttnArgs& a, void* ws, hipStream_t stream);
+// Joins the nsplit parts of a call's rows (part, part_lse set) into o and lse.
+hipError_t launch_attn_join(Store st, const AttnArgs& a, hipStream_t stream);
+
+// Norm of the rows of q and k (x w rstd, rstd = (mean x^2 + eps)^-1/2) and rotation of their first R
+// values by the token's position times freq (sc_qknorm.hip); index 0 is q, 1 is k.  Strides: batch,
+// token, head.
+struct QkArgs {
+    const void* x[2];
+    void* y[2];              // backward: dx
+    const void* dy[2];       // backward
+    const void* w[2];        // (D) or null: 1
+    void* dw[2];             // backward, or null
+    int64_t xs[2][3], ys[2][3], dys[2][3];
+    const float* freq;       // (R / 2)
+    const int32_t* pos;      // (B, L) or null
+    const int32_t* len;      // (B) or null
+    int64_t B, L, tokens;    // tokens = B L
+    int H[2], D, R;
+    float eps;
+    bool pairs;              // values 2 i and 2 i + 1 turn together, not i and i + R / 2
+    bool whole;              // every row starts 16-byte aligned
+    // set by the launchers
+    int tb;                  // tokens of a workgroup at a time
+    float* part;             // backward: sums of dw by workgroup
+};
+hipError_t launch_qk(Store st, const QkArgs& a, hipStream_t stream);
+size_t qk_bwd_bytes(Store st, const QkArgs& a);
+hipError_t launch_qk_bwd(Store st, const QkArgs& a, void* ws, hipStream_t stream);
+
+// A cache of 8-bit codes in blocks of 64 tokens of a head (layout and rounding in sc_cache.h).
+enum class Code { I8, E4M3 };
+struct CacheArgs {
+    void *k, *v;             // codes of block p, head h from (p Hkv + h) 64 D on
+    float *ks, *vs;          // scales (P, Hkv)
+    const int32_t* table;    // (B, N): a row's blocks, or null: b N + i
+    int B, N, P, Hkv, D;
+};
+// Token i < L of row b stands at position len[b] - L + i; k and v strides: batch, token, head.
+struct CacheIo {
+    const void *k, *v;       // write: the tokens
+    void *ko, *vo;           // read: where they go
+    int64_t kst[3], vst[3];
+    const int32_t* len;
+    int L;
+};
+hipError_t launch_cache_write(Store st, Code code, const CacheArgs& c, const CacheIo& io, hipStream_t stream);
+hipError_t launch_cache_read(Store st, Code code, const CacheArgs& c, const CacheIo& io, hipStream_t stream);
+
+// Attention over such a cache (sc_cached_attn.hip): q, o, lse, slopes, kv_len, sizes, window, scale and
+// cap of `a`, whose Lk is the cache's 64 N; the first `sinks` keys are visible past the window.
+size_t cached_attn_bytes(const AttnArgs& a, int sinks);
+hipError_t launch_cached_attn(Store st, Code code, const AttnArgs& a, const CacheArgs& c, int sinks,
+                              void* ws, hipStream_t stream);
 
 }  // namespace sc

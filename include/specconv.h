@@ -530,6 +530,111 @@ sc_status sc_causal_attn_bwd(sc_kind kind, const sc_attn* a, const void* dout, c
                              hipStream_t stream);
 
 /*
+ * Norm and rotation of q and k before attention.  For each row x of D values (one head of one token of
+ * q or k) with weight w (D values of the call's kind, or null: 1):
+ *     n = x w / sqrt(mean(x^2) + eps)
+ * and the first R values of n (R even, R <= D) are turned in pairs (n_a, n_b) by theta = p inv_freq[i]:
+ *     y_a = n_a cos theta - n_b sin theta,   y_b = n_b cos theta + n_a sin theta
+ * pair i being the values i and i + R / 2, or 2 i and 2 i + 1 (interleaved = 1); values from R on stay n.
+ * p is the token's position: positions[b][t], or kv_len[b] - L + t (the last L positions of each
+ * sequence, as attention counts them; not both), or t.  The angle is taken in 64 bits, so it is good to
+ * float32 precision at any position (exactly p times the float32 inv_freq for |p| < 2^29).
+ *
+ *  sc_qk_norm_rotary -- q (B, L, H, D) to q_out, k (B, L, Hkv, D) to k_out; with no heads of one of
+ *      them its pointers are not looked at.  q_out may be q itself (the same pointer and strides), k_out
+ *      k.  No other overlap.
+ *  sc_qk_norm_rotary_bwd -- for the output gradients dq_out, dk_out (strides q_out, k_out), from the
+ *      inputs q, k: dq, dk, and the gradients of the weights dwq, dwk (D values, or null: not wanted; of
+ *      a null weight: of ones).  ws: sc_qk_norm_rotary_workspace_bytes(kind, a) bytes with dwq or dwk,
+ *      else 0.  Without tokens or heads dwq and dwk are set to zero.
+ * Strides are in elements, {batch, token, head}; the D values are contiguous, D <= 512.  Rows that all
+ * start 16-byte aligned, with D (and, for halves, R) a multiple of 32 bytes, are moved in vectors; any
+ * others work, slower.  A row of NaN or infinity affects itself (and dw) only.
+ */
+typedef struct sc_qk {
+    int64_t B, L, H, Hkv, D, R;
+    int64_t q[3], k[3], q_out[3], k_out[3];
+    int64_t dq[3], dk[3];                    /* sc_qk_norm_rotary_bwd only */
+    float eps;                               /* >= 0 */
+    int32_t interleaved;
+    const float* inv_freq;                   /* (R / 2), radians a position; null with R = 0 */
+    const int32_t* positions;                /* (B, L) or null */
+    const int32_t* kv_len;                   /* (B) or null    */
+} sc_qk;
+sc_status sc_qk_norm_rotary(sc_kind kind, const sc_qk* a, const void* q, const void* k, const void* wq,
+                            const void* wk, void* q_out, void* k_out, hipStream_t stream);
+size_t sc_qk_norm_rotary_workspace_bytes(sc_kind kind, const sc_qk* a);
+sc_status sc_qk_norm_rotary_bwd(sc_kind kind, const sc_qk* a, const void* dq_out, const void* dk_out,
+                                const void* q, const void* k, const void* wq, const void* wk, void* dq,
+                                void* dk, void* dwq, void* dwk, void* ws, size_t ws_bytes,
+                                hipStream_t stream);
+
+/*
+ * A cache of k and v in 8 bits.  SC_CACHE_BLOCK = 64 consecutive tokens of one key head are a block; its
+ * k and its v have one scale each, a power of two 2^e, and a value is held as code * 2^e:
+ *     e = the smallest in -60 .. 60 with max |x| <= Q 2^e over the block,
+ *     code = x / 2^e rounded once (ties to even) to an integer of -127 .. 127 (SC_CODE_I8, Q = 127) or
+ *     to an e4m3 value (SC_CODE_E4M3, Q = 448: 4 exponent and 3 mantissa bits, subnormals down to 2^-9).
+ * Infinities count as the largest code and not towards max |x| (as do values past Q 2^60); NaN is 0 in
+ * int8 and stays NaN in e4m3.  When tokens are appended to a block that holds older ones, its exponent
+ * is the larger of the one it has and the new tokens'; where it grows, the older codes are rounded again
+ * at the new scale.
+ *
+ * sc_cache describes the memory, which the caller owns: P blocks of Hkv heads, codes in k and v of
+ * P Hkv 64 D bytes each (16-byte aligned; their order inside a block is the library's own: read them
+ * through sc_cache_read), scales k_scale, v_scale (P, Hkv) float32.  Sequence b < B holds up to 64 N
+ * tokens; its block i (tokens 64 i .. 64 i + 63) is table[b][i], or b N + i without a table (then
+ * P >= B N).  A table entry outside 0 .. P - 1 is no block: writes to it are dropped, it reads as 0 and
+ * attention sees none of its keys.  Blocks that one call writes must be distinct; blocks that are only
+ * read may be shared by sequences.  D is a multiple of 16 up to 128, 64 N <= 2^30, B Hkv < 2^31 (else
+ * SC_ERR_UNSUPPORTED).  The memory needs no initial value.
+ *
+ * In all three calls kv_len (B) int32 is each sequence's length with the call's tokens: token i < L of
+ * sequence b stands at position kv_len[b] - L + i.  Positions below 0 or from 64 N on do not exist:
+ * their tokens are not written, read as 0, and see nothing.  Strides are in elements, {batch, token,
+ * head}; rows are 16-byte aligned.
+ *
+ *  sc_cache_write -- stores k, v (B, L, Hkv, D).  What a sequence held at kv_len[b] and beyond is given up.
+ *  sc_cache_read -- the values of the last L positions as k, v (B, L, Hkv, D): exact, but for bfloat16
+ *      results of magnitudes below its range.
+ *  sc_cached_attn -- causal attention of q (B, Lq, H, D) over the cache, as sc_causal_attn: query i at
+ *      position p = kv_len[b] - Lq + i sees key j <= p when j > p - window (window 0: always) or
+ *      j < sinks, the first tokens that stay visible;
+ *          x = scale q_i . k_j,   s = cap tanh(x / cap) (cap > 0) or x,   s -= slopes[h] (p - j)
+ *          o_i = sum_j softmax(s)_j v_j,   lse_i = log sum_j exp(s_j)  (lse (B, H, Lq) float32 or null)
+ *      A row that sees nothing gives o = 0, lse = -infinity.  Products run on the codes in half precision
+ *      with float32 sums: a query row enters scaled by a power of two (bfloat16 exact down to 2^-29 of
+ *      its largest value, float32 as two halves), weights with 11 bits (float32: two halves).  Cached
+ *      values of existing positions must be finite (an e4m3 NaN may reach other rows).  H a multiple of
+ *      Hkv; ws as for sc_causal_attn, sc_cached_attn_workspace_bytes(kind, c, a) bytes.
+ */
+#define SC_CACHE_BLOCK 64
+enum { SC_CODE_I8 = 0, SC_CODE_E4M3 = 1 };
+typedef struct sc_cache {
+    int64_t B, N, P, Hkv, D;
+    int32_t code;
+    void *k, *v;
+    float *k_scale, *v_scale;
+    const int32_t* table;      /* (B, N) or null */
+} sc_cache;
+typedef struct sc_cached {
+    int64_t Lq, H;
+    int64_t q[3], o[3];        /* strides */
+    float scale, cap;          /* > 0; >= 0 (0: none) */
+    int64_t window, sinks;
+    const float* slopes;       /* (H) or null */
+    const int32_t* kv_len;     /* (B) */
+} sc_cached;
+sc_status sc_cache_write(sc_kind kind, const sc_cache* c, const void* k, const int64_t k_strides[3],
+                         const void* v, const int64_t v_strides[3], int64_t L, const int32_t* kv_len,
+                         hipStream_t stream);
+sc_status sc_cache_read(sc_kind kind, const sc_cache* c, void* k, const int64_t k_strides[3], void* v,
+                        const int64_t v_strides[3], int64_t L, const int32_t* kv_len, hipStream_t stream);
+size_t sc_cached_attn_workspace_bytes(sc_kind kind, const sc_cache* c, const sc_cached* a);
+sc_status sc_cached_attn(sc_kind kind, const sc_cache* c, const sc_cached* a, const void* q, void* o,
+                         float* lse, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
  * sc_ntt_range_ok -- 1 if every |v_j| <= max_abs_v and |g_j| <= max_abs_g guarantee that
  *   the exact sums fit the symmetric residue range, i.e. L * max_abs_v * max_abs_g <=
  *   (p-1)/2; 0 otherwise (or on negative arguments).  Host only.
