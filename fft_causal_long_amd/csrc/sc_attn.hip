@@ -397,21 +397,16 @@ hipError_t shape(const AttnArgs& a, hipStream_t st)
 }
 
 template <class IO>
-hipError_t join(const AttnArgs& a, hipStream_t st)
-{
-    const int64_t rows = (int64_t)a.nbh * a.nrow;
-    if (!grid_ok(rows, NT)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((attn_join<IO>), dim3((unsigned)rows), dim3(NT), 0, st, a);
-    return hipGetLastError();
-}
-
-template <class IO>
 hipError_t run(AttnArgs a, hipStream_t st)
 {
     a.nsplit = splits(a);
     a.part_lse = a.part + (int64_t)a.nsplit * a.nbh * a.nrow * a.D;
     const hipError_t e = a.D <= 64 ? shape<IO, 64>(a, st) : shape<IO, 128>(a, st);
-    return e != hipSuccess || a.nsplit == 1 ? e : join<IO>(a, st);
+    if (e != hipSuccess || a.nsplit == 1) return e;
+    const int64_t rows = (int64_t)a.nbh * a.nrow;
+    if (!grid_ok(rows, NT)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((attn_join<IO>), dim3((unsigned)rows), dim3(NT), 0, st, a);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -427,11 +422,6 @@ hipError_t launch_attn(Store s, const AttnArgs& a, void* ws, hipStream_t st)
     AttnArgs x = a;
     x.part = (float*)ws;
     return s == Store::F32 ? run<f32_io>(x, st) : run<bf16_io>(x, st);
-}
-
-hipError_t launch_attn_join(Store s, const AttnArgs& a, hipStream_t st)
-{
-    return s == Store::F32 ? join<f32_io>(a, st) : join<bf16_io>(a, st);
 }
 
 }  // namespace sc

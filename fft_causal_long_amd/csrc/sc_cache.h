@@ -59,9 +59,9 @@ __device__ __forceinline__ int exponent_of(float top)
 }
 __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 // The exponent of a stored scale (whatever memory holds is brought into range).
-__device__ __forceinline__ int exponent_at(const float* scale)
+__device__ __forceinline__ int exponent_of_scale(float scale)
 {
-    return min(max((int)(__float_as_uint(*scale) >> 23 & 255) - 127, E_LOW), E_HIGH);
+    return min(max((int)(__float_as_uint(scale) >> 23 & 255) - 127, E_LOW), E_HIGH);
 }
 
 // A magnitude for the largest: infinities and NaN do not count.

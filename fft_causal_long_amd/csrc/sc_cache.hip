@@ -124,7 +124,7 @@ __global__ __launch_bounds__(NT) void cache_put(CacheArgs c, CacheIo io, int nbl
             mx = fmaxf(mx, magnitude(x[i][e]));
         }
     }
-    const int had = from ? exponent_at(scale) : E_LOW;
+    const int had = from ? exponent_of_scale(*scale) : E_LOW;
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) mx = fmaxf(mx, __shfl_xor(mx, m));
     if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = mx;
@@ -217,7 +217,7 @@ __global__ __launch_bounds__(NT) void cache_get(CacheArgs c, CacheIo io, int nbl
     const int from = (int)(start > at0 ? start - at0 : 0), to = (int)(end - at0 < T ? end - at0 : T);
     const int64_t* st = is_v ? io.vst : io.kst;
     E* dst = (E*)(is_v ? io.vo : io.ko) + b * st[0] + h * st[2];
-    const float scale = p < 0 ? 0.f : power(exponent_at((is_v ? c.vs : c.ks) + (int64_t)p * c.Hkv + h));
+    const float scale = p < 0 ? 0.f : power(exponent_of_scale((is_v ? c.vs : c.ks)[(int64_t)p * c.Hkv + h]));
     const uint8_t* in = (const uint8_t*)(is_v ? c.v : c.k) + ((int64_t)(p < 0 ? 0 : p) * c.Hkv + h) * T * D;
     const int row = (D + PAD) / 4;
     if (is_v && p >= 0) {

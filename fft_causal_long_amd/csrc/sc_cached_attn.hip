@@ -19,8 +19,8 @@
 //
 // Few rows (decoding): the four waves of a workgroup share 16 rows and take blocks in turn, each with
 // its next block on its way in registers, and join their results through LDS; keys are split over
-// workgroups to fill the GPU.  More rows: a wave has rows of its own and the workgroup's blocks come by
-// asynchronous loads into a ring of three LDS places.
+// workgroups to fill the GPU.  More rows: a wave has rows of its own; a block's codes are turned into
+// half precision once, a quarter by each wave, and shared through two LDS places.
 
 #include <hip/hip_runtime.h>
 
@@ -83,11 +83,40 @@ struct Blocks {
 // Positions p0 .. p1 of the tokens t .. t + count - 1 that exist (p0 > p1: none).
 __device__ __forceinline__ void positions(const AttnArgs& a, int64_t off, int t, int count, int& p0, int& p1)
 {
-    p0 = (int)min<int64_t>(max<int64_t>(off + t, 0), INT_MAX);
-    p1 = (int)max<int64_t>(min<int64_t>(off + t + count - 1, a.Lk - 1), -1);
+    p0 = (int)std::min<int64_t>(std::max<int64_t>(off + t, 0), INT_MAX);
+    p1 = (int)std::max<int64_t>(std::min<int64_t>(off + t + count - 1, a.Lk - 1), -1);
 }
 
+// Read once: past the caches' own keeping.
+__device__ __forceinline__ uint4 stream16(const uint8_t* p)
+{
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const u32x4 x = __builtin_nontemporal_load((const u32x4*)p);
+    return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
+// A block of a row and head: where it lies in the pool (-1: none) and its scales, loaded with its codes.
+struct Place {
+    int p;
+    float ks, vs;
+    __device__ __forceinline__ Place(const CacheArgs& c, int b, int hk, int blk) : p(block_of(c, b, blk))
+    {
+        const int64_t at = (int64_t)std::max(p, 0) * c.Hkv + hk;
+        ks = c.ks[at];
+        vs = c.vs[at];
+    }
+    __device__ __forceinline__ Place() : p(-1), ks(0.f), vs(0.f) {}
+    __device__ __forceinline__ int64_t bytes(const CacheArgs& c, int hk) const
+    {
+        return ((int64_t)std::max(p, 0) * c.Hkv + hk) * (T * c.D);
+    }
+};
+
 // One block's bytes of a wave: the operands of lane (g, c), 16 bytes each.
+template <int J>
+struct Bytes;
+template <>
+struct Bytes<0> {};
 template <int J>
 struct Bytes {
     uint4 k[4][J], v[4 * J];
@@ -99,10 +128,10 @@ struct Bytes {
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const int ch = 4 * j + g < chunks ? 4 * j + g : 0;
-                k[kb][j] = *(const uint4*)(kp + ((kb * chunks + ch) * 16 + (lane & 15)) * 16);
+                k[kb][j] = stream16(kp + ((kb * chunks + ch) * 16 + (lane & 15)) * 16);
             }
 #pragma unroll
-        for (int d = 0; d < 4 * J; ++d) v[d] = *(const uint4*)(vp + ((d < chunks ? d : 0) * 64 + lane) * 16);
+        for (int d = 0; d < 4 * J; ++d) v[d] = stream16(vp + ((d < chunks ? d : 0) * 64 + lane) * 16);
     }
 };
 
@@ -111,9 +140,9 @@ __global__ __launch_bounds__((64 * S::NW), 2) void cached_attn(AttnArgs a, Cache
 {
     using E = typename IO::T;
     constexpr int NQ = S::NQ, NW = S::NW, WM = S::WM, BM = S::BM, ND = 4 * J, P = IO::SIZE == 4 ? 2 : 1;
-    constexpr int DP = 64 * J, NS = 3, STAGE = 2 * T * DP;
-    // the ring of blocks, or what the waves join
-    constexpr int LDS = S::KEYS ? NW * WM * (DP + 2) * 4 : NS * STAGE;
+    constexpr int DP = 64 * J, STAGE = 2 * T * DP * 2;
+    // what the waves join, or two blocks in half precision
+    constexpr int LDS = S::KEYS ? NW * WM * (DP + 2) * 4 : 2 * STAGE;
     __shared__ __attribute__((aligned(1024))) uint8_t sh[LDS];
 
     uint32_t id = blockIdx.x;
@@ -123,16 +152,51 @@ __global__ __launch_bounds__((64 * S::NW), 2) void cached_attn(AttnArgs a, Cache
     const int tile = a.ntile - 1 - (int)(id / (uint32_t)a.nsplit);   // the last rows see most keys: first
     const int b = bh / a.Hkv, hk = bh % a.Hkv, chunks = a.D / 16;
     const int64_t off = (int64_t)a.kv_len[b] - a.Lq;   // position of token 0
-    const int n = (int)min<int64_t>(max<int64_t>(off + a.Lq, 0), a.Lk);
+    const int n = (int)std::min<int64_t>(std::max<int64_t>(off + a.Lq, 0), a.Lk);
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+    // what the wave's rows and the workgroup's see
+    const int rw = tile * BM + (S::KEYS ? 0 : wave * WM);   // the wave's first row
+    int p0, p1, w0, w1;
+    {
+        const int t = token_of(a, min(tile * BM, a.nrow - 1));
+        positions(a, off, t, token_of(a, min(tile * BM + BM, a.nrow) - 1) - t + 1, p0, p1);
+        const int tw = token_of(a, min(rw, a.nrow - 1));
+        positions(a, off, tw, rw < a.nrow ? token_of(a, min(rw + WM, a.nrow) - 1) - tw + 1 : 0, w0, w1);
+    }
+    const int wlo = max(0, w0 - a.window + 1), wlast = max(0, w1 - a.window + 1);   // first keys of the wave's rows
+    Blocks bl = {0, 0, 0};
+    if (p0 <= p1) {
+        const int klo = max(0, p0 - a.window + 1);
+        bl.t0 = klo / T;
+        bl.t1 = p1 / T + 1;
+        bl.sink = min((min(sinks, klo) + T - 1) / T, bl.t0);
+    }
+    int u0 = 0, u1 = bl.count();
+    if (a.nsplit > 1) {
+        const int per = (u1 + a.nsplit - 1) / a.nsplit;
+        u0 = min(u1, split * per);
+        u1 = min(u1, u0 + per);
+    }
+
+    // KEYS: this wave's blocks are u0 + wave, + NW, ...; the first is on its way before the queries are
+    Bytes<S::KEYS ? J : 0> now, next;
+    auto bring = [&](int u, auto& to) {
+        const Place p(cc, b, hk, bl.at(u));
+        const int64_t at = p.bytes(cc, hk);
+        to.from((const uint8_t*)cc.k + at, (const uint8_t*)cc.v + at, chunks, g, lane);
+        return p;
+    };
+    Place here;
+    if constexpr (S::KEYS)
+        if (u0 + wave < u1) here = bring(u0 + wave, now);
 
     // this lane's rows
     int row[NQ], pos[NQ], lo[NQ];
     bool empty[NQ];
     half8_t q[NQ][J][2][P];
     float slope[NQ], back[NQ];   // back: what undoes the row's power of two, with the score's scale
-    const int rw = tile * BM + (S::KEYS ? 0 : wave * WM);   // the wave's first row
     const float scale2 = score_scale<CAP>(a), cap2 = a.cap * LOG2E;
 #pragma unroll
     for (int m = 0; m < NQ; ++m) {
@@ -182,29 +246,6 @@ __global__ __launch_bounds__((64 * S::NW), 2) void cached_attn(AttnArgs a, Cache
                 if constexpr (P == 2) q[m][j][k][1] = rest_of(x[j][k], q[m][j][k][0]);
             }
     }
-    // what the wave's rows and the workgroup's see
-    int p0, p1, w0, w1;
-    {
-        const int t = token_of(a, min(tile * BM, a.nrow - 1));
-        positions(a, off, t, token_of(a, min(tile * BM + BM, a.nrow) - 1) - t + 1, p0, p1);
-        const int tw = token_of(a, min(rw, a.nrow - 1));
-        positions(a, off, tw, rw < a.nrow ? token_of(a, min(rw + WM, a.nrow) - 1) - tw + 1 : 0, w0, w1);
-    }
-    const int wlo = max(0, w0 - a.window + 1), wlast = max(0, w1 - a.window + 1);   // first keys of the wave's rows
-    Blocks bl = {0, 0, 0};
-    if (p0 <= p1) {
-        const int klo = max(0, p0 - a.window + 1);
-        bl.t0 = klo / T;
-        bl.t1 = p1 / T + 1;
-        bl.sink = min((min(sinks, klo) + T - 1) / T, bl.t0);
-    }
-    int u0 = 0, u1 = bl.count();
-    if (a.nsplit > 1) {
-        const int per = (u1 + a.nsplit - 1) / a.nsplit;
-        u0 = min(u1, split * per);
-        u1 = min(u1, u0 + per);
-    }
-
     f32x4 o[ND][NQ];
     float mx[NQ], sum[NQ];
 #pragma unroll
@@ -214,10 +255,10 @@ __global__ __launch_bounds__((64 * S::NW), 2) void cached_attn(AttnArgs a, Cache
 #pragma unroll
         for (int d = 0; d < ND; ++d) o[d][m] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    const int64_t step = (int64_t)T * a.D;   // bytes of a block and head
-
-    // one block, its operands given by kf(kb, j) and vf(d)
-    auto block = [&](int j0, float ks, int ve, auto&& kf, auto&& vf) {
+    // one block, its operands given by kf(kb, j, half of the 16 values) and vf(d, half of the 16 keys)
+    auto block = [&](int j0, const Place& at, auto&& kf, auto&& vf) {
+        const float ks = power(exponent_of_scale(at.ks));
+        const int ve = exponent_of_scale(at.vs);
         f32x4 s[4][NQ];
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb) {
@@ -225,14 +266,14 @@ __global__ __launch_bounds__((64 * S::NW), 2) void cached_attn(AttnArgs a, Cache
             for (int m = 0; m < NQ; ++m) s[kb][m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                const uint4 u = kf(kb, j);
-                const half8_t f[2] = {halves8<CODE>(u.x, u.y), halves8<CODE>(u.z, u.w)};
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
+                for (int k = 0; k < 2; ++k) {
+                    const half8_t f = kf(kb, j, k);
 #pragma unroll
                     for (int m = 0; m < NQ; ++m)
 #pragma unroll
-                        for (int p = 0; p < P; ++p) s[kb][m] = mma(f[k], q[m][j][k][p], s[kb][m]);
+                        for (int p = 0; p < P; ++p) s[kb][m] = mma(f, q[m][j][k][p], s[kb][m]);
+                }
             }
         }
         const bool edge = j0 + T - 1 > w0 || (j0 < wlast && j0 + T > sinks);
@@ -260,8 +301,9 @@ __global__ __launch_bounds__((64 * S::NW), 2) void cached_attn(AttnArgs a, Cache
                 for (int kb = 0; kb < 4; ++kb)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int key = j + 4 * kb + r;
-                        if (key > pos[m] || (key < lo[m] && key >= sinks)) s[kb][m][r] = -INFINITY;
+                        const int key = j + 4 * kb + r;   // (no short circuits: selects, not branches)
+                        const bool hidden = (key > pos[m]) | ((key < lo[m]) & (key >= sinks));
+                        s[kb][m][r] = hidden ? -INFINITY : s[kb][m][r];
                     }
             }
             float top = s[0][m][0];
@@ -302,53 +344,44 @@ __global__ __launch_bounds__((64 * S::NW), 2) void cached_attn(AttnArgs a, Cache
                 if constexpr (P == 2) w[m][k][1] = rest_of(x, w[m][k][0]);
             }
         }
-        // e4m3 bytes behind the sequence's last token may stand for NaN: weight 0 does not hide it
-        const int left = n - j0 - 16 * g;
-        const bool tail = CODE == Code::E4M3 && j0 + T > n;
 #pragma unroll
-        for (int d = 0; d < ND; ++d) {
-            if (16 * d >= a.D) break;
-            uint4 u = vf(d);
-            if (tail) {
-                keep_branch();
-                uint32_t* x = (uint32_t*)&u;
+        for (int d = 0; d < ND; ++d) {   // (values past D repeat the first: a branch would wait for each)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int keep = left - 4 * k;
-                    x[k] &= keep >= 4 ? ~0u : keep <= 0 ? 0u : (1u << (8 * keep)) - 1;
-                }
-            }
-            const half8_t f[2] = {halves8<CODE>(u.x, u.y), halves8<CODE>(u.z, u.w)};
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < 2; ++k) {
+                const half8_t f = vf(d, k);
 #pragma unroll
                 for (int m = 0; m < NQ; ++m)
 #pragma unroll
-                    for (int p = 0; p < P; ++p) o[d][m] = mma(f[k], w[m][k][p], o[d][m]);
+                    for (int p = 0; p < P; ++p) o[d][m] = mma(f, w[m][k][p], o[d][m]);
+            }
         }
     };
+    // e4m3 bytes of v behind the sequence's last token may stand for NaN: weight 0 does not hide it
+    auto clear = [&](int j0, uint4& u) {
+        if (CODE != Code::E4M3 || j0 + T <= n) return;
+        keep_branch();
+        uint32_t* x = (uint32_t*)&u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int keep = n - j0 - 16 * g - 4 * k;
+            x[k] &= keep >= 4 ? ~0u : keep <= 0 ? 0u : (1u << (8 * keep)) - 1;
+        }
+    };
+    auto half = [](const uint4& u, int k) { return k ? halves8<CODE>(u.z, u.w) : halves8<CODE>(u.x, u.y); };
 
     if constexpr (S::KEYS) {
-        // this wave's blocks: u0 + wave, + NW, ...
-        Bytes<J> now, next;
-        auto fetch = [&](int u, Bytes<J>& to) -> int {
-            const int p = block_of(cc, b, bl.at(u));
-            const int64_t at = ((int64_t)max(p, 0) * a.Hkv + hk) * step;
-            to.from((const uint8_t*)cc.k + at, (const uint8_t*)cc.v + at, chunks, g, lane);
-            return p;
-        };
-        int u = u0 + wave, p = -1;
-        if (u < u1) p = fetch(u, now);
-        for (; u < u1; u += NW) {
-            int pn = -1;
-            if (u + NW < u1) pn = fetch(u + NW, next);
-            if (p >= 0) {
-                const int64_t at = (int64_t)p * a.Hkv + hk;
-                block(bl.at(u) * T, power(exponent_at(cc.ks + at)), exponent_at(cc.vs + at),
-                      [&](int kb, int j) { return now.k[kb][j]; }, [&](int d) { return now.v[d]; });
+        for (int u = u0 + wave; u < u1; u += NW) {
+            Place then;
+            if (u + NW < u1) then = bring(u + NW, next);
+            if (here.p >= 0) {
+                const int j0 = bl.at(u) * T;
+#pragma unroll
+                for (int d = 0; d < ND; ++d) clear(j0, now.v[d]);
+                block(j0, here, [&](int kb, int j, int k) { return half(now.k[kb][j], k); },
+                      [&](int d, int k) { return half(now.v[d], k); });
             }
             now = next;
-            p = pn;
+            here = then;
         }
         // join the waves: their rows' base, sum and o
         float* st = (float*)sh;                  // [wave][2][16]
@@ -397,47 +430,54 @@ __global__ __launch_bounds__((64 * S::NW), 2) void cached_attn(AttnArgs a, Cache
             else if (a.lse) a.lse[((int64_t)b * a.H + h) * a.Lq + i] = ls * LN2;
         }
     } else {
-        // D / 8 kilobytes a block (k, then v): every wave brings the same number, the last ones twice
-        const int kilo = a.D / 8, rounds = (kilo + NW - 1) / NW;
-        int blk[NS];   // the pool's block in each place
-        auto issue = [&](int u, int place) {
-            const int p = block_of(cc, b, bl.at(u));
-            const int64_t at = ((int64_t)max(p, 0) * a.Hkv + hk) * step;
+        // the block's 8 J runs of 1024 bytes (k: kb J + j, then v: d), dealt to the waves; they lie in LDS in
+        // half precision, two runs each, in the order of the operands
+        constexpr int RUNS = 8 * J / NW;
+        static_assert(8 * J % NW == 0, "whole runs");
+        uint4 raw[RUNS];
+        auto fetch = [&](int u) {
+            const Place p(cc, b, hk, bl.at(u));
+            const int64_t at = p.bytes(cc, hk);
 #pragma unroll
-            for (int i = 0; i < DP / 8 / NW; ++i) {
-                if (i >= rounds) break;
-                const int k = min(i * NW + wave, kilo - 1), half = kilo / 2;
-                const uint8_t* src = (k < half ? (const uint8_t*)cc.k + at + k * 1024 : (const uint8_t*)cc.v + at + (k - half) * 1024) + lane * 16;
-                load_lds16(src, __builtin_amdgcn_readfirstlane(lds_offset(sh) + place * STAGE + k * 1024));
+            for (int i = 0; i < RUNS; ++i) {
+                const int f = i * NW + wave, kb = f / J, d = f - 4 * J;
+                const int ch = 4 * (f % J) + g;   // values past D read the first
+                const uint8_t* src = f < 4 * J ? (const uint8_t*)cc.k + at + (kb * chunks + (ch < chunks ? ch : 0)) * 256
+                                               : (const uint8_t*)cc.v + at + ((d < chunks ? d : 0) * 4 + g) * 256;
+                raw[i] = *(const uint4*)(src + c * 16);
             }
             return p;
         };
-        auto wait_but = [&](int stages) {   // all but the last `stages` stages' loads have arrived
-            if (stages == 0) wait_loads<0>();
-            else if (rounds == 1) wait_loads<1>();
-            else if (rounds == 2) wait_loads<2>();
-            else if (rounds == 3) wait_loads<3>();
-            else wait_loads<4>();
+        auto put = [&](int u, uint8_t* to) {
+            const int j0 = bl.at(u) * T;
+#pragma unroll
+            for (int i = 0; i < RUNS; ++i) {
+                const int f = i * NW + wave;
+                if (f >= 4 * J) clear(j0, raw[i]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) *(half8_t*)(to + ((f * 2 + k) * 64 + lane) * 16) = half(raw[i], k);
+            }
         };
-        for (int s = 0; s < NS - 1; ++s) blk[s] = u0 + s < u1 ? issue(u0 + s, s) : -1;
-        int place = 0;
+        Place then;
+        if (u0 < u1) {
+            here = fetch(u0);
+            put(u0, sh);
+            if (u0 + 1 < u1) then = fetch(u0 + 1);
+        }
         for (int u = u0; u < u1; ++u) {
-            wait_but(u + 1 < u1 ? 1 : 0);
-            stage_barrier();
-            const int j0 = bl.at(u) * T, p = blk[0];
-            blk[0] = blk[1];
-            if (u + NS - 1 < u1) blk[1] = issue(u + NS - 1, place == 0 ? NS - 1 : place - 1);
-            const uint8_t* kt = sh + place * STAGE;
-            const uint8_t* vt = kt + T * a.D;
-            place = place + 1 == NS ? 0 : place + 1;
-            if (p < 0 || w0 > w1 || j0 > w1 || (j0 + T - 1 < wlo && j0 >= sinks)) continue;
-            const int64_t at = (int64_t)p * a.Hkv + hk;
-            block(j0, power(exponent_at(cc.ks + at)), exponent_at(cc.vs + at),
-                  [&](int kb, int j) {
-                      const int ch = 4 * j + g < chunks ? 4 * j + g : 0;
-                      return *(const uint4*)(kt + ((kb * chunks + ch) * 16 + c) * 16);
-                  },
-                  [&](int d) { return *(const uint4*)(vt + (d * 64 + lane) * 16); });
+            const uint8_t* at = sh + ((u - u0) & 1) * STAGE;
+            stage_barrier();   // this block is in LDS, and the place of the one before is free
+            const int j0 = bl.at(u) * T;
+            const Place pl = here;
+            if (u + 1 < u1) {
+                put(u + 1, sh + ((u - u0 + 1) & 1) * STAGE);
+                here = then;
+                if (u + 2 < u1) then = fetch(u + 2);
+            }
+            if (pl.p < 0 || w0 > w1 || j0 > w1 || (j0 + T - 1 < wlo && j0 >= sinks)) continue;
+            block(j0, pl,
+                  [&](int kb, int j, int k) { return *(const half8_t*)(at + (((kb * J + j) * 2 + k) * 64 + lane) * 16); },
+                  [&](int d, int k) { return *(const half8_t*)(at + (((4 * J + d) * 2 + k) * 64 + lane) * 16); });
         }
 #pragma unroll
         for (int m = 0; m < NQ; ++m) {
@@ -463,18 +503,65 @@ __global__ __launch_bounds__((64 * S::NW), 2) void cached_attn(AttnArgs a, Cache
     }
 }
 
+// Joins the splits of a row: o = sum_s 2^(lse_s - lse) o_s.  One workgroup a row: thread s weighs split s,
+// then COLS threads side by side sum the splits for four values each, 256 / COLS splits at a time.
+constexpr int NT = 256;
+__device__ __forceinline__ float over_block(float x, float (&sh)[NT / 64], bool max)
+{
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+        const float y = __shfl_xor(x, m);
+        x = max ? fmaxf(x, y) : x + y;
+    }
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = x;
+    __syncthreads();
+    return max ? fmaxf(fmaxf(sh[0], sh[1]), fmaxf(sh[2], sh[3])) : (sh[0] + sh[1]) + (sh[2] + sh[3]);
+}
+
+template <class IO, int COLS>
+__global__ __launch_bounds__(NT) void cached_join(AttnArgs a)
+{
+    __shared__ float weight[NT], wave[NT / 64];
+    __shared__ f32x4 part[NT];
+    const int64_t total = (int64_t)a.nbh * a.nrow, at = blockIdx.x;
+    const int t = threadIdx.x, col = t % COLS, d0 = 4 * col;
+    const float ls = t < a.nsplit ? a.part_lse[t * total + at] : -INFINITY;
+    const float mx = over_block(ls, wave, true);
+    const float e = ls == -INFINITY ? 0.f : exp2_hw(ls - mx);
+    const float sum = over_block(e, wave, false);
+    weight[t] = sum > 0.f ? e / sum : 0.f;
+    __syncthreads();
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+    const float* p = a.part + at * a.D + (d0 < a.D ? d0 : 0);
+#pragma unroll 4
+    for (int s = t / COLS; s < a.nsplit; s += NT / COLS) x += *(const f32x4*)(p + s * total * a.D) * weight[s];
+    part[t] = x;
+    __syncthreads();
+    const int bh = (int)(at / a.nrow), r = (int)(at % a.nrow);
+    const int b = bh / a.Hkv, i = r / a.G, h = bh % a.Hkv * a.G + r % a.G;
+    if (t < COLS && d0 < a.D) {
+#pragma unroll
+        for (int k = 1; k < NT / COLS; ++k) x += part[k * COLS + t];
+        put4<IO>((typename IO::T*)a.o + b * a.os[0] + (int64_t)i * a.os[1] + h * a.os[2] + d0, x);
+    }
+    if (a.lse && t == 0)
+        a.lse[((int64_t)b * a.H + h) * a.Lq + i] = sum > 0.f ? (mx + __builtin_amdgcn_logf(sum)) * LN2 : -INFINITY;
+}
+
 // Rows of a workgroup: 16 shared by four waves for the few rows of decoding, else 64 or 128.
 constexpr int FEW = 16;
-constexpr int64_t TWO_A_CU = 512;
+constexpr int64_t TWO_A_CU = 512, FILL = 512;
 int tile_rows(const AttnArgs& a)
 {
     if (a.nrow <= FEW) return 16;
-    return (a.nrow + 127) / 128 * (int64_t)a.nbh <= TWO_A_CU ? 64 : 128;
+    const int64_t w128 = (a.nrow + 127) / 128 * (int64_t)a.nbh, w64 = (a.nrow + 63) / 64 * (int64_t)a.nbh;
+    return w128 > TWO_A_CU || (a.nrow > 64 && 2 * w64 <= FILL) ? 128 : 64;
 }
 
 // Key splits while the rows do not fill the GPU, each of at least SPLIT_MIN keys.
-constexpr int64_t FILL = 512, FILL_FEW = 768, SPLIT_MIN = 512;
-constexpr int64_t SPLIT_MAX = 64;   // the join weighs one split a lane
+constexpr int64_t FILL_FEW = 768, SPLIT_MIN = 512;
+constexpr int64_t SPLIT_MAX = NT;   // the join weighs one split a thread
 
 int splits(const AttnArgs& a, int sinks)
 {
@@ -509,12 +596,17 @@ hipError_t shape(const AttnArgs& a, const CacheArgs& c, int sinks, hipStream_t s
 }
 
 template <class IO, Code CODE>
-hipError_t run(AttnArgs a, const CacheArgs& c, int sinks, Store s, hipStream_t st)
+hipError_t run(AttnArgs a, const CacheArgs& c, int sinks, hipStream_t st)
 {
     a.nsplit = splits(a, sinks);
     a.part_lse = a.part + (int64_t)a.nsplit * a.nbh * a.nrow * a.D;
     const hipError_t e = a.D <= 64 ? shape<IO, CODE, 1>(a, c, sinks, st) : shape<IO, CODE, 2>(a, c, sinks, st);
-    return e != hipSuccess || a.nsplit == 1 ? e : launch_attn_join(s, a, st);
+    if (e != hipSuccess || a.nsplit == 1) return e;
+    const int64_t rows = (int64_t)a.nbh * a.nrow;
+    if (!grid_ok(rows, NT)) return hipErrorInvalidValue;
+    if (a.D <= 64) hipLaunchKernelGGL((cached_join<IO, 16>), dim3((unsigned)rows), dim3(NT), 0, st, a);
+    else hipLaunchKernelGGL((cached_join<IO, 32>), dim3((unsigned)rows), dim3(NT), 0, st, a);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -530,8 +622,8 @@ hipError_t launch_cached_attn(Store s, Code code, const AttnArgs& a, const Cache
     AttnArgs x = a;
     x.part = (float*)ws;
     if (s == Store::F32)
-        return code == Code::I8 ? run<f32_io, Code::I8>(x, c, sinks, s, st) : run<f32_io, Code::E4M3>(x, c, sinks, s, st);
-    return code == Code::I8 ? run<bf16_io, Code::I8>(x, c, sinks, s, st) : run<bf16_io, Code::E4M3>(x, c, sinks, s, st);
+        return code == Code::I8 ? run<f32_io, Code::I8>(x, c, sinks, st) : run<f32_io, Code::E4M3>(x, c, sinks, st);
+    return code == Code::I8 ? run<bf16_io, Code::I8>(x, c, sinks, st) : run<bf16_io, Code::E4M3>(x, c, sinks, st);
 }
 
 }  // namespace sc
