@@ -328,8 +328,6 @@ size_t attn_fwd_bytes(const AttnArgs& a);
 hipError_t launch_attn(Store st, const AttnArgs& a, void* ws, hipStream_t stream);
 size_t attn_bwd_bytes(const AttnArgs& a);
 hipError_t launch_attn_bwd(Store st, const AttnArgs& a, void* ws, hipStream_t stream);
-// Joins the nsplit parts of a call's rows (part, part_lse set) into o and lse.
-hipError_t launch_attn_join(Store st, const AttnArgs& a, hipStream_t stream);
 
 // Norm of the rows of q and k (x w rstd, rstd = (mean x^2 + eps)^-1/2) and rotation of their first R
 // values by the token's position times freq (sc_qknorm.hip); index 0 is q, 1 is k.  Strides: batch,
@@ -350,7 +348,8 @@ struct QkArgs {
     bool pairs;              // values 2 i and 2 i + 1 turn together, not i and i + R / 2
     bool whole;              // every row starts 16-byte aligned
     // set by the launchers
-    int tb;                  // tokens of a workgroup at a time
+    int tb, turns;           // tokens of a turn; turns of a sequence
+    uint32_t all;            // turns
     float* part;             // backward: sums of dw by workgroup
 };
 hipError_t launch_qk(Store st, const QkArgs& a, hipStream_t stream);

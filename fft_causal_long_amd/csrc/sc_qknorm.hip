@@ -19,6 +19,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "sc_internal.h"
 #include "sc_rows.h"
@@ -54,194 +55,279 @@ __device__ __forceinline__ float2 turn_of(int p, float f)
     return make_float2(q == 1 || q == 2 ? -cq : cq, q >= 2 ? -sq : sq);
 }
 
-// Where the pairs of a row lie.  WHOLE: lane l of a row's D / 2V holds V pairs, the elements a + i and
-// b + i (or a + 2 i and a + 2 i + 1).  Pairs past R / 2 are the values that do not turn.
-template <class IO>
-struct Cut {
-    static constexpr int V = vec_elems<IO>;
-    int a, b;
-    __device__ __forceinline__ Cut(const QkArgs& q, int l)
+// V neighbouring values of a row: 8 or 16 bytes.
+template <class IO, int V>
+struct Vec {
+    typedef uint32_t Raw __attribute__((ext_vector_type(V * IO::SIZE / 4)));
+    __device__ __forceinline__ static Raw load(const typename IO::T* p) { return *(const Raw*)p; }
+    __device__ __forceinline__ static float at(const Raw& r, int i)
     {
-        if (q.pairs) {
-            a = 2 * V * l;
-            b = a + V;
-        } else if (V * l < q.R / 2) {
-            a = V * l;
-            b = q.R / 2 + a;
-        } else {
-            a = 2 * V * l;
-            b = a + V;
+        if constexpr (IO::SIZE == 2) return __uint_as_float(i & 1 ? r[i / 2] & 0xffff0000u : r[i / 2] << 16);
+        else return __uint_as_float(r[i]);
+    }
+    __device__ __forceinline__ static void store(typename IO::T* p, const float (&x)[V])
+    {
+        Raw r;
+#pragma unroll
+        for (int i = 0; i < V * IO::SIZE / 4; ++i) {
+            if constexpr (IO::SIZE == 2) r[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+            else r[i] = __float_as_uint(x[i]);
         }
+        *(Raw*)p = r;
+    }
+};
+
+// Where lane l of a row's D / 2V finds its V pairs: the elements a + i and b + i, or, of a vector pair
+// a, b = a + V, neighbours (PAIRS).  Pairs past R / 2 are the values that do not turn.
+template <int V, bool PAIRS>
+struct Cut {
+    int a, b;
+    __device__ __forceinline__ Cut(int R, int l)
+    {
+        const bool halves = !PAIRS && V * l < R / 2;
+        a = halves ? V * l : 2 * V * l;
+        b = halves ? R / 2 + a : a + V;
     }
 };
 
 // 2 V values of a row as V pairs.
-template <class IO>
+template <class IO, int V, bool PAIRS>
 struct Row {
-    static constexpr int V = vec_elems<IO>;
+    using W = Vec<IO, V>;
     float a[V], b[V];
-    __device__ __forceinline__ void from(const uint4& u, const uint4& v, bool pairs)
+    __device__ __forceinline__ void from(const typename W::Raw& u, const typename W::Raw& v)
     {
-        const Lanes<IO> x = widen<IO>(u), y = widen<IO>(v);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            a[i] = pairs ? (2 * i < V ? x.x[2 * i % V] : y.x[2 * i % V]) : x.x[i];
-            b[i] = pairs ? (2 * i < V ? x.x[(2 * i + 1) % V] : y.x[(2 * i + 1) % V]) : y.x[i];
+            a[i] = !PAIRS ? W::at(u, i) : 2 * i < V ? W::at(u, 2 * i % V) : W::at(v, 2 * i % V);
+            b[i] = !PAIRS ? W::at(v, i) : 2 * i < V ? W::at(u, (2 * i + 1) % V) : W::at(v, (2 * i + 1) % V);
         }
     }
-    __device__ __forceinline__ void to(typename IO::T* p, const Cut<IO>& c, bool pairs) const
+    __device__ __forceinline__ void to(typename IO::T* p, const Cut<V, PAIRS>& c) const
     {
-        Lanes<IO> x, y;
+        float x[V], y[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            x.x[i] = pairs ? (i & 1 ? b[i / 2] : a[i / 2]) : a[i];
-            y.x[i] = pairs ? (i & 1 ? b[V / 2 + i / 2] : a[V / 2 + i / 2]) : b[i];
+            x[i] = PAIRS ? (i & 1 ? b[i / 2] : a[i / 2]) : a[i];
+            y[i] = PAIRS ? (i & 1 ? b[V / 2 + i / 2] : a[V / 2 + i / 2]) : b[i];
         }
-        *(uint4*)(p + c.a) = narrow<IO>(x);
-        *(uint4*)(p + c.b) = narrow<IO>(y);
+        W::store(p + c.a, x);
+        W::store(p + c.b, y);
     }
 };
 
-// sum over the LPR neighbouring lanes of a row
+// Sum over the LPR neighbouring lanes of a row, in every one of them.  Up to 16 lanes the partner comes
+// with the addition (data-parallel primitives: lane ^ 1, lane ^ 2, then the mirror of 8 and of 16 lanes,
+// whose halves are equal by then).
+template <int CTRL>
+__device__ __forceinline__ float from_lane(float x)
+{
+    return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(x), CTRL, 0xf, 0xf, true));
+}
 template <int LPR>
 __device__ __forceinline__ float row_sum(float x)
 {
-#pragma unroll
-    for (int m = 1; m < LPR; m <<= 1) x += __shfl_xor(x, m);
+    if constexpr (LPR >= 2) x += from_lane<0xb1>(x);
+    if constexpr (LPR >= 4) x += from_lane<0x4e>(x);
+    if constexpr (LPR >= 8) x += from_lane<0x141>(x);
+    if constexpr (LPR >= 16) x += from_lane<0x140>(x);
+    if constexpr (LPR >= 32) x += __shfl_xor(x, 16);
+    if constexpr (LPR >= 64) x += __shfl_xor(x, 32);
     return x;
 }
 
-__device__ __forceinline__ int position(const QkArgs& a, int64_t token)
-{
-    if (a.pos) return a.pos[token];
-    const int64_t b = token / a.L, t = token - b * a.L;
-    return (int)(a.len ? a.len[b] - a.L + t : t);
-}
+// Tokens of a workgroup's turn: t0 .. t0 + n - 1 of sequence b.
+struct Span {
+    int64_t b, t0;
+    int n;
+    __device__ __forceinline__ Span(const QkArgs& a, uint32_t turn)
+    {
+        const uint32_t seq = turn / (uint32_t)a.turns;   // uniform
+        b = seq;
+        t0 = (int64_t)(turn - seq * (uint32_t)a.turns) * a.tb;
+        n = (int)std::min<int64_t>(a.tb, a.L - t0);
+    }
+};
 
-// The angles of tokens t0 .. t0 + n - 1 into table[token][pair] (D / 2 pairs a token, odd D: one more;
-// those past R / 2 stay where they are).
-__device__ __forceinline__ void fill_angles(const QkArgs& a, float2* table, int64_t t0, int n)
+// A slot's rows slot, slot + step, ... of H heads a token: token i, head h, without a division a row.
+struct Walk {
+    int i, h, di, dh, H;
+    __device__ __forceinline__ Walk(int slot, int step, int H_) : i(slot / H_), h(slot - i * H_), di(step / H_), dh(step - di * H_), H(H_) {}
+    // to the next row; true if that wrapped the head
+    __device__ __forceinline__ bool next()
+    {
+        const bool wrap = h + dh >= H;
+        i += di + (wrap ? 1 : 0);
+        h += dh - (wrap ? H : 0);
+        return wrap;
+    }
+};
+
+// The place of a walk's row in a tensor (the tensor's numbers are taken once: an index into the call's
+// arguments inside the loop would be a load for each row).
+template <class E>
+struct Path {
+    E* p;
+    int64_t inc, wrap;
+    __device__ __forceinline__ Path(E* base, int64_t sb, int64_t st, int64_t sh, const Span& s, const Walk& w)
+        : p(base + s.b * sb + (s.t0 + w.i) * st + w.h * sh), inc(w.di * st + w.dh * sh), wrap(st - w.H * sh)
+    {
+    }
+    __device__ __forceinline__ void next(bool wrapped) { p += wrapped ? inc + wrap : inc; }
+};
+
+// The angles of the span's tokens into table[token][pair] (D / 2 pairs a token, odd D: one more; those past
+// R / 2 stay where they are).
+__device__ __forceinline__ void fill_angles(const QkArgs& a, float2* table, const Span& p)
 {
     const int half = (a.D + 1) / 2;
-    for (int i = threadIdx.x; i < n * half; i += NT) {
-        const int t = i / half, p = i - t * half;
-        table[i] = 2 * p < a.R ? turn_of(position(a, t0 + t), a.freq[p]) : make_float2(1.f, 0.f);
+    for (int i = threadIdx.x; i < p.n * half; i += NT) {
+        const int t = i / half, k = i - t * half;
+        const int64_t at = p.t0 + t;
+        const int pos = a.pos ? a.pos[p.b * a.L + at] : (int)(a.len ? a.len[p.b] - a.L + at : at);
+        table[i] = 2 * k < a.R ? turn_of(pos, a.freq[k]) : make_float2(1.f, 0.f);
     }
 }
 
-template <class IO>
-__device__ __forceinline__ int64_t row_at(const int64_t (&s)[3], int64_t b, int64_t t, int h)
+// (v + eps)^-1/2 to about 1 ulp; the reciprocal root takes no subnormal numbers.
+__device__ __forceinline__ float rstd_of(float v)
 {
-    return b * s[0] + t * s[1] + h * s[2];
+    const bool low = v < 0x1p-96f;
+    return __builtin_amdgcn_rsqf(low ? v * 0x1p64f : v) * (low ? 0x1p32f : 1.f);
 }
 
-// Rows of a workgroup's tokens in turn, q's first: LPR lanes a row, D / 2V of them with values.
-template <class IO, int LPR, bool BWD>
+// Rows of a workgroup's tokens in turn, a row's loads issued before the row before it is finished: LPR
+// lanes a row, D / 2V of them with values.  Backward, q's tokens first and then k's, so that one set of
+// sums for dw is held.
+template <class IO, int V, int LPR, bool PAIRS, bool BWD>
 __global__ __launch_bounds__(NT) void qk_rows(QkArgs a)
 {
     using E = typename IO::T;
-    constexpr int V = vec_elems<IO>, RPP = NT / LPR;   // rows at a time
+    using W = Vec<IO, V>;
+    constexpr int RPP = NT / LPR;   // rows at a time
     extern __shared__ float2 table[];
+    __shared__ float sum[BWD ? 4 : 1][BWD ? 2 * V * LPR : 1];
     const int l = threadIdx.x % LPR, slot = threadIdx.x / LPR, half = (a.D + 1) / 2;
     const bool on = 2 * V * l < a.D;
-    const Cut<IO> cut(a, on ? l : 0);
+    const int lv = on ? l : 0;
+    const Cut<V, PAIRS> cut(a.R, lv);
     const float inv = 1.0f / (float)a.D;
-    float dw[BWD ? 2 : 1][2][V];
-    if constexpr (BWD)
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int i = 0; i < V; ++i) dw[s][0][i] = dw[s][1][i] = 0.f;
+    struct Raw {
+        typename W::Raw xa, xb, ga, gb;
+    };
 
-    for (int64_t t0 = (int64_t)blockIdx.x * a.tb; t0 < a.tokens; t0 += (int64_t)gridDim.x * a.tb) {
-        const int n = (int)std::min<int64_t>(a.tb, a.tokens - t0);
-        __syncthreads();
-        fill_angles(a, table, t0, n);
-        __syncthreads();
+    auto tensor = [&](int s, uint32_t turn, float (&dw)[2][V], bool angles) {
+        const Span span(a, turn);
+        const int H = s ? a.H[1] : a.H[0], rows = span.n * H;
+        const auto pick = [&](const int64_t(&t)[2][3], int i) { return s ? t[1][i] : t[0][i]; };
+        Walk walk(slot, RPP, std::max(H, 1));
+        Path<const E> x((const E*)(s ? a.x[1] : a.x[0]), pick(a.xs, 0), pick(a.xs, 1), pick(a.xs, 2), span, walk);
+        Path<const E> g((const E*)(s ? a.dy[1] : a.dy[0]), pick(a.dys, 0), pick(a.dys, 1), pick(a.dys, 2), span, walk);
+        Path<E> y((E*)(s ? a.y[1] : a.y[0]), pick(a.ys, 0), pick(a.ys, 1), pick(a.ys, 2), span, walk);
+        Raw now;
+        auto load = [&] {
+            now.xa = W::load(x.p + cut.a);
+            now.xb = W::load(x.p + cut.b);
+            if constexpr (BWD) {
+                now.ga = W::load(g.p + cut.a);
+                now.gb = W::load(g.p + cut.b);
+            }
+        };
+        if (slot < rows) load();
+        const E* wp = (const E*)(s ? a.w[1] : a.w[0]);
+        Row<IO, V, PAIRS> w;
+        if (wp) {
+            w.from(W::load(wp + cut.a), W::load(wp + cut.b));
+        } else {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int H = a.H[s], rows = n * H;
-            Row<IO> w;
-            if (a.w[s]) {
-                w.from(*(const uint4*)((const E*)a.w[s] + cut.a), *(const uint4*)((const E*)a.w[s] + cut.b), a.pairs);
+            for (int i = 0; i < V; ++i) w.a[i] = w.b[i] = 1.f;
+        }
+        if (angles) {
+            __syncthreads();
+            fill_angles(a, table, span);
+            __syncthreads();
+        }
+        for (int r = slot; r < rows; r += RPP) {
+            const float2* cs = table + walk.i * half + lv * V;
+            E* yp = y.p;
+            Row<IO, V, PAIRS> v, e;
+            v.from(now.xa, now.xb);
+            if constexpr (BWD) e.from(now.ga, now.gb);
+            const bool wrap = walk.next();
+            y.next(wrap);
+            if (r + RPP < rows) {   // else the same row again, for nothing: no branch around the loads
+                x.next(wrap);
+                if constexpr (BWD) g.next(wrap);
+            }
+            load();
+            float sq = 0.f, ex = 0.f;
+#pragma unroll
+            for (int k = 0; k < V; ++k) sq += v.a[k] * v.a[k] + v.b[k] * v.b[k];
+            if constexpr (BWD) {
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const float2 c = cs[k];
+                    const float ea = e.a[k] * c.x + e.b[k] * c.y, eb = e.b[k] * c.x - e.a[k] * c.y;
+                    e.a[k] = ea;
+                    e.b[k] = eb;
+                    ex += ea * w.a[k] * v.a[k] + eb * w.b[k] * v.b[k];
+                }
+                ex = row_sum<LPR>(on ? ex : 0.f);
+            }
+            sq = row_sum<LPR>(on ? sq : 0.f);
+            const float rstd = rstd_of(sq * inv + a.eps);
+            if constexpr (BWD) {
+                const float m = ex * inv * rstd;
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const float na = v.a[k] * rstd, nb = v.b[k] * rstd;
+                    dw[0][k] += e.a[k] * na;
+                    dw[1][k] += e.b[k] * nb;
+                    v.a[k] = (e.a[k] * w.a[k] - na * m) * rstd;
+                    v.b[k] = (e.b[k] * w.b[k] - nb * m) * rstd;
+                }
             } else {
 #pragma unroll
-                for (int i = 0; i < V; ++i) w.a[i] = w.b[i] = 1.f;
+                for (int k = 0; k < V; ++k) {
+                    const float2 c = cs[k];
+                    const float na = v.a[k] * rstd * w.a[k], nb = v.b[k] * rstd * w.b[k];
+                    v.a[k] = na * c.x - nb * c.y;
+                    v.b[k] = nb * c.x + na * c.y;
+                }
             }
-            for (int r = slot; r < rows; r += RPP) {
-                const int i = r / H, h = r - i * H;
-                const int64_t b = (t0 + i) / a.L, t = t0 + i - b * a.L;
-                const E* x = (const E*)a.x[s] + row_at<IO>(a.xs[s], b, t, h);
-                Row<IO> v, e;
-                const uint4 xa = *(const uint4*)(x + cut.a), xb = *(const uint4*)(x + cut.b);
-                v.from(xa, xb, a.pairs);
-                if constexpr (BWD) {
-                    const E* g = (const E*)a.dy[s] + row_at<IO>(a.dys[s], b, t, h);
-                    e.from(*(const uint4*)(g + cut.a), *(const uint4*)(g + cut.b), a.pairs);
-                }
-                const float2* turn = table + i * half + (on ? l : 0) * V;
-                float sq = 0.f, ex = 0.f;
-#pragma unroll
-                for (int k = 0; k < V; ++k) sq += v.a[k] * v.a[k] + v.b[k] * v.b[k];
-                if constexpr (BWD) {
-#pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        const float2 c = turn[k];
-                        const float ea = e.a[k] * c.x + e.b[k] * c.y, eb = e.b[k] * c.x - e.a[k] * c.y;
-                        e.a[k] = ea;
-                        e.b[k] = eb;
-                        ex += ea * w.a[k] * v.a[k] + eb * w.b[k] * v.b[k];
-                    }
-                    ex = row_sum<LPR>(on ? ex : 0.f);
-                }
-                sq = row_sum<LPR>(on ? sq : 0.f);
-                const float rstd = 1.0f / sqrtf(sq * inv + a.eps);
-                if constexpr (BWD) {
-                    const float m = ex * inv * rstd;
-#pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        const float na = v.a[k] * rstd, nb = v.b[k] * rstd;
-                        dw[s][0][k] += e.a[k] * na;
-                        dw[s][1][k] += e.b[k] * nb;
-                        v.a[k] = (e.a[k] * w.a[k] - na * m) * rstd;
-                        v.b[k] = (e.b[k] * w.b[k] - nb * m) * rstd;
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        const float2 c = turn[k];
-                        const float na = v.a[k] * rstd * w.a[k], nb = v.b[k] * rstd * w.b[k];
-                        v.a[k] = na * c.x - nb * c.y;
-                        v.b[k] = nb * c.x + na * c.y;
-                    }
-                }
-                if (on) v.to((E*)a.y[s] + row_at<IO>(a.ys[s], b, t, h), cut, a.pairs);
-            }
+            if (on) v.to(yp, cut);
         }
-    }
-    if constexpr (BWD) {
-        if (!a.part) return;
-        // the rows of a wave, then the waves
-        __shared__ float sum[4][2][2 * V * LPR];
-        const int wave = threadIdx.x >> 6;
+    };
+    float dw[2][V];
+    if constexpr (!BWD) {
+        for (uint32_t turn = blockIdx.x; turn < a.all; turn += gridDim.x)
+#pragma unroll 1
+            for (int s = 0; s < 2; ++s) tensor(s, turn, dw, s == 0);
+    } else {
+#pragma unroll 1
+        for (int s = 0; s < 2; ++s) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+            for (int i = 0; i < V; ++i) dw[0][i] = dw[1][i] = 0.f;
+            for (uint32_t turn = blockIdx.x; turn < a.all; turn += gridDim.x) tensor(s, turn, dw, true);
+            if (!a.part) continue;
+            // the rows of a wave, then the waves
+            __syncthreads();
 #pragma unroll
             for (int k = 0; k < 2 * V; ++k) {
-                float x = dw[s][k / V][k % V];
+                float x = dw[k / V][k % V];
 #pragma unroll
                 for (int m = LPR; m < 64; m <<= 1) x += __shfl_xor(x, m);
-                if ((threadIdx.x & 63) < LPR) sum[wave][s][k * LPR + l] = x;
+                if ((threadIdx.x & 63) < LPR) sum[threadIdx.x >> 6][k * LPR + l] = x;
             }
-        __syncthreads();
-        float* out = a.part + (int64_t)blockIdx.x * 2 * a.D;
-        if (slot < 2 && on) {
+            __syncthreads();
+            if (slot == 0 && on) {
+                float* out = a.part + ((int64_t)blockIdx.x * 2 + s) * a.D;
 #pragma unroll
-            for (int k = 0; k < 2 * V; ++k) {
-                const int at = k * LPR + l;
-                const float x = (sum[0][slot][at] + sum[1][slot][at]) + (sum[2][slot][at] + sum[3][slot][at]);
-                const int i = k % V;
-                out[slot * a.D + (a.pairs ? cut.a + 2 * i + k / V : (k < V ? cut.a : cut.b) + i)] = x;
+                for (int k = 0; k < 2 * V; ++k) {
+                    const int at = k * LPR + l, i = k % V;
+                    out[PAIRS ? cut.a + 2 * i + k / V : (k < V ? cut.a : cut.b) + i] =
+                        (sum[0][at] + sum[1][at]) + (sum[2][at] + sum[3][at]);
+                }
             }
         }
     }
@@ -274,21 +360,22 @@ __global__ __launch_bounds__(NT) void qk_pairs(QkArgs a)
             for (int k = 0; k < PAIRS; ++k) dw[s][0][k] = dw[s][1][k] = 0.f;
     auto get = [](const E* p, int i) { return i < 0 ? 0.f : IO::load(p, i); };
 
-    for (int64_t t0 = (int64_t)blockIdx.x * a.tb; t0 < a.tokens; t0 += (int64_t)gridDim.x * a.tb) {
-        const int n = (int)std::min<int64_t>(a.tb, a.tokens - t0);
+    for (uint32_t turn = blockIdx.x; turn < a.all; turn += gridDim.x) {
+        const Span span(a, turn);
         __syncthreads();
-        fill_angles(a, table, t0, n);
+        fill_angles(a, table, span);
         __syncthreads();
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int H = a.H[s], rows = n * H;
+            const int rows = span.n * a.H[s];
             const E* w = (const E*)a.w[s];
-            for (int r = wave; r < rows; r += NT / 64) {
-                const int i = r / H, h = r - i * H;
-                const int64_t b = (t0 + i) / a.L, t = t0 + i - b * a.L;
-                const E* x = (const E*)a.x[s] + row_at<IO>(a.xs[s], b, t, h);
-                const E* g = BWD ? (const E*)a.dy[s] + row_at<IO>(a.dys[s], b, t, h) : nullptr;
-                E* y = (E*)a.y[s] + row_at<IO>(a.ys[s], b, t, h);
+            Walk walk(wave, NT / 64, std::max(a.H[s], 1));
+            for (int r = wave; r < rows; r += NT / 64, walk.next()) {
+                const int i = walk.i;
+                const int64_t t = span.t0 + i;
+                const E* x = (const E*)a.x[s] + span.b * a.xs[s][0] + t * a.xs[s][1] + walk.h * a.xs[s][2];
+                const E* g = BWD ? (const E*)a.dy[s] + span.b * a.dys[s][0] + t * a.dys[s][1] + walk.h * a.dys[s][2] : nullptr;
+                E* y = (E*)a.y[s] + span.b * a.ys[s][0] + t * a.ys[s][1] + walk.h * a.ys[s][2];
                 float va[PAIRS], vb[PAIRS], ea[PAIRS], eb[PAIRS], wa[PAIRS], wb[PAIRS], sq = 0.f, ex = 0.f;
 #pragma unroll
                 for (int k = 0; k < PAIRS; ++k) {
@@ -305,7 +392,7 @@ __global__ __launch_bounds__(NT) void qk_pairs(QkArgs a)
                         ex += ea[k] * wa[k] * va[k] + eb[k] * wb[k] * vb[k];
                     }
                 }
-                const float rstd = 1.0f / sqrtf(row_sum<64>(sq) * inv + a.eps);
+                const float rstd = rstd_of(row_sum<64>(sq) * inv + a.eps);
                 const float m = BWD ? row_sum<64>(ex) * inv * rstd : 0.f;
 #pragma unroll
                 for (int k = 0; k < PAIRS; ++k) {
@@ -353,63 +440,75 @@ __global__ __launch_bounds__(NT) void qk_pairs(QkArgs a)
     }
 }
 
-// dw = the workgroups' sums added: 8 columns a workgroup, 32 threads a column.
+// dw = the workgroups' sums added: 4 columns a workgroup, 64 threads a column, whose loads are all in
+// flight at once (1024 parts: 16 a thread).
 template <class IO>
 __global__ __launch_bounds__(NT) void qk_sum(QkArgs a, int parts)
 {
     __shared__ float sum[NT];
-    const int at = blockIdx.x * 8 + threadIdx.x % 8;
+    const int at = blockIdx.x * 4 + threadIdx.x % 4;
     float x = 0.f;
     if (at < 2 * a.D) {
-#pragma unroll 8
-        for (int p = threadIdx.x / 8; p < parts; p += 32) x += a.part[(int64_t)p * 2 * a.D + at];
+#pragma unroll 16
+        for (int p = threadIdx.x / 4; p < parts; p += 64) x += a.part[(int64_t)p * 2 * a.D + at];
     }
     sum[threadIdx.x] = x;
     __syncthreads();
 #pragma unroll
-    for (int m = NT / 2; m >= 8; m >>= 1) {
+    for (int m = NT / 2; m >= 4; m >>= 1) {
         if ((int)threadIdx.x < m) sum[threadIdx.x] += sum[threadIdx.x + m];
         __syncthreads();
     }
-    if (threadIdx.x >= 8 || at >= 2 * a.D) return;
+    if (threadIdx.x >= 4 || at >= 2 * a.D) return;
     typename IO::T* out = (typename IO::T*)a.dw[at < a.D ? 0 : 1];
     if (out) IO::store(out, at % a.D, sum[threadIdx.x]);
 }
 
-struct Plan {
-    int tb;
-    int64_t wgs;
-};
-
-// Tokens of a workgroup: as many as give every thread an angle, fewer while the workgroups do not
-// fill the GPU.
+// Tokens of a turn (of one sequence): fewer while the workgroups do not fill the GPU, up to what 16 KB
+// of angles hold.
 constexpr int64_t FILL = 1024, MOST = 1 << 20;   // MOST: what a launch holds; they walk the rest
+constexpr int ANGLES = 2048;
+struct Plan {
+    int64_t tb, turns, all, wgs;   // turns of a sequence, of all of them
+};
 Plan plan(const QkArgs& a, bool bwd)
 {
-    const int half = (a.D + 1) / 2;
+    const int64_t half = (a.D + 1) / 2;
     Plan p;
-    p.tb = (int)std::max<int64_t>(1, std::min<int64_t>(std::max(1, NT / half), a.tokens / FILL));
-    p.wgs = (a.tokens + p.tb - 1) / p.tb;
-    p.wgs = std::min(p.wgs, bwd ? FILL : MOST);
+    p.tb = std::max<int64_t>(1, std::min<int64_t>({a.tokens / FILL, ANGLES / half, a.L}));
+    p.turns = (a.L + p.tb - 1) / p.tb;
+    p.all = a.B * p.turns;
+    p.wgs = std::min(p.all, bwd ? FILL : MOST);
     return p;
 }
 
 template <class IO, bool BWD>
 hipError_t go(QkArgs a, hipStream_t st)
 {
-    constexpr int V = vec_elems<IO>;
+    constexpr int V = BWD ? 4 : vec_elems<IO>;   // values of a load: see below
     const Plan p = plan(a, BWD);
-    a.tb = p.tb;
-    if (!grid_ok(p.wgs, NT)) return hipErrorInvalidValue;
+    a.tb = (int)p.tb;
+    a.turns = (int)p.turns;
+    if (p.all > INT32_MAX) return hipErrorInvalidValue;   // (the walk's 32 bits)
+    a.all = (uint32_t)p.all;
     const dim3 grid((unsigned)p.wgs), block(NT);
-    const size_t lds = (size_t)p.tb * ((a.D + 1) / 2) * sizeof(float2);
+    const size_t lds = (size_t)a.tb * ((a.D + 1) / 2) * sizeof(float2);
     const int lanes = a.D / (2 * V);
-    const bool whole = a.whole && a.D % (2 * V) == 0 && (a.pairs || a.R % (2 * V) == 0);
-    if (!whole) hipLaunchKernelGGL((qk_pairs<IO, BWD>), grid, block, lds, st, a);
-    else if (lanes <= 4) hipLaunchKernelGGL((qk_rows<IO, 4, BWD>), grid, block, lds, st, a);
-    else if (lanes <= 8) hipLaunchKernelGGL((qk_rows<IO, 8, BWD>), grid, block, lds, st, a);
-    else if (lanes <= 16) hipLaunchKernelGGL((qk_rows<IO, 16, BWD>), grid, block, lds, st, a);
-    else hipLaunchKernelGGL((qk_rows<IO, 64, BWD>), grid, block, lds, st, a);
+    const bool whole = a.whole && a.D % (2 * V) == 0 && (a.pairs || a.R % (2 * V) == 0);   // rows of whole lanes
+    if (!whole) {
+        hipLaunchKernelGGL((qk_pairs<IO, BWD>), grid, block, lds, st, a);
+        return hipGetLastError();
+    }
+    auto rows = [&](auto lpr) {
+        constexpr int LPR = decltype(lpr)::value;
+        if (a.pairs) hipLaunchKernelGGL((qk_rows<IO, V, LPR, true, BWD>), grid, block, lds, st, a);
+        else hipLaunchKernelGGL((qk_rows<IO, V, LPR, false, BWD>), grid, block, lds, st, a);
+    };
+    if (lanes <= 4) rows(std::integral_constant<int, 4>());
+    else if (lanes <= 8) rows(std::integral_constant<int, 8>());
+    else if (lanes <= 16) rows(std::integral_constant<int, 16>());
+    else if (lanes <= 32) rows(std::integral_constant<int, 32>());
+    else rows(std::integral_constant<int, 64>());
     return hipGetLastError();
 }
 
@@ -423,7 +522,7 @@ hipError_t bwd(QkArgs a, void* ws, hipStream_t st)
     }
     if (!a.dw[0] && !a.dw[1]) return hipSuccess;
     const int parts = a.tokens > 0 ? (int)plan(a, true).wgs : 0;   // none: sums of no rows
-    hipLaunchKernelGGL(qk_sum<IO>, dim3((2 * a.D + 7) / 8), dim3(NT), 0, st, a, parts);
+    hipLaunchKernelGGL(qk_sum<IO>, dim3((2 * a.D + 3) / 4), dim3(NT), 0, st, a, parts);
     return hipGetLastError();
 }
 

@@ -103,7 +103,8 @@ def _lengths(kv_len, B):
         raise ValueError("kv_len must be (B,)")
 
 
-def _qk_args(q, k, q_weight, k_weight, inv_freq, positions, kv_len, interleaved, eps):
+def _qk_args(q, k, qo, ko, dq, dk, q_weight, k_weight, inv_freq, positions, kv_len, interleaved, eps):
+    """The call's struct; qo, ko: the results, or their gradients."""
     _typed(q, torch.float32, inv_freq)
     _typed(q, torch.int32, positions, kv_len)
     sq = _strides(q)
@@ -115,22 +116,21 @@ def _qk_args(q, k, q_weight, k_weight, inv_freq, positions, kv_len, interleaved,
             raise ValueError("q_weight and k_weight must be contiguous (D,) tensors")
     R = 0
     if inv_freq is not None:
-        R = 2 * inv_freq.numel()
-        if inv_freq.dim() != 1 or R > D:
+        if inv_freq.dim() != 1 or 2 * inv_freq.shape[0] > D:
             raise ValueError("inv_freq must hold at most D / 2 values")
-    if positions is not None and kv_len is not None:
-        raise ValueError("positions and kv_len exclude each other")
-    if positions is not None and tuple(positions.shape) != (B, L):
-        raise ValueError("positions must be (B, L)")
+        R = 2 * inv_freq.shape[0]
+    if positions is not None:
+        if kv_len is not None:
+            raise ValueError("positions and kv_len exclude each other")
+        if tuple(positions.shape) != (B, L):
+            raise ValueError("positions must be (B, L)")
     if kv_len is not None:
         _lengths(kv_len, B)
-    a = sc_qk(B, L, H, 0 if k is None else k.shape[2], D, R)
-    a.q = sq
-    if k is not None:
-        a.k = _strides(k)
-    a.eps, a.interleaved = float(eps), int(bool(interleaved))
-    a.inv_freq, a.positions, a.kv_len = _ptr(inv_freq) if R else None, _ptr(positions), _ptr(kv_len)
-    return a
+    none = _int3()
+    return sc_qk(B, L, H, 0 if k is None else k.shape[2], D, R, sq, none if k is None else _strides(k),
+                 _strides(qo), none if k is None else _strides(ko), none if dq is None else _strides(dq),
+                 none if dk is None else _strides(dk), eps, bool(interleaved), _ptr(inv_freq) if R else None,
+                 _ptr(positions), _ptr(kv_len))
 
 
 def qk_norm_rotary(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tensor | None = None,
@@ -144,12 +144,10 @@ def qk_norm_rotary(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tens
     (sc_qk_norm_rotary).  Positions: ``positions`` (B, L) int32, or the last L of each sequence of
     ``kv_len`` (B,) int32, or 0 .. L - 1.  q_out may be q itself, k_out k."""
     kind = _check(q, k, q_weight, k_weight, q_out, k_out)
-    a = _qk_args(q, k, q_weight, k_weight, inv_freq, positions, kv_len, interleaved, eps)
     q_out = _out(q_out, q, "q_out")
-    a.q_out = _strides(q_out)
     if k is not None:
         k_out = _out(k_out, k, "k_out")
-        a.k_out = _strides(k_out)
+    a = _qk_args(q, k, q_out, k_out, None, None, q_weight, k_weight, inv_freq, positions, kv_len, interleaved, eps)
     _run("qk_norm_rotary", _lib.sc_qk_norm_rotary, q.device, kind, ctypes.byref(a), q.data_ptr(), _ptr(k),
          _ptr(q_weight), _ptr(k_weight), q_out.data_ptr(), _ptr(k_out))
     return q_out, k_out
@@ -166,14 +164,12 @@ def qk_norm_rotary_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor | None, q: tor
     of its results, from its inputs (sc_qk_norm_rotary_bwd); ``params`` false: no weight gradients
     (None)."""
     kind = _check(q, dq_out, dk_out, k, q_weight, k_weight, dq, dk)
-    a = _qk_args(q, k, q_weight, k_weight, inv_freq, positions, kv_len, interleaved, eps)
     if dq_out.shape != q.shape or (k is None) != (dk_out is None) or (k is not None and dk_out.shape != k.shape):
         raise ValueError("dq_out and dk_out must have the shapes of q and k")
     dq = _out(dq, q, "dq")
-    a.q_out, a.dq = _strides(dq_out), _strides(dq)
     if k is not None:
         dk = _out(dk, k, "dk")
-        a.k_out, a.dk = _strides(dk_out), _strides(dk)
+    a = _qk_args(q, k, dq_out, dk_out, dq, dk, q_weight, k_weight, inv_freq, positions, kv_len, interleaved, eps)
     dwq = dwk = None
     if params:
         dwq = torch.empty(a.D, dtype=q.dtype, device=q.device)
