@@ -4,7 +4,9 @@ Layers, each on layer-normalised activations with a residual connection, as the 
 "Caracal: Causal Architecture via Spectral Mixing" arrange them: causal convolution layers
 (v and a data-dependent gate stream from the same input), window attention with a distance bias
 (positional encodings are removed), and a gated recurrence.  Projections are torch matmuls; the
-mixing and the norms, forward and backward, are this library's kernels.
+mixing and the norms, forward and backward, are this library's kernels.  With ``rotary`` the attention
+layers norm and rotate their queries and keys instead of the bias, and decoding can hold its caches in
+8 bits, a window of them with the first tokens kept visible.
 
     python examples/hybrid_stack.py            # a few steps of training, then decoding
 """
@@ -68,6 +70,30 @@ class WindowAttention(torch.autograd.Function):
         return dqkv, None, None, None, None, None
 
 
+class NormRotary(torch.autograd.Function):
+    """The q, k, v columns of one projection with q and k normed and rotated."""
+
+    @staticmethod
+    def forward(ctx, qkv, wq, wk, freq, H, Hkv):
+        out = torch.empty_like(qkv)
+        (q, k, v), (qo, ko, vo) = columns(qkv, H, Hkv), columns(out, H, Hkv)
+        sc.qk_norm_rotary(q, k, wq, wk, freq, q_out=qo, k_out=ko)
+        vo.copy_(v)
+        ctx.save_for_backward(qkv, wq, wk, freq)
+        ctx.args = H, Hkv
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        qkv, wq, wk, freq = ctx.saved_tensors
+        H, Hkv = ctx.args
+        dqkv, dout = torch.empty_like(qkv), dout.contiguous()
+        (q, k, _), (dqo, dko, dvo), (dq, dk, dv) = (columns(t, H, Hkv) for t in (qkv, dout, dqkv))
+        _, _, dwq, dwk = sc.qk_norm_rotary_bwd(dqo, dko, q, k, wq, wk, freq, dq=dq, dk=dk)
+        dv.copy_(dvo)
+        return dqkv, dwq, dwk, None, None, None
+
+
 class Recurrence(torch.autograd.Function):
     """h of the z, u halves of one projection (B, L, 2 C)."""
 
@@ -93,10 +119,11 @@ def columns(qkv, H, Hkv):
 
 
 class Stack(torch.nn.Module):
-    """`layout`: one letter a layer, c convolution, a attention, r recurrence."""
+    """`layout`: one letter a layer, c convolution, a attention, r recurrence.  `rotary`: attention layers
+    norm and rotate their queries and keys, in place of the distance bias."""
 
     def __init__(self, vocab=64, C=128, heads=4, kv_heads=2, D=32, window=32, layout="ccar",
-                 dtype=torch.bfloat16, device="cuda", seed=0):
+                 dtype=torch.bfloat16, device="cuda", seed=0, rotary=False):
         super().__init__()
         gen = torch.Generator().manual_seed(seed)
         self.layout, self.H, self.Hkv, self.D, self.window = layout, heads, kv_heads, D, window
@@ -113,6 +140,11 @@ class Stack(torch.nn.Module):
         self.norm_w = torch.nn.ParameterList([torch.nn.Parameter(torch.ones(C, dtype=dtype, device=device)) for _ in range(n)])
         self.norm_b = torch.nn.ParameterList([torch.nn.Parameter(torch.zeros(C, dtype=dtype, device=device)) for _ in range(n)])
         self.slopes = torch.tensor([2.0 ** (-8 * (h + 1) / heads) for h in range(heads)], device=device)
+        self.freq = None
+        if rotary:
+            self.slopes, self.freq = None, 10000.0 ** (-torch.arange(0, D, 2, device=device) / D)
+            self.q_w, self.k_w = (torch.nn.ParameterList(
+                [torch.nn.Parameter(torch.ones(D, dtype=dtype, device=device)) for _ in range(layout.count("a"))]) for _ in "qk")
 
     def forward(self, tokens, doc_start=None):
         """Logits (B, L, vocab) in float32."""
@@ -123,6 +155,9 @@ class Stack(torch.nn.Module):
                 v, s = p.transpose(1, 2).chunk(2, 1)
                 m = CausalConv.apply(v.contiguous(), (torch.sigmoid(s) / tokens.shape[1] ** 0.5).contiguous()).transpose(1, 2)
             elif kind == "a":
+                if self.freq is not None:
+                    a = self.layout[:i].count("a")
+                    p = NormRotary.apply(p, self.q_w[a], self.k_w[a], self.freq, self.H, self.Hkv)
                 m = WindowAttention.apply(p, self.H, self.Hkv, self.window, self.slopes, doc_start)
             else:
                 m = Recurrence.apply(p)
@@ -132,12 +167,15 @@ class Stack(torch.nn.Module):
     # ---- one token at a time (attention and recurrence layers: a convolution's output depends on
     # its whole past, it has no state of fixed size)
 
-    def start(self, B, length):
-        """The caches and states of an empty sequence of up to `length` tokens."""
+    def start(self, B, length, cache=None):
+        """The caches and states of an empty sequence of up to `length` tokens; `cache` "int8" or "e4m3":
+        caches of 8-bit codes."""
         dev, dt = self.embed.device, self.embed.dtype
         state = []
         for kind in self.layout:
-            if kind == "a":
+            if kind == "a" and cache:
+                state.append(sc.KVCache(B, length, self.Hkv, self.D, cache, device=dev))
+            elif kind == "a":
                 state.append(torch.zeros(2, B, length, self.Hkv, self.D, dtype=dt, device=dev))
             elif kind == "r":
                 state.append(torch.zeros(B, self.embed.shape[1], device=dev))
@@ -146,8 +184,9 @@ class Stack(torch.nn.Module):
         return state, torch.zeros(B, dtype=torch.int32, device=dev)
 
     @torch.no_grad()
-    def step(self, tokens, state, lengths):
-        """Logits (B, vocab) of the next tokens (B,); caches, states and lengths move on."""
+    def step(self, tokens, state, lengths, sinks=0):
+        """Logits (B, vocab) of the next tokens (B,); caches, states and lengths move on.  `sinks`: first
+        tokens that 8-bit caches keep visible past the window."""
         x = self.embed[tokens][:, None]
         rows = torch.arange(len(tokens), device=tokens.device)
         at = lengths.long()
@@ -156,9 +195,16 @@ class Stack(torch.nn.Module):
             p = sc.layer_norm(x, self.norm_w[i], self.norm_b[i]) @ self.w_in[i]
             if kind == "a":
                 q, k, v = columns(p, self.H, self.Hkv)
-                state[i][0][rows, at], state[i][1][rows, at] = k[:, 0], v[:, 0]
-                m = sc.causal_attention(q, state[i][0], state[i][1], window=self.window, slopes=self.slopes,
-                                        kv_len=lengths).flatten(2)
+                if self.freq is not None:
+                    a = self.layout[:i].count("a")
+                    sc.qk_norm_rotary(q, k, self.q_w[a], self.k_w[a], self.freq, kv_len=lengths, q_out=q, k_out=k)
+                if isinstance(state[i], sc.KVCache):
+                    sc.cache_write(state[i], k, v, lengths)
+                    m = sc.cached_attention(q, state[i], lengths, window=self.window, sinks=sinks, slopes=self.slopes).flatten(2)
+                else:
+                    state[i][0][rows, at], state[i][1][rows, at] = k[:, 0], v[:, 0]
+                    m = sc.causal_attention(q, state[i][0], state[i][1], window=self.window, slopes=self.slopes,
+                                            kv_len=lengths).flatten(2)
             else:
                 C = p.shape[-1] // 2
                 m, _ = sc.gated_recurrence(p[..., :C], p[..., C:], state[i], hT=state[i])
@@ -209,6 +255,14 @@ def main():
         logits = model.step(x[:, t], state, lengths)
     full = model(x).detach()[:, -1]
     print("after 64 tokens one at a time, logits within %.3g of the whole sequence's" % float((logits - full).abs().max()))
+    model = Stack(layout="ara", rotary=True)
+    train(model, say=None)
+    full = model(x).detach()[:, -1]
+    for code in ("int8", "e4m3"):
+        state, lengths = model.start(4, 96, code)
+        for t in range(x.shape[1]):
+            logits = model.step(x[:, t], state, lengths)
+        print("normed and rotated, caches in %s: within %.3g" % (code, float((logits - full).abs().max())))
 
 
 if __name__ == "__main__":
