@@ -13,7 +13,7 @@ import math
 import torch
 
 from . import SC_ERR_UNSUPPORTED, SpecConvError, _lib
-from .layers import _check, _int3, _out, _ptr, _run, _scratch, _strides, _typed
+from .layers import _check, _int3, _out, _ptr, _run, _scratch, _typed
 
 __all__ = [
     "qk_norm_rotary", "qk_norm_rotary_bwd", "KVCache", "cache_write", "cache_read",
@@ -98,39 +98,63 @@ def sc_cached_attn(kind, c, a, q, o, lse, ws, ws_bytes, stream):
 
 # ---------------------------------------------------------------- norm and rotation
 
-def _lengths(kv_len, B):
-    if tuple(kv_len.shape) != (B,):
-        raise ValueError("kv_len must be (B,)")
+# A decoding step is a handful of microseconds, most of them spent in these functions: they look at each
+# tensor once and fill a struct in one go.
+
+_NONE = (0, 0, 0)
+
+
+def _bld(t):
+    """The {batch, token, head} strides of a (B, L, H, D) tensor (an axis of one place: whatever it says)."""
+    s = t.stride()
+    if len(s) != 4:
+        raise ValueError("tensors must be (B, L, H, D)")
+    if s[3] != 1 and t.shape[3] > 1:
+        raise ValueError("the D values of a head must be contiguous")
+    return s[:3]
+
+
+def _lengths(kv_len, B, dev):
+    if kv_len.dtype != torch.int32 or kv_len.shape != (B,) or not kv_len.is_contiguous():
+        raise ValueError("kv_len must be a contiguous int32 (B,) tensor")
+    if kv_len.device != dev:
+        raise ValueError("tensors must be on the same GPU")
+    return kv_len.data_ptr()
 
 
 def _qk_args(q, k, qo, ko, dq, dk, q_weight, k_weight, inv_freq, positions, kv_len, interleaved, eps):
     """The call's struct; qo, ko: the results, or their gradients."""
-    _typed(q, torch.float32, inv_freq)
-    _typed(q, torch.int32, positions, kv_len)
-    sq = _strides(q)
+    sq = _bld(q)
     B, L, H, D = q.shape
-    if k is not None and (k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != D):
-        raise ValueError("k must be (B, L, Hkv, D) for q (B, L, H, D)")
+    Hkv, sk, sko, sdk = 0, _NONE, _NONE, _NONE
+    if k is not None:
+        sk, sko = _bld(k), _bld(ko)
+        Hkv = k.shape[2]
+        if k.shape != (B, L, Hkv, D):
+            raise ValueError("k must be (B, L, Hkv, D) for q (B, L, H, D)")
+        if dk is not None:
+            sdk = _bld(dk)
     for w in (q_weight, k_weight):
-        if w is not None and (tuple(w.shape) != (D,) or not w.is_contiguous()):
+        if w is not None and (w.shape != (D,) or not w.is_contiguous()):
             raise ValueError("q_weight and k_weight must be contiguous (D,) tensors")
-    R = 0
+    R, f, pos, n = 0, None, None, None
     if inv_freq is not None:
+        _typed(q, torch.float32, inv_freq)
         if inv_freq.dim() != 1 or 2 * inv_freq.shape[0] > D:
             raise ValueError("inv_freq must hold at most D / 2 values")
         R = 2 * inv_freq.shape[0]
+        f = inv_freq.data_ptr() if R else None
     if positions is not None:
+        _typed(q, torch.int32, positions)
         if kv_len is not None:
             raise ValueError("positions and kv_len exclude each other")
-        if tuple(positions.shape) != (B, L):
+        if positions.shape != (B, L):
             raise ValueError("positions must be (B, L)")
+        pos = positions.data_ptr()
     if kv_len is not None:
-        _lengths(kv_len, B)
-    none = _int3()
-    return sc_qk(B, L, H, 0 if k is None else k.shape[2], D, R, sq, none if k is None else _strides(k),
-                 _strides(qo), none if k is None else _strides(ko), none if dq is None else _strides(dq),
-                 none if dk is None else _strides(dk), eps, bool(interleaved), _ptr(inv_freq) if R else None,
-                 _ptr(positions), _ptr(kv_len))
+        n = _lengths(kv_len, B, q.device)
+    return sc_qk(B, L, H, Hkv, D, R, sq, sk, _bld(qo), sko, _NONE if dq is None else _bld(dq), sdk, eps,
+                 bool(interleaved), f, pos, n)
 
 
 def qk_norm_rotary(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tensor | None = None,
@@ -233,23 +257,22 @@ class KVCache:
 
 
 def _cache_kv(cache, k, v, kv_len):
+    """The checked call's strides of k and v and pointer of kv_len."""
     if k.device != cache.device:
         raise ValueError("tensors must be on the cache's GPU")
-    _typed(k, torch.int32, kv_len)
-    sk, sv = _strides(k), _strides(v)
-    if k.shape != v.shape or (k.shape[0], k.shape[2], k.shape[3]) != (cache.B, cache.Hkv, cache.D):
+    sk, sv = _bld(k), _bld(v)
+    if k.shape != v.shape or k.shape != (cache.B, k.shape[1], cache.Hkv, cache.D):
         raise ValueError("k and v must be (B, L, Hkv, D) of the cache's sizes")
-    _lengths(kv_len, cache.B)
-    return sk, sv
+    return _int3(*sk), _int3(*sv), _lengths(kv_len, cache.B, cache.device)
 
 
 def cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, kv_len: torch.Tensor) -> None:
     """Stores k, v (B, L, Hkv, D) as the last L tokens of each sequence of kv_len (B,) int32
     (sc_cache_write); what a sequence held from there on is given up."""
     kind = _check(k, v)
-    sk, sv = _cache_kv(cache, k, v, kv_len)
+    sk, sv, n = _cache_kv(cache, k, v, kv_len)
     _run("cache_write", _lib.sc_cache_write, k.device, kind, cache._ref, k.data_ptr(), sk, v.data_ptr(), sv,
-         k.shape[1], kv_len.data_ptr())
+         k.shape[1], n)
 
 
 def cache_read(cache: KVCache, L: int, kv_len: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
@@ -260,13 +283,12 @@ def cache_read(cache: KVCache, L: int, kv_len: torch.Tensor, dtype: torch.dtype 
     if k is None:
         k = torch.empty(shape, dtype=dtype, device=cache.device)
     if v is None:
-        v = torch.empty(shape, dtype=dtype, device=cache.device)
+        v = torch.empty_like(k) if k.is_contiguous() else torch.empty(shape, dtype=dtype, device=cache.device)
     kind = _check(k, v)
-    sk, sv = _cache_kv(cache, k, v, kv_len)
+    sk, sv, n = _cache_kv(cache, k, v, kv_len)
     if k.shape[1] != L or k.dtype != dtype:
         raise ValueError("k and v must be (B, L, Hkv, D) of the asked dtype")
-    _run("cache_read", _lib.sc_cache_read, k.device, kind, cache._ref, k.data_ptr(), sk, v.data_ptr(), sv, L,
-         kv_len.data_ptr())
+    _run("cache_read", _lib.sc_cache_read, k.device, kind, cache._ref, k.data_ptr(), sk, v.data_ptr(), sv, L, n)
     return k, v
 
 
@@ -280,18 +302,17 @@ def cached_attention(q: torch.Tensor, cache: KVCache, kv_len: torch.Tensor, *, w
     kind = _check(q, out)
     if q.device != cache.device:
         raise ValueError("tensors must be on the cache's GPU")
-    _typed(q, torch.float32, slopes)
-    _typed(q, torch.int32, kv_len)
-    sq = _strides(q)
+    sq = _bld(q)
     B, Lq, H, D = q.shape
     if B != cache.B or D != cache.D:
         raise ValueError("q must be (B, Lq, H, D) of the cache's B and D")
-    _lengths(kv_len, B)
-    if slopes is not None and tuple(slopes.shape) != (H,):
-        raise ValueError("slopes must be (H,)")
+    if slopes is not None:
+        _typed(q, torch.float32, slopes)
+        if slopes.shape != (H,):
+            raise ValueError("slopes must be (H,)")
     o = _out(out, q, "out")
-    a = sc_cached(Lq, H, sq, _strides(o), (1.0 / math.sqrt(D) if D else 1.0) if scale is None else float(scale),
-                  float(cap), int(window), int(sinks), _ptr(slopes), kv_len.data_ptr())
+    a = sc_cached(Lq, H, sq, _bld(o), (1.0 / math.sqrt(D) if D else 1.0) if scale is None else scale, cap, window, sinks,
+                  _ptr(slopes), _lengths(kv_len, B, q.device))
     if lse and D == 0 and B * H * Lq:   # the call has no result to write then, and no lse
         raise SpecConvError(SC_ERR_UNSUPPORTED, "cached_attention: lse of heads of no values")
     L = torch.empty((B, H, Lq), dtype=torch.float32, device=q.device) if lse else None
