@@ -349,7 +349,7 @@ struct QkArgs {
     bool whole;              // every row starts 16-byte aligned
     // set by the launchers
     int tb, turns;           // tokens of a turn; turns of a sequence
-    uint32_t all;            // turns
+    uint32_t all, wgs[2];    // turns; workgroups of q's rows, of k's
     float* part;             // backward: sums of dw by workgroup
 };
 hipError_t launch_qk(Store st, const QkArgs& a, hipStream_t stream);

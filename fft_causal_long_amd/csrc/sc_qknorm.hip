@@ -196,9 +196,20 @@ __device__ __forceinline__ float rstd_of(float v)
     return __builtin_amdgcn_rsqf(low ? v * 0x1p64f : v) * (low ? 0x1p32f : 1.f);
 }
 
+// The first wgs[0] workgroups take q's rows, the others k's, each their tokens in turns.
+struct Share {
+    int s;
+    uint32_t id, step;
+    __device__ __forceinline__ Share(const QkArgs& a)
+        : s(blockIdx.x >= a.wgs[0]), id(blockIdx.x - (s ? a.wgs[0] : 0u)), step(s ? a.wgs[1] : a.wgs[0])
+    {
+    }
+    // where this workgroup's sums of dw go
+    __device__ __forceinline__ float* part(const QkArgs& a) const { return a.part + (int64_t)blockIdx.x * a.D; }
+};
+
 // Rows of a workgroup's tokens in turn, a row's loads issued before the row before it is finished: LPR
-// lanes a row, D / 2V of them with values.  Backward, q's tokens first and then k's, so that one set of
-// sums for dw is held.
+// lanes a row, D / 2V of them with values.
 template <class IO, int V, int LPR, bool PAIRS, bool BWD>
 __global__ __launch_bounds__(NT) void qk_rows(QkArgs a)
 {
@@ -211,19 +222,34 @@ __global__ __launch_bounds__(NT) void qk_rows(QkArgs a)
     const bool on = 2 * V * l < a.D;
     const int lv = on ? l : 0;
     const Cut<V, PAIRS> cut(a.R, lv);
+    using RowT = Row<IO, V, PAIRS>;
     const float inv = 1.0f / (float)a.D;
     struct Raw {
         typename W::Raw xa, xb, ga, gb;
     };
 
-    auto tensor = [&](int s, uint32_t turn, float (&dw)[2][V], bool angles) {
+    const Share share(a);
+    const int H = share.s ? a.H[1] : a.H[0];
+    const auto pick = [&](const int64_t(&t)[2][3], int i) { return share.s ? t[1][i] : t[0][i]; };
+    const E* wp = (const E*)(share.s ? a.w[1] : a.w[0]);
+    RowT w;
+    if (wp) {
+        w.from(W::load(wp + cut.a), W::load(wp + cut.b));
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) w.a[i] = w.b[i] = 1.f;
+    }
+    float dw[2][V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) dw[0][i] = dw[1][i] = 0.f;
+
+    for (uint32_t turn = share.id; turn < a.all; turn += share.step) {
         const Span span(a, turn);
-        const int H = s ? a.H[1] : a.H[0], rows = span.n * H;
-        const auto pick = [&](const int64_t(&t)[2][3], int i) { return s ? t[1][i] : t[0][i]; };
-        Walk walk(slot, RPP, std::max(H, 1));
-        Path<const E> x((const E*)(s ? a.x[1] : a.x[0]), pick(a.xs, 0), pick(a.xs, 1), pick(a.xs, 2), span, walk);
-        Path<const E> g((const E*)(s ? a.dy[1] : a.dy[0]), pick(a.dys, 0), pick(a.dys, 1), pick(a.dys, 2), span, walk);
-        Path<E> y((E*)(s ? a.y[1] : a.y[0]), pick(a.ys, 0), pick(a.ys, 1), pick(a.ys, 2), span, walk);
+        const int rows = span.n * H;
+        Walk walk(slot, RPP, H);
+        Path<const E> x((const E*)(share.s ? a.x[1] : a.x[0]), pick(a.xs, 0), pick(a.xs, 1), pick(a.xs, 2), span, walk);
+        Path<const E> g((const E*)(share.s ? a.dy[1] : a.dy[0]), pick(a.dys, 0), pick(a.dys, 1), pick(a.dys, 2), span, walk);
+        Path<E> y((E*)(share.s ? a.y[1] : a.y[0]), pick(a.ys, 0), pick(a.ys, 1), pick(a.ys, 2), span, walk);
         Raw now;
         auto load = [&] {
             now.xa = W::load(x.p + cut.a);
@@ -234,23 +260,13 @@ __global__ __launch_bounds__(NT) void qk_rows(QkArgs a)
             }
         };
         if (slot < rows) load();
-        const E* wp = (const E*)(s ? a.w[1] : a.w[0]);
-        Row<IO, V, PAIRS> w;
-        if (wp) {
-            w.from(W::load(wp + cut.a), W::load(wp + cut.b));
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) w.a[i] = w.b[i] = 1.f;
-        }
-        if (angles) {
-            __syncthreads();
-            fill_angles(a, table, span);
-            __syncthreads();
-        }
+        __syncthreads();
+        fill_angles(a, table, span);
+        __syncthreads();
         for (int r = slot; r < rows; r += RPP) {
             const float2* cs = table + walk.i * half + lv * V;
             E* yp = y.p;
-            Row<IO, V, PAIRS> v, e;
+            RowT v, e;
             v.from(now.xa, now.xb);
             if constexpr (BWD) e.from(now.ga, now.gb);
             const bool wrap = walk.next();
@@ -297,38 +313,24 @@ __global__ __launch_bounds__(NT) void qk_rows(QkArgs a)
             }
             if (on) v.to(yp, cut);
         }
-    };
-    float dw[2][V];
-    if constexpr (!BWD) {
-        for (uint32_t turn = blockIdx.x; turn < a.all; turn += gridDim.x)
-#pragma unroll 1
-            for (int s = 0; s < 2; ++s) tensor(s, turn, dw, s == 0);
-    } else {
-#pragma unroll 1
-        for (int s = 0; s < 2; ++s) {
+    }
+    if constexpr (BWD) {
+        if (!a.part) return;
+        // the rows of a wave, then the waves
 #pragma unroll
-            for (int i = 0; i < V; ++i) dw[0][i] = dw[1][i] = 0.f;
-            for (uint32_t turn = blockIdx.x; turn < a.all; turn += gridDim.x) tensor(s, turn, dw, true);
-            if (!a.part) continue;
-            // the rows of a wave, then the waves
-            __syncthreads();
+        for (int k = 0; k < 2 * V; ++k) {
+            float x = dw[k / V][k % V];
 #pragma unroll
-            for (int k = 0; k < 2 * V; ++k) {
-                float x = dw[k / V][k % V];
+            for (int m = LPR; m < 64; m <<= 1) x += __shfl_xor(x, m);
+            if ((threadIdx.x & 63) < LPR) sum[threadIdx.x >> 6][k * LPR + l] = x;
+        }
+        __syncthreads();
+        if (slot != 0 || !on) return;
+        float* out = share.part(a);
 #pragma unroll
-                for (int m = LPR; m < 64; m <<= 1) x += __shfl_xor(x, m);
-                if ((threadIdx.x & 63) < LPR) sum[threadIdx.x >> 6][k * LPR + l] = x;
-            }
-            __syncthreads();
-            if (slot == 0 && on) {
-                float* out = a.part + ((int64_t)blockIdx.x * 2 + s) * a.D;
-#pragma unroll
-                for (int k = 0; k < 2 * V; ++k) {
-                    const int at = k * LPR + l, i = k % V;
-                    out[PAIRS ? cut.a + 2 * i + k / V : (k < V ? cut.a : cut.b) + i] =
-                        (sum[0][at] + sum[1][at]) + (sum[2][at] + sum[3][at]);
-                }
-            }
+        for (int k = 0; k < 2 * V; ++k) {
+            const int at = k * LPR + l, i = k % V;
+            out[PAIRS ? cut.a + 2 * i + k / V : (k < V ? cut.a : cut.b) + i] = (sum[0][at] + sum[1][at]) + (sum[2][at] + sum[3][at]);
         }
     }
 }
@@ -352,30 +354,30 @@ __global__ __launch_bounds__(NT) void qk_pairs(QkArgs a)
         if (ia[k] >= a.D) ia[k] = -1;
         if (ib[k] >= a.D) ib[k] = -1;
     }
-    float dw[BWD ? 2 : 1][2][PAIRS];
-    if constexpr (BWD)
+    const Share share(a);
+    const int s = share.s, H = s ? a.H[1] : a.H[0];
+    const auto pick = [&](const int64_t(&t)[2][3], int i) { return s ? t[1][i] : t[0][i]; };
+    const E *xp = (const E*)(s ? a.x[1] : a.x[0]), *gp = (const E*)(s ? a.dy[1] : a.dy[0]), *w = (const E*)(s ? a.w[1] : a.w[0]);
+    E* yp = (E*)(s ? a.y[1] : a.y[0]);
+    float dw[2][PAIRS];
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int k = 0; k < PAIRS; ++k) dw[s][0][k] = dw[s][1][k] = 0.f;
+    for (int k = 0; k < PAIRS; ++k) dw[0][k] = dw[1][k] = 0.f;
     auto get = [](const E* p, int i) { return i < 0 ? 0.f : IO::load(p, i); };
 
-    for (uint32_t turn = blockIdx.x; turn < a.all; turn += gridDim.x) {
+    for (uint32_t turn = share.id; turn < a.all; turn += share.step) {
         const Span span(a, turn);
         __syncthreads();
         fill_angles(a, table, span);
         __syncthreads();
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int rows = span.n * a.H[s];
-            const E* w = (const E*)a.w[s];
-            Walk walk(wave, NT / 64, std::max(a.H[s], 1));
+        {
+            const int rows = span.n * H;
+            Walk walk(wave, NT / 64, H);
             for (int r = wave; r < rows; r += NT / 64, walk.next()) {
                 const int i = walk.i;
                 const int64_t t = span.t0 + i;
-                const E* x = (const E*)a.x[s] + span.b * a.xs[s][0] + t * a.xs[s][1] + walk.h * a.xs[s][2];
-                const E* g = BWD ? (const E*)a.dy[s] + span.b * a.dys[s][0] + t * a.dys[s][1] + walk.h * a.dys[s][2] : nullptr;
-                E* y = (E*)a.y[s] + span.b * a.ys[s][0] + t * a.ys[s][1] + walk.h * a.ys[s][2];
+                const E* x = xp + span.b * pick(a.xs, 0) + t * pick(a.xs, 1) + walk.h * pick(a.xs, 2);
+                const E* g = BWD ? gp + span.b * pick(a.dys, 0) + t * pick(a.dys, 1) + walk.h * pick(a.dys, 2) : nullptr;
+                E* y = yp + span.b * pick(a.ys, 0) + t * pick(a.ys, 1) + walk.h * pick(a.ys, 2);
                 float va[PAIRS], vb[PAIRS], ea[PAIRS], eb[PAIRS], wa[PAIRS], wb[PAIRS], sq = 0.f, ex = 0.f;
 #pragma unroll
                 for (int k = 0; k < PAIRS; ++k) {
@@ -399,8 +401,8 @@ __global__ __launch_bounds__(NT) void qk_pairs(QkArgs a)
                     float oa, ob;
                     if constexpr (BWD) {
                         const float na = va[k] * rstd, nb = vb[k] * rstd;
-                        dw[s][0][k] += ea[k] * na;
-                        dw[s][1][k] += eb[k] * nb;
+                        dw[0][k] += ea[k] * na;
+                        dw[1][k] += eb[k] * nb;
                         oa = (ea[k] * wa[k] - na * m) * rstd;
                         ob = (eb[k] * wb[k] - nb * m) * rstd;
                     } else {
@@ -417,40 +419,38 @@ __global__ __launch_bounds__(NT) void qk_pairs(QkArgs a)
     }
     if constexpr (BWD) {
         if (!a.part) return;
-        __shared__ float sum[4][2][2][64 * PAIRS];
+        __shared__ float sum[4][2][64 * PAIRS];
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int k = 0; k < PAIRS; ++k) {
+            sum[wave][0][64 * k + lane] = dw[0][k];
+            sum[wave][1][64 * k + lane] = dw[1][k];
+        }
+        __syncthreads();
+        float* out = share.part(a);
+        if (wave < 2) {   // wave 0 the pairs' first values, wave 1 the second
 #pragma unroll
             for (int k = 0; k < PAIRS; ++k) {
-                sum[wave][s][0][64 * k + lane] = dw[s][0][k];
-                sum[wave][s][1][64 * k + lane] = dw[s][1][k];
+                const int at = 64 * k + lane, i = wave ? ib[k] : ia[k];
+                const float x = (sum[0][wave][at] + sum[1][wave][at]) + (sum[2][wave][at] + sum[3][wave][at]);
+                if (i >= 0) out[i] = x;
             }
-        __syncthreads();
-        float* out = a.part + (int64_t)blockIdx.x * 2 * a.D;
-        if (wave < 2) {
-#pragma unroll
-            for (int k = 0; k < PAIRS; ++k)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int at = 64 * k + lane, i = j ? ib[k] : ia[k];
-                    const float x = (sum[0][wave][j][at] + sum[1][wave][j][at]) + (sum[2][wave][j][at] + sum[3][wave][j][at]);
-                    if (i >= 0) out[wave * a.D + i] = x;
-                }
         }
     }
 }
 
 // dw = the workgroups' sums added: 4 columns a workgroup, 64 threads a column, whose loads are all in
-// flight at once (1024 parts: 16 a thread).
+// flight at once (up to 1024 parts: 16 a thread).
 template <class IO>
-__global__ __launch_bounds__(NT) void qk_sum(QkArgs a, int parts)
+__global__ __launch_bounds__(NT) void qk_sum(QkArgs a)
 {
     __shared__ float sum[NT];
-    const int at = blockIdx.x * 4 + threadIdx.x % 4;
+    const int at = blockIdx.x * 4 + threadIdx.x % 4, s = at >= a.D;
     float x = 0.f;
     if (at < 2 * a.D) {
+        const float* p = a.part + (s ? (int64_t)a.wgs[0] * a.D : 0) + (at - s * a.D);
+        const int parts = (int)a.wgs[s];
 #pragma unroll 16
-        for (int p = threadIdx.x / 4; p < parts; p += 64) x += a.part[(int64_t)p * 2 * a.D + at];
+        for (int k = threadIdx.x / 4; k < parts; k += 64) x += p[(int64_t)k * a.D];
     }
     sum[threadIdx.x] = x;
     __syncthreads();
@@ -466,19 +466,20 @@ __global__ __launch_bounds__(NT) void qk_sum(QkArgs a, int parts)
 
 // Tokens of a turn (of one sequence): fewer while the workgroups do not fill the GPU, up to what 16 KB
 // of angles hold.
-constexpr int64_t FILL = 1024, MOST = 1 << 20;   // MOST: what a launch holds; they walk the rest
+constexpr int64_t FILL = 2048, MOST = 1 << 20;   // MOST: what a launch holds; they walk the rest
 constexpr int ANGLES = 2048;
 struct Plan {
-    int64_t tb, turns, all, wgs;   // turns of a sequence, of all of them
+    int64_t tb, turns, all, wgs[2];   // turns of a sequence, of all of them; workgroups of q's rows, of k's
 };
 Plan plan(const QkArgs& a, bool bwd)
 {
-    const int64_t half = (a.D + 1) / 2;
+    const int64_t half = (a.D + 1) / 2, most = bwd ? FILL : MOST, heads = (int64_t)a.H[0] + a.H[1];
     Plan p;
     p.tb = std::max<int64_t>(1, std::min<int64_t>({a.tokens / FILL, ANGLES / half, a.L}));
     p.turns = (a.L + p.tb - 1) / p.tb;
     p.all = a.B * p.turns;
-    p.wgs = std::min(p.all, bwd ? FILL : MOST);
+    for (int s = 0; s < 2; ++s)
+        p.wgs[s] = a.H[s] == 0 ? 0 : std::max<int64_t>(1, std::min(p.all, most * a.H[s] / heads));
     return p;
 }
 
@@ -491,7 +492,9 @@ hipError_t go(QkArgs a, hipStream_t st)
     a.turns = (int)p.turns;
     if (p.all > INT32_MAX) return hipErrorInvalidValue;   // (the walk's 32 bits)
     a.all = (uint32_t)p.all;
-    const dim3 grid((unsigned)p.wgs), block(NT);
+    a.wgs[0] = (uint32_t)p.wgs[0];
+    a.wgs[1] = (uint32_t)p.wgs[1];
+    const dim3 grid(a.wgs[0] + a.wgs[1]), block(NT);
     const size_t lds = (size_t)a.tb * ((a.D + 1) / 2) * sizeof(float2);
     const int lanes = a.D / (2 * V);
     const bool whole = a.whole && a.D % (2 * V) == 0 && (a.pairs || a.R % (2 * V) == 0);   // rows of whole lanes
@@ -516,13 +519,15 @@ template <class IO>
 hipError_t bwd(QkArgs a, void* ws, hipStream_t st)
 {
     a.part = a.dw[0] || a.dw[1] ? (float*)ws : nullptr;
-    if (a.tokens > 0) {
+    if (a.tokens > 0) {   // (else sums of no rows)
         const hipError_t e = go<IO, true>(a, st);
         if (e != hipSuccess || !a.part) return e;
+        const Plan p = plan(a, true);
+        a.wgs[0] = (uint32_t)p.wgs[0];
+        a.wgs[1] = (uint32_t)p.wgs[1];
     }
     if (!a.dw[0] && !a.dw[1]) return hipSuccess;
-    const int parts = a.tokens > 0 ? (int)plan(a, true).wgs : 0;   // none: sums of no rows
-    hipLaunchKernelGGL(qk_sum<IO>, dim3((2 * a.D + 3) / 4), dim3(NT), 0, st, a, parts);
+    hipLaunchKernelGGL(qk_sum<IO>, dim3((2 * a.D + 3) / 4), dim3(NT), 0, st, a);
     return hipGetLastError();
 }
 
@@ -535,7 +540,9 @@ hipError_t launch_qk(Store s, const QkArgs& a, hipStream_t st)
 
 size_t qk_bwd_bytes(Store, const QkArgs& a)
 {
-    return a.tokens > 0 ? (size_t)plan(a, true).wgs * 2 * a.D * sizeof(float) : 0;
+    if (a.tokens == 0) return 0;
+    const Plan p = plan(a, true);
+    return (size_t)(p.wgs[0] + p.wgs[1]) * a.D * sizeof(float);
 }
 
 hipError_t launch_qk_bwd(Store s, const QkArgs& a, void* ws, hipStream_t st)
