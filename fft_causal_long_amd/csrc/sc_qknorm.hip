@@ -12,7 +12,7 @@
 // Bound by memory: two elements a value move forward, three backward.  A lane holds the pairs it
 // turns: the 16-byte vectors at l V and R/2 + l V of a row, or two neighbouring vectors where
 // neighbours are pairs, so a row is read once and turned without an exchange, and its sums are a
-// few shuffles.  Rows that are not such vectors go pair by pair, a wave a row.  The angles of a
+// few shuffles.  Rows that are not such vectors are read in shorter ones, or value by value.  The angles of a
 // token are the same for all its heads: a workgroup makes those of its tokens once, one a thread,
 // in LDS, while its first rows are on their way.
 
@@ -77,16 +77,28 @@ struct Vec {
     }
 };
 
+// One value at a time: rows that start anywhere.
+template <class IO>
+struct Vec<IO, 1> {
+    typedef float Raw;
+    __device__ __forceinline__ static Raw load(const typename IO::T* p) { return IO::load(p, 0); }
+    __device__ __forceinline__ static float at(Raw r, int) { return r; }
+    __device__ __forceinline__ static void store(typename IO::T* p, const float (&x)[1]) { IO::store(p, 0, x[0]); }
+};
+
 // Where lane l of a row's D / 2V finds its V pairs: the elements a + i and b + i, or, of a vector pair
 // a, b = a + V, neighbours (PAIRS).  Pairs past R / 2 are the values that do not turn.
 template <int V, bool PAIRS>
 struct Cut {
     int a, b;
-    __device__ __forceinline__ Cut(int R, int l)
+    bool lone;   // one value at a time: the last of an odd D has no second (b is it again)
+    __device__ __forceinline__ Cut(int R, int D, int l)
     {
         const bool halves = !PAIRS && V * l < R / 2;
         a = halves ? V * l : 2 * V * l;
         b = halves ? R / 2 + a : a + V;
+        lone = V == 1 && b >= D;
+        if (lone) b = a;
     }
 };
 
@@ -95,8 +107,13 @@ template <class IO, int V, bool PAIRS>
 struct Row {
     using W = Vec<IO, V>;
     float a[V], b[V];
-    __device__ __forceinline__ void from(const typename W::Raw& u, const typename W::Raw& v)
+    __device__ __forceinline__ void from(const typename W::Raw& u, const typename W::Raw& v, const Cut<V, PAIRS>& c)
     {
+        if constexpr (V == 1) {
+            a[0] = W::at(u, 0);
+            b[0] = c.lone ? 0.f : W::at(v, 0);
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             a[i] = !PAIRS ? W::at(u, i) : 2 * i < V ? W::at(u, 2 * i % V) : W::at(v, 2 * i % V);
@@ -105,6 +122,11 @@ struct Row {
     }
     __device__ __forceinline__ void to(typename IO::T* p, const Cut<V, PAIRS>& c) const
     {
+        if constexpr (V == 1) {
+            W::store(p + c.a, a);
+            if (!c.lone) W::store(p + c.b, b);
+            return;
+        }
         float x[V], y[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -221,7 +243,7 @@ __global__ __launch_bounds__(NT) void qk_rows(QkArgs a)
     const int l = threadIdx.x % LPR, slot = threadIdx.x / LPR, half = (a.D + 1) / 2;
     const bool on = 2 * V * l < a.D;
     const int lv = on ? l : 0;
-    const Cut<V, PAIRS> cut(a.R, lv);
+    const Cut<V, PAIRS> cut(a.R, a.D, lv);
     using RowT = Row<IO, V, PAIRS>;
     const float inv = 1.0f / (float)a.D;
     struct Raw {
@@ -234,7 +256,7 @@ __global__ __launch_bounds__(NT) void qk_rows(QkArgs a)
     const E* wp = (const E*)(share.s ? a.w[1] : a.w[0]);
     RowT w;
     if (wp) {
-        w.from(W::load(wp + cut.a), W::load(wp + cut.b));
+        w.from(W::load(wp + cut.a), W::load(wp + cut.b), cut);
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) w.a[i] = w.b[i] = 1.f;
@@ -267,8 +289,8 @@ __global__ __launch_bounds__(NT) void qk_rows(QkArgs a)
             const float2* cs = table + walk.i * half + lv * V;
             E* yp = y.p;
             RowT v, e;
-            v.from(now.xa, now.xb);
-            if constexpr (BWD) e.from(now.ga, now.gb);
+            v.from(now.xa, now.xb, cut);
+            if constexpr (BWD) e.from(now.ga, now.gb, cut);
             const bool wrap = walk.next();
             y.next(wrap);
             if (r + RPP < rows) {   // else the same row again, for nothing: no branch around the loads
@@ -330,12 +352,13 @@ __global__ __launch_bounds__(NT) void qk_rows(QkArgs a)
 #pragma unroll
         for (int k = 0; k < 2 * V; ++k) {
             const int at = k * LPR + l, i = k % V;
+            if (V == 1 && k == 1 && cut.lone) continue;
             out[PAIRS ? cut.a + 2 * i + k / V : (k < V ? cut.a : cut.b) + i] = (sum[0][at] + sum[1][at]) + (sum[2][at] + sum[3][at]);
         }
     }
 }
 
-// Any rows: a wave a row, a lane the pairs lane, lane + 64, ...
+// Any rows of more than 128 values: a wave a row, a lane the pairs lane, lane + 64, ...
 constexpr int PAIRS = 4;   // D up to 512
 template <class IO, bool BWD>
 __global__ __launch_bounds__(NT) void qk_pairs(QkArgs a)
@@ -466,16 +489,16 @@ __global__ __launch_bounds__(NT) void qk_sum(QkArgs a)
 
 // Tokens of a turn (of one sequence): fewer while the workgroups do not fill the GPU, up to what 16 KB
 // of angles hold.
-constexpr int64_t FILL = 2048, MOST = 1 << 20;   // MOST: what a launch holds; they walk the rest
+constexpr int64_t FILL = 4096, FILL_BWD = 2048, MOST = 1 << 20;   // MOST: what a launch holds; they walk the rest
 constexpr int ANGLES = 2048;
 struct Plan {
     int64_t tb, turns, all, wgs[2];   // turns of a sequence, of all of them; workgroups of q's rows, of k's
 };
 Plan plan(const QkArgs& a, bool bwd)
 {
-    const int64_t half = (a.D + 1) / 2, most = bwd ? FILL : MOST, heads = (int64_t)a.H[0] + a.H[1];
+    const int64_t half = (a.D + 1) / 2, most = bwd ? FILL_BWD : MOST, heads = (int64_t)a.H[0] + a.H[1];
     Plan p;
-    p.tb = std::max<int64_t>(1, std::min<int64_t>({a.tokens / FILL, ANGLES / half, a.L}));
+    p.tb = std::max<int64_t>(1, std::min<int64_t>({a.tokens / (bwd ? FILL_BWD : FILL), ANGLES / half, a.L}));
     p.turns = (a.L + p.tb - 1) / p.tb;
     p.all = a.B * p.turns;
     for (int s = 0; s < 2; ++s)
@@ -486,7 +509,6 @@ Plan plan(const QkArgs& a, bool bwd)
 template <class IO, bool BWD>
 hipError_t go(QkArgs a, hipStream_t st)
 {
-    constexpr int V = BWD ? 4 : vec_elems<IO>;   // values of a load: see below
     const Plan p = plan(a, BWD);
     a.tb = (int)p.tb;
     a.turns = (int)p.turns;
@@ -496,22 +518,30 @@ hipError_t go(QkArgs a, hipStream_t st)
     a.wgs[1] = (uint32_t)p.wgs[1];
     const dim3 grid(a.wgs[0] + a.wgs[1]), block(NT);
     const size_t lds = (size_t)a.tb * ((a.D + 1) / 2) * sizeof(float2);
-    const int lanes = a.D / (2 * V);
-    const bool whole = a.whole && a.D % (2 * V) == 0 && (a.pairs || a.R % (2 * V) == 0);   // rows of whole lanes
-    if (!whole) {
-        hipLaunchKernelGGL((qk_pairs<IO, BWD>), grid, block, lds, st, a);
-        return hipGetLastError();
-    }
-    auto rows = [&](auto lpr) {
-        constexpr int LPR = decltype(lpr)::value;
+    // V pairs a lane where the rows are whole lanes of them: 16-byte vectors forward, half of them backward
+    // (half the registers: B 4, L 4096, 20 heads of 128 bf16 57 us, 68 with 16 bytes), half or a quarter
+    // where the sizes ask for it, else single values
+    auto fits = [&](int v) { return a.whole && a.D % (2 * v) == 0 && (a.pairs || a.R % (2 * v) == 0); };
+    auto rows = [&](auto v, auto lpr) {
+        constexpr int V = decltype(v)::value, LPR = decltype(lpr)::value;
         if (a.pairs) hipLaunchKernelGGL((qk_rows<IO, V, LPR, true, BWD>), grid, block, lds, st, a);
         else hipLaunchKernelGGL((qk_rows<IO, V, LPR, false, BWD>), grid, block, lds, st, a);
     };
-    if (lanes <= 4) rows(std::integral_constant<int, 4>());
-    else if (lanes <= 8) rows(std::integral_constant<int, 8>());
-    else if (lanes <= 16) rows(std::integral_constant<int, 16>());
-    else if (lanes <= 32) rows(std::integral_constant<int, 32>());
-    else rows(std::integral_constant<int, 64>());
+    using std::integral_constant;
+    auto lanes = [&](auto v) {
+        const int n = (a.D + 2 * decltype(v)::value - 1) / (2 * decltype(v)::value);
+        if (n <= 4) rows(v, integral_constant<int, 4>());
+        else if (n <= 8) rows(v, integral_constant<int, 8>());
+        else if (n <= 16) rows(v, integral_constant<int, 16>());
+        else if (n <= 32) rows(v, integral_constant<int, 32>());
+        else rows(v, integral_constant<int, 64>());
+    };
+    constexpr int W = vec_elems<IO>;
+    if (!BWD && W == 8 && fits(8)) lanes(integral_constant<int, W>());
+    else if (fits(4)) lanes(integral_constant<int, 4>());
+    else if (fits(2) && a.D <= 256) lanes(integral_constant<int, 2>());
+    else if (a.D <= 128) lanes(integral_constant<int, 1>());
+    else hipLaunchKernelGGL((qk_pairs<IO, BWD>), grid, block, lds, st, a);
     return hipGetLastError();
 }
 

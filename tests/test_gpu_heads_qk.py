@@ -53,6 +53,15 @@ CASES = [
     ("bf16", 2, 9, 2, 0, 64, 64, False, "row", "dense"),       # no k
     ("bf16", 2, 9000, 1, 1, 64, 64, False, "row", "dense"),    # more tokens than workgroups hold at once
     ("f32", 1, 2100, 3, 2, 40, 20, True, "list", "odd"),
+    ("f32", 2, 5, 3, 2, 20, 12, False, "list", "dense"),       # vectors of every length
+    ("bf16", 2, 5, 3, 2, 40, 20, False, "list", "dense"),
+    ("bf16", 2, 5, 3, 2, 40, 24, False, "len", "columns"),
+    ("bf16", 2, 5, 3, 2, 40, 30, True, "len", "heads"),
+    ("bf16", 2, 5, 3, 2, 64, 26, False, "list", "dense"),
+    ("f32", 2, 5, 3, 2, 120, 58, False, "list", "columns"),
+    ("bf16", 2, 5, 3, 2, 127, 126, False, "list", "odd"),
+    ("f32", 2, 5, 3, 2, 129, 128, True, "len", "odd"),
+    ("f32", 2, 700, 3, 2, 256, 132, False, "len", "dense"),
 ]
 
 
