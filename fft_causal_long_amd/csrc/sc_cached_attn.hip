@@ -21,6 +21,21 @@
 // its next block on its way in registers, and join their results through LDS; keys are split over
 // workgroups to fill the GPU.  More rows: a wave has rows of its own; a block's codes are turned into
 // half precision once, a quarter by each wave, and shared through two LDS places.
+//
+// Measured (MI355X; a large copy moves 5.4 TB/s, reads alone up to 6.3, a half-precision product of 8192^3
+// reaches 1200 TFLOP/s), whole calls:
+//  * 8 sequences over ragged caches of up to 65536, one token, 16 heads of 64 on 4, int8: 43 us, of it 38 the
+//    kernel (5.5 TB/s of the codes) and 4.6 the join: bound by the codes' bytes.  Loads past the caches took it
+//    there from 50 (44 the kernel).  The same in bfloat16 caches: 88.
+//  * 32 sequences, window 256 and 4 sinks, 16 heads of 64, e4m3 in a pool: 9 us of kernel, five blocks a
+//    workgroup: the chain length, table, codes, scores.
+//  * 4 sequences of up to 10007, 5 tokens, 12 heads of 64, float32, capped: 17 us and 4 of join for 50 MB:
+//    the same chain before the bytes, three blocks a wave.
+//  * 2048 tokens over 8192, 16 heads of 128 on 4, int8: 172 us, 700 TFLOP/s of the products that the mask
+//    leaves (sc_causal_attn on bfloat16: 228).  Vector instructions (176 for 16 x 64 scores, of them 64 the
+//    conversion, 16 exponentials) and the products share the issue: 46% and 26% of the cycles at 1.7 waves a
+//    SIMD.  Four waves a SIMD (the keys of a block in two halves) changed nothing, the next block's conversion
+//    placed beside the first product made it 198, each wave converting for itself 257.
 
 #include <hip/hip_runtime.h>
 
@@ -549,19 +564,28 @@ __global__ __launch_bounds__(NT) void cached_join(AttnArgs a)
         a.lse[((int64_t)b * a.H + h) * a.Lq + i] = sum > 0.f ? (mx + __builtin_amdgcn_logf(sum)) * LN2 : -INFINITY;
 }
 
-// Rows of a workgroup: 16 shared by four waves for the few rows of decoding, else 64 or 128.
+// Rows of a workgroup: 16 shared by four waves for the few rows of decoding; else 128, which convert a
+// block's codes once for all of them, or 64 where these fill the GPU once (heads up to 64 hold twice the
+// workgroups a CU) and 128 would leave half of it empty.  Workgroups of 128 against 64, int8 codes: 16
+// heads of 64 on 4, B 3, 1024 tokens over 4096 (384 of 128) 91 and 78 us; 16 on 16, B 8 (1024) 175 and 193;
+// heads of 128 on 4, 2048 over 8192 (256) 182 and 173, B 3, 1024 over 4096 (384) 131 and 146; 64 tokens over 4
+// caches of 16384 (32, keys split) 59 and 67.
 constexpr int FEW = 16;
-constexpr int64_t TWO_A_CU = 512, FILL = 512;
+constexpr int64_t FILL = 512;
 int tile_rows(const AttnArgs& a)
 {
     if (a.nrow <= FEW) return 16;
     const int64_t w128 = (a.nrow + 127) / 128 * (int64_t)a.nbh, w64 = (a.nrow + 63) / 64 * (int64_t)a.nbh;
-    return w128 > TWO_A_CU || (a.nrow > 64 && 2 * w64 <= FILL) ? 128 : 64;
+    return w128 > (a.D <= 64 ? FILL : FILL / 2) || (a.nrow > 64 && 2 * w64 <= FILL) ? 128 : 64;
 }
 
-// Key splits while the rows do not fill the GPU, each of at least SPLIT_MIN keys.
+// Key splits while the rows do not fill the GPU, each of at least SPLIT_MIN keys; the second launch costs
+// what few of them gain (one token, 4 key heads, whole calls: 1000 keys 16.4 us split and 11.8 not, 2500
+// keys 16.4 and 13.3, 3500 keys 16.5 in 6 parts and not).  8 caches of up
+// to 65536, 4 key heads, one token: 768 workgroups 44.0 us, 512 43.5, 1024 45.5, 1536 44.5; 64 caches of up
+// to 4096 47, 48, 46, 47; 4 of up to 10007, 12 heads, 5 tokens, float32: 21, 21, 24, 24.
 constexpr int64_t FILL_FEW = 768, SPLIT_MIN = 512;
-constexpr int64_t SPLIT_MAX = NT;   // the join weighs one split a thread
+constexpr int64_t SPLIT_LEAST = 5, SPLIT_MAX = NT;   // the join weighs one split a thread
 
 int splits(const AttnArgs& a, int sinks)
 {
@@ -569,7 +593,8 @@ int splits(const AttnArgs& a, int sinks)
     const int64_t wgs = (a.nrow + bm - 1) / bm * (int64_t)a.nbh, fill = a.nrow <= FEW ? FILL_FEW : FILL;
     const int64_t keys = std::min<int64_t>(a.Lk, (int64_t)a.window + sinks + std::min<int64_t>(a.Lq, bm));
     if (wgs <= 0 || 2 * wgs > fill) return 1;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({(fill + wgs - 1) / wgs, keys / SPLIT_MIN, SPLIT_MAX}));
+    const int64_t n = std::min<int64_t>({(fill + wgs - 1) / wgs, keys / SPLIT_MIN, SPLIT_MAX});
+    return n < (a.nrow <= FEW ? SPLIT_LEAST : 2) ? 1 : (int)n;
 }
 
 template <class IO, Code CODE, int J, class S>

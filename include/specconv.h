@@ -595,8 +595,7 @@ sc_status sc_qk_norm_rotary_bwd(sc_kind kind, const sc_qk* a, const void* dq_out
  * head}; rows are 16-byte aligned.
  *
  *  sc_cache_write -- stores k, v (B, L, Hkv, D).  What a sequence held at kv_len[b] and beyond is given up.
- *  sc_cache_read -- the values of the last L positions as k, v (B, L, Hkv, D): exact, but for bfloat16
- *      results of magnitudes below its range.
+ *  sc_cache_read -- the values of the last L positions as k, v (B, L, Hkv, D): exact in both kinds.
  *  sc_cached_attn -- causal attention of q (B, Lq, H, D) over the cache, as sc_causal_attn: query i at
  *      position p = kv_len[b] - Lq + i sees key j <= p when j > p - window (window 0: always) or
  *      j < sinks, the first tokens that stay visible;
