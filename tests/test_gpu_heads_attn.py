@@ -189,3 +189,72 @@ def test_offsets_past_32_bits(sc):
         (ro, rl), (bo, bl) = ref.cached_attention(qx, kx, vx, [180, 170], float(np.float32(128 ** -0.5)), bf16=True)
         check(o, ro, bo, "bf16", "o")
         check(lse, rl, bl, "f32", "lse")
+
+
+EDGES = [
+    # dtype, code, B, T, Lq, H, Hkv, D, window, sinks, lens
+    ("bf16", "e4m3", 2, 64, 1, 1, 1, 112, 0, 0, [64, 63]),          # a block to its end
+    ("f32", "int8", 2, 128, 64, 1, 1, 16, 64, 0, [128, 64]),        # a window of a block
+    ("bf16", "int8", 1, 129, 1, 16, 1, 64, 0, 0, [129]),            # sixteen rows, one token in the last block
+    ("bf16", "int8", 1, 129, 17, 1, 1, 64, 3, 200, [128]),          # seventeen; more sinks than tokens
+    ("f32", "e4m3", 3, 320, 2, 24, 3, 128, 64, 64, [320, 129, 128]),   # a window that begins where sinks end
+    ("bf16", "e4m3", 1, 256, 256, 5, 5, 48, 1, 1, [256]),
+    ("bf16", "int8", 40, 100, 1, 4, 2, 32, 10, 2, [100 - 2 * i for i in range(40)]),
+]
+
+
+@pytest.mark.parametrize("case", EDGES, ids=lambda c: "-".join(map(str, c[:10])))
+def test_edges_of_blocks_and_windows(sc, case):
+    print("case attn8 edges", case, flush=True)
+    dtype, code, B, T, Lq, H, Hkv, D, window, sinks, lens = case
+    rng = np.random.default_rng(T + Lq)
+    c, kx, vx, live = filled(sc, rng, B, T, Hkv, D, code, lens)
+    q, qx = draw(rng, (B, Lq, H, D), dtype, 1.5)
+    o, lse = sc.cached_attention(q, c, lengths(*lens), window=window, sinks=sinks, scale=0.2, lse=True)
+    (ro, rl), (bo, bl) = ref.cached_attention(qx, kx, vx, lens, float(np.float32(0.2)), window, sinks, bf16=dtype == "bf16")
+    check(o, ro, bo, dtype, "o")
+    check(lse, rl, bl, "f32", "lse")
+
+
+def test_blocks_of_zeros(sc):
+    # a block whose values are all 0 has the smallest scale: its weights count all the same
+    print("case attn8 zeros", flush=True)
+    for code in ("int8", "e4m3"):
+        for dtype in ("f32", "bf16"):
+            rng = np.random.default_rng(7)
+            c = sc.KVCache(1, 192, 1, 64, code, device=DEV)
+            k, _ = draw(rng, (1, 192, 1, 64), "f32")
+            v, _ = draw(rng, (1, 192, 1, 64), "f32")
+            v[:, :64] = 0
+            k[:, 64:128] = 0
+            sc.cache_write(c, k, v, lengths(192))
+            kx, vx = (f64(t) for t in sc.cache_read(c, 192, lengths(192), torch.float32))
+            for Lq, n in ((1, 192), (1, 64), (3, 64), (70, 150)):
+                q, qx = draw(rng, (1, Lq, 3, 64), dtype)
+                o, lse = sc.cached_attention(q, c, lengths(n), lse=True)
+                (ro, rl), (bo, bl) = ref.cached_attention(qx, kx, vx, [n], 0.125, bf16=dtype == "bf16")
+                check(o, ro, bo, dtype, "o")
+                check(lse, rl, bl, "f32", "lse")
+
+
+def test_a_table_that_changes(sc):
+    # sequences take another's blocks: by new values in the table, and by another tensor
+    print("case attn8 tables", flush=True)
+    rng = np.random.default_rng(9)
+    table = torch.tensor([[0, 1], [2, 3]], dtype=torch.int32, device=DEV)
+    c = sc.KVCache(2, 128, 2, 64, "int8", device=DEV, blocks=6, table=table)
+    k, _ = draw(rng, (2, 100, 2, 64), "bf16")
+    sc.cache_write(c, k, k, lengths(100, 90))
+    q, _ = draw(rng, (1, 1, 2, 64), "bf16")
+    q = q.expand(2, 1, 2, 64).contiguous()
+    a = sc.cached_attention(q, c, lengths(100, 90))
+    table.copy_(torch.tensor([[2, 3], [0, 1]]))
+    b = sc.cached_attention(q, c, lengths(90, 100))
+    assert torch.equal(a[0], b[1]) and torch.equal(a[1], b[0])
+    c.table = torch.tensor([[0, 1], [0, 1]], dtype=torch.int32, device=DEV)
+    d = sc.cached_attention(q, c, lengths(100, 100))
+    assert torch.equal(d[0], a[0]) and torch.equal(d[1], a[0])
+    c.table = None              # row b's blocks are 2 b, 2 b + 1 again
+    assert torch.equal(sc.cached_attention(q, c, lengths(100, 90)), a)
+    with pytest.raises(ValueError):
+        c.table = torch.zeros(2, 3, dtype=torch.int32, device=DEV)
