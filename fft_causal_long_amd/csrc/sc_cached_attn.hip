@@ -10,7 +10,11 @@
 // One pass with a running base and sum, in base 2.  Codes are exact in half precision, so both products
 // run on the half-precision matrix instruction: a query row is multiplied by the power of two that
 // brings its largest value to 2^14 .. 2^15 (bfloat16 values then are exact down to 2^-29 of it; float32
-// ones are the sum of two halves, 2^-22 of each), and a weight carries 11 bits (float32: two halves).  A
+// ones are the sum of two halves, 2^-22 of each).  A weight is two halves in float32 calls and in those
+// of few rows.  In bfloat16 calls of more rows it is one, 11 bits: off by 2^-12 of itself at most, a
+// sixteenth of the result's own rounding, while the second half and its product took a quarter to a third
+// of the call (2048 tokens after 6144, 16 heads of 128 on 4: 214 us for 172; B 8, 1024 tokens over 4096, 16
+// heads of 64: 236 for 173; but one token over the caches of the first call below: 45.3 for 43.8).  A
 // block's vs goes into the weights' exponent, w = 2^(s + log2 vs - base), so that every weight is
 // relative to the row's largest contribution to o, whatever the scales; the sum takes w / vs.
 // The heads that share a key head are packed into one row axis, scores are made transposed (keys x
@@ -155,6 +159,7 @@ __global__ __launch_bounds__((64 * S::NW), 2) void cached_attn(AttnArgs a, Cache
 {
     using E = typename IO::T;
     constexpr int NQ = S::NQ, NW = S::NW, WM = S::WM, BM = S::BM, ND = 4 * J, P = IO::SIZE == 4 ? 2 : 1;
+    constexpr int PW = S::KEYS ? 2 : P;   // halves of q, of a weight
     constexpr int DP = 64 * J, STAGE = 2 * T * DP * 2;
     // what the waves join, or two blocks in half precision
     constexpr int LDS = S::KEYS ? NW * WM * (DP + 2) * 4 : 2 * STAGE;
@@ -293,7 +298,7 @@ __global__ __launch_bounds__((64 * S::NW), 2) void cached_attn(AttnArgs a, Cache
         }
         const bool edge = j0 + T - 1 > w0 || (j0 < wlast && j0 + T > sinks);
         const float vexp = (float)ve, vback = power(-ve);
-        half8_t w[NQ][2][P];
+        half8_t w[NQ][2][PW];
 #pragma unroll
         for (int m = 0; m < NQ; ++m) {
             // Scores in base 2 with the block's vs, less the row's base: the running maximum as it was
@@ -356,7 +361,7 @@ __global__ __launch_bounds__((64 * S::NW), 2) void cached_attn(AttnArgs a, Cache
                 const float x[8] = {s[2 * k][m][0], s[2 * k][m][1], s[2 * k][m][2], s[2 * k][m][3],
                                     s[2 * k + 1][m][0], s[2 * k + 1][m][1], s[2 * k + 1][m][2], s[2 * k + 1][m][3]};
                 w[m][k][0] = halves_of(x);
-                if constexpr (P == 2) w[m][k][1] = rest_of(x, w[m][k][0]);
+                if constexpr (PW == 2) w[m][k][1] = rest_of(x, w[m][k][0]);
             }
         }
 #pragma unroll
@@ -367,7 +372,7 @@ __global__ __launch_bounds__((64 * S::NW), 2) void cached_attn(AttnArgs a, Cache
 #pragma unroll
                 for (int m = 0; m < NQ; ++m)
 #pragma unroll
-                    for (int p = 0; p < P; ++p) o[d][m] = mma(f, w[m][k][p], o[d][m]);
+                    for (int p = 0; p < PW; ++p) o[d][m] = mma(f, w[m][k][p], o[d][m]);
             }
         }
     };

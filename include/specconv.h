@@ -603,9 +603,10 @@ sc_status sc_qk_norm_rotary_bwd(sc_kind kind, const sc_qk* a, const void* dq_out
  *          o_i = sum_j softmax(s)_j v_j,   lse_i = log sum_j exp(s_j)  (lse (B, H, Lq) float32 or null)
  *      A row that sees nothing gives o = 0, lse = -infinity.  Products run on the codes in half precision
  *      with float32 sums: a query row enters scaled by a power of two (bfloat16 exact down to 2^-29 of
- *      its largest value, float32 as two halves), weights with 11 bits (float32: two halves).  Cached
- *      values of existing positions must be finite (an e4m3 NaN may reach other rows).  H a multiple of
- *      Hkv; ws as for sc_causal_attn, sc_cached_attn_workspace_bytes(kind, c, a) bytes.
+ *      its largest value, float32 as two halves), a weight as two halves, 22 bits, in float32 and where
+ *      Lq H / Hkv <= 16, else as one, 11 bits.  Cached values of existing positions must be finite (an
+ *      e4m3 NaN may reach other rows).  H a multiple of Hkv; ws as for sc_causal_attn,
+ *      sc_cached_attn_workspace_bytes(kind, c, a) bytes.
  */
 #define SC_CACHE_BLOCK 64
 enum { SC_CODE_I8 = 0, SC_CODE_E4M3 = 1 };
