@@ -550,7 +550,8 @@ __global__ __launch_bounds__(NT) void cached_join(AttnArgs a)
     const float mx = over_block(ls, wave, true);
     const float e = ls == -INFINITY ? 0.f : exp2_hw(ls - mx);
     const float sum = over_block(e, wave, false);
-    weight[t] = sum > 0.f ? e / sum : 0.f;
+    const bool none = sum == 0.f;   // (a sum of NaN is not empty: the row is NaN)
+    weight[t] = none ? 0.f : e / sum;
     __syncthreads();
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
     const float* p = a.part + at * a.D + (d0 < a.D ? d0 : 0);
@@ -566,7 +567,7 @@ __global__ __launch_bounds__(NT) void cached_join(AttnArgs a)
         put4<IO>((typename IO::T*)a.o + b * a.os[0] + (int64_t)i * a.os[1] + h * a.os[2] + d0, x);
     }
     if (a.lse && t == 0)
-        a.lse[((int64_t)b * a.H + h) * a.Lq + i] = sum > 0.f ? (mx + __builtin_amdgcn_logf(sum)) * LN2 : -INFINITY;
+        a.lse[((int64_t)b * a.H + h) * a.Lq + i] = none ? -INFINITY : (mx + __builtin_amdgcn_logf(sum)) * LN2;
 }
 
 // Rows of a workgroup: 16 shared by four waves for the few rows of decoding; else 128, which convert a
