@@ -316,7 +316,8 @@ __global__ __launch_bounds__(NT) void attn_join(AttnArgs a)
     float sum = e;
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
-    if (wave == 0) weight[lane] = sum > 0.f ? e / sum : 0.f;
+    const bool none = sum == 0.f;   // (a sum of NaN is not empty: the row is NaN)
+    if (wave == 0) weight[lane] = none ? 0.f : e / sum;
     const int bh = (int)(at / a.nrow), r = (int)(at % a.nrow);
     const int b = bh / a.Hkv, i = r / a.G, h = bh % a.Hkv * a.G + r % a.G;
     E* op = (E*)a.o + b * a.os[0] + (int64_t)i * a.os[1] + h * a.os[2];
@@ -332,7 +333,7 @@ __global__ __launch_bounds__(NT) void attn_join(AttnArgs a)
             IO::store(op, d0 + lane, (sum4[0][lane] + sum4[1][lane]) + (sum4[2][lane] + sum4[3][lane]));
     }
     if (a.lse && threadIdx.x == 0)
-        a.lse[((int64_t)b * a.H + h) * a.Lq + i] = sum > 0.f ? (mx + __builtin_amdgcn_logf(sum)) * LN2 : -INFINITY;
+        a.lse[((int64_t)b * a.H + h) * a.Lq + i] = none ? -INFINITY : (mx + __builtin_amdgcn_logf(sum)) * LN2;
 }
 
 // Rows of a workgroup: 16 (one wave) for the few rows of decoding, where waves without rows would
