@@ -210,12 +210,34 @@ def qk_norm_rotary_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor | None, q: tor
 _CODES = {"int8": CODE_I8, "e4m3": CODE_E4M3}
 
 
+def _fixed(name):
+    return property(lambda self: getattr(self, name))
+
+
+def _memory(name):
+    """The cache's memory `name`, whose address the calls take from the struct."""
+    held = "_" + name
+
+    def put(self, t):
+        now = getattr(self, held)
+        if t.dtype != now.dtype or t.shape != now.shape or t.device != now.device or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous %s %s tensor on the cache's device" % (name, tuple(now.shape), now.dtype))
+        setattr(self, held, t)
+        setattr(self._struct, name, t.data_ptr())
+    return property(lambda self: getattr(self, held), put)
+
+
 class KVCache:
     """k and v of B sequences of up to ``length`` tokens in 8-bit codes, one scale for each 64 tokens
     of a head: ``code`` "int8" or "e4m3".  ``blocks``: blocks in the pool (default: enough for every
     sequence); ``table`` (B, N) int32, N = ceil(length / 64): each sequence's blocks in the pool
-    (default: row b's are b N .. b N + N - 1).  The table's values may change between calls; another
-    tensor may take its place through the attribute."""
+    (default: row b's are b N .. b N + N - 1).  The table's values may change between calls.  Other
+    tensors may take the place of ``table``, ``k``, ``v``, ``k_scale`` and ``v_scale`` through these
+    attributes (a block is a row of the last four); the sizes and the code stay.  ``copy.copy`` is a cache
+    over the same memory with attributes of its own, ``copy.deepcopy`` has memory of its own."""
+
+    B, N, blocks, Hkv, D, code, device = map(_fixed, ("_B", "_N", "_blocks", "_Hkv", "_D", "_code", "_device"))
+    k, v, k_scale, v_scale = map(_memory, ("k", "v", "k_scale", "v_scale"))
 
     def __init__(self, B: int, length: int, Hkv: int, D: int, code: str = "int8", *, device="cuda",
                  blocks: int | None = None, table: torch.Tensor | None = None):
@@ -227,17 +249,31 @@ class KVCache:
             raise ValueError("sizes must not be negative, D a multiple of 16 up to 128")
         if table is None and P < B * N:
             raise ValueError("a pool smaller than B N blocks needs a table")
-        self.B, self.N, self.blocks, self.Hkv, self.D, self.code = B, N, P, Hkv, D, code
+        self._B, self._N, self._blocks, self._Hkv, self._D, self._code = B, N, P, Hkv, D, code
         dev = torch.device(device)
-        self.k = torch.empty(P, Hkv, CACHE_BLOCK * D, dtype=torch.uint8, device=dev)
-        self.v = torch.empty_like(self.k)
-        self.k_scale = torch.zeros(P, Hkv, dtype=torch.float32, device=dev)
-        self.v_scale = torch.zeros_like(self.k_scale)
-        self.device = self.k.device
-        self._struct = sc_cache(B, N, P, Hkv, D, _CODES[code], self.k.data_ptr(), self.v.data_ptr(),
-                                self.k_scale.data_ptr(), self.v_scale.data_ptr(), None)
-        self._ref = ctypes.byref(self._struct)
+        self._k = torch.empty(P, Hkv, CACHE_BLOCK * D, dtype=torch.uint8, device=dev)
+        self._v = torch.empty_like(self._k)
+        self._k_scale = torch.zeros(P, Hkv, dtype=torch.float32, device=dev)
+        self._v_scale = torch.zeros_like(self._k_scale)
+        self._device = self._k.device
+        self._table = None
+        self._bind()
         self.table = table
+
+    def _bind(self):
+        """The struct that the calls take, of what the attributes hold."""
+        self._struct = sc_cache(self._B, self._N, self._blocks, self._Hkv, self._D, _CODES[self._code],
+                                *(t.data_ptr() for t in (self._k, self._v, self._k_scale, self._v_scale)), _ptr(self._table))
+        self._ref = ctypes.byref(self._struct)
+
+    # a copy, or what was pickled, has a struct of its own
+    def __getstate__(self):
+        return {n: x for n, x in self.__dict__.items() if n not in ("_struct", "_ref")}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        self._device = self._k.device
+        self._bind()
 
     @property
     def table(self):
@@ -246,11 +282,11 @@ class KVCache:
     @table.setter
     def table(self, table):
         if table is None:
-            if self.blocks < self.B * self.N:
+            if self._blocks < self._B * self._N:
                 raise ValueError("a pool smaller than B N blocks needs a table")
         else:
-            if table.dtype != torch.int32 or not table.is_contiguous() or table.device != self.device \
-                    or tuple(table.shape) != (self.B, self.N):
+            if table.dtype != torch.int32 or not table.is_contiguous() or table.device != self._device \
+                    or tuple(table.shape) != (self._B, self._N):
                 raise ValueError("table must be a contiguous int32 (B, N) tensor on the cache's device")
         self._table = table
         self._struct.table = _ptr(table)
@@ -258,12 +294,12 @@ class KVCache:
 
 def _cache_kv(cache, k, v, kv_len):
     """The checked call's strides of k and v and pointer of kv_len."""
-    if k.device != cache.device:
+    if k.device != cache._device:
         raise ValueError("tensors must be on the cache's GPU")
     sk, sv = _bld(k), _bld(v)
-    if k.shape != v.shape or k.shape != (cache.B, k.shape[1], cache.Hkv, cache.D):
+    if k.shape != v.shape or k.shape != (cache._B, k.shape[1], cache._Hkv, cache._D):
         raise ValueError("k and v must be (B, L, Hkv, D) of the cache's sizes")
-    return _int3(*sk), _int3(*sv), _lengths(kv_len, cache.B, cache.device)
+    return _int3(*sk), _int3(*sv), _lengths(kv_len, cache._B, cache._device)
 
 
 def cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, kv_len: torch.Tensor) -> None:
@@ -279,11 +315,11 @@ def cache_read(cache: KVCache, L: int, kv_len: torch.Tensor, dtype: torch.dtype 
                k: torch.Tensor | None = None, v: torch.Tensor | None = None):
     """(k, v) (B, L, Hkv, D): the values of the last L tokens of each sequence of kv_len (B,) int32, 0
     before its first (sc_cache_read); ``k`` and ``v`` are written if given."""
-    shape = (cache.B, L, cache.Hkv, cache.D)
+    shape = (cache._B, L, cache._Hkv, cache._D)
     if k is None:
-        k = torch.empty(shape, dtype=dtype, device=cache.device)
+        k = torch.empty(shape, dtype=dtype, device=cache._device)
     if v is None:
-        v = torch.empty_like(k) if k.is_contiguous() else torch.empty(shape, dtype=dtype, device=cache.device)
+        v = torch.empty_like(k) if k.is_contiguous() else torch.empty(shape, dtype=dtype, device=cache._device)
     kind = _check(k, v)
     sk, sv, n = _cache_kv(cache, k, v, kv_len)
     if k.shape[1] != L or k.dtype != dtype:
@@ -300,11 +336,11 @@ def cached_attention(q: torch.Tensor, cache: KVCache, kv_len: torch.Tensor, *, w
     int32, over ``cache`` (sc_cached_attn), options as :func:`causal_attention`; with a ``window`` the
     first ``sinks`` tokens stay visible.  ``lse``: returns (o, lse), lse (B, H, Lq) float32."""
     kind = _check(q, out)
-    if q.device != cache.device:
+    if q.device != cache._device:
         raise ValueError("tensors must be on the cache's GPU")
     sq = _bld(q)
     B, Lq, H, D = q.shape
-    if B != cache.B or D != cache.D:
+    if B != cache._B or D != cache._D:
         raise ValueError("q must be (B, Lq, H, D) of the cache's B and D")
     if slopes is not None:
         _typed(q, torch.float32, slopes)
