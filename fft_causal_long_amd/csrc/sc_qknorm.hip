@@ -38,15 +38,17 @@ namespace {
 
 constexpr int NT = 256;
 
-// cos and sin of p f.  The product is exact in 64 bits for |p| < 2^29; the quarter turns are taken
-// off it with 2 / pi in two parts, so the rest is right to 2^-53 of a quarter turn whatever p, and
-// Taylor series (to x^9 and x^10, the next terms under 2e-9) then give float32 values.
+// cos and sin of p f.  The product has up to 55 bits: a double and what that leaves.  The quarter turns are
+// taken off it with 2 / pi in two parts, so for angles under 2^48 the rest is right to 2^-53 of a quarter
+// turn (2 / pi is good to 2^-108; the number of turns is off by 2^-6 at most before it is rounded), and
+// Taylor series (to x^9 and x^10, the next terms under 3e-9) then give float32 values.
 __device__ __forceinline__ float2 turn_of(int p, float f)
 {
-    const double a = (double)p * (double)f;
+    const double a = (double)p * (double)f, left = fma((double)p, (double)f, -a);
     const double n = rint(a * 0.63661977236758134308);
     double r = fma(a, 0.63661977236758134308, -n);
     r = fma(a, -3.9357353350364971764e-17, r);   // 2 / pi less its double
+    r = fma(left, 0.63661977236758134308, r);
     const float x = (float)(r * 1.57079632679489661923);
     const int q = (int)(n - 4.0 * floor(n * 0.25));
     const float z = x * x;

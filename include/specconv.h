@@ -537,8 +537,8 @@ sc_status sc_causal_attn_bwd(sc_kind kind, const sc_attn* a, const void* dout, c
  *     y_a = n_a cos theta - n_b sin theta,   y_b = n_b cos theta + n_a sin theta
  * pair i being the values i and i + R / 2, or 2 i and 2 i + 1 (interleaved = 1); values from R on stay n.
  * p is the token's position: positions[b][t], or kv_len[b] - L + t (the last L positions of each
- * sequence, as attention counts them; not both), or t.  The angle is taken in 64 bits, so it is good to
- * float32 precision at any position (exactly p times the float32 inv_freq for |p| < 2^29).
+ * sequence, as attention counts them; not both), or t.  The angle is p times the float32 inv_freq, exactly,
+ * reduced in 64 bits: good to float32 precision at any position, for angles under 2^48.
  *
  *  sc_qk_norm_rotary -- q (B, L, H, D) to q_out, k (B, L, Hkv, D) to k_out; with no heads of one of
  *      them its pointers are not looked at.  q_out may be q itself (the same pointer and strides), k_out
