@@ -216,7 +216,8 @@ __global__ __launch_bounds__((64 * S::NW), 2) void cached_attn(AttnArgs a, Cache
     int row[NQ], pos[NQ], lo[NQ];
     bool empty[NQ];
     half8_t q[NQ][J][2][P];
-    float slope[NQ], back[NQ];   // back: what undoes the row's power of two, with the score's scale
+    float slope[NQ];
+    int back[NQ];   // the exponent that undoes the row's power of two
     const float scale2 = score_scale<CAP>(a), cap2 = a.cap * LOG2E;
 #pragma unroll
     for (int m = 0; m < NQ; ++m) {
@@ -255,7 +256,7 @@ __global__ __launch_bounds__((64 * S::NW), 2) void cached_attn(AttnArgs a, Cache
             }
         top = gmax(top);
         const int ex = min((int)(__float_as_uint(top) >> 23), 254) - 127;
-        back[m] = __builtin_amdgcn_ldexpf(scale2, ex - Q_TOP);
+        back[m] = ex - Q_TOP;
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -277,7 +278,7 @@ __global__ __launch_bounds__((64 * S::NW), 2) void cached_attn(AttnArgs a, Cache
     }
     // one block, its operands given by kf(kb, j, half of the 16 values) and vf(d, half of the 16 keys)
     auto block = [&](int j0, const Place& at, auto&& kf, auto&& vf) {
-        const float ks = power(exponent_of_scale(at.ks));
+        const int ke = exponent_of_scale(at.ks);
         const int ve = exponent_of_scale(at.vs);
         f32x4 s[4][NQ];
 #pragma unroll
@@ -304,7 +305,8 @@ __global__ __launch_bounds__((64 * S::NW), 2) void cached_attn(AttnArgs a, Cache
             // Scores in base 2 with the block's vs, less the row's base: the running maximum as it was
             // when a score last passed it by SLACK.
             const float base = mx[m] == -INFINITY ? 0.f : mx[m];
-            const float by = back[m] * ks;
+            // (all powers of two at once, and no more than float32 holds: a product of 0 stays 0)
+            const float by = fminf(__builtin_amdgcn_ldexpf(scale2, back[m] + ke), 3.402823466e38f);
             const float shift = (BIAS ? slope[m] * (float)(j0 + 16 * g - pos[m]) : 0.f) + (vexp + HEAD - base);
 #pragma unroll
             for (int kb = 0; kb < 4; ++kb)
