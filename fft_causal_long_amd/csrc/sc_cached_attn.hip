@@ -587,22 +587,38 @@ int tile_rows(const AttnArgs& a)
     return w128 > (a.D <= 64 ? FILL : FILL / 2) || (a.nrow > 64 && 2 * w64 <= FILL) ? 128 : 64;
 }
 
-// Key splits while the rows do not fill the GPU, each of at least SPLIT_MIN keys; the second launch costs
-// what few of them gain (one token, 4 key heads, whole calls: 1000 keys 16.4 us split and 11.8 not, 2500
-// keys 16.4 and 13.3, 3500 keys 16.5 in 6 parts and not).  8 caches of up
-// to 65536, 4 key heads, one token: 768 workgroups 44.0 us, 512 43.5, 1024 45.5, 1536 44.5; 64 caches of up
-// to 4096 47, 48, 46, 47; 4 of up to 10007, 12 heads, 5 tokens, float32: 21, 21, 24, 24.
+// Key splits while the rows do not fill the GPU, each of at least SPLIT_MIN keys.  8 caches of up to 65536,
+// 4 key heads, one token: 768 workgroups 44.0 us, 512 43.5, 1024 45.5, 1536 44.5; 64 caches of up to 4096 47,
+// 48, 46, 47; 4 of up to 10007, 12 heads, 5 tokens, float32: 21, 21, 24, 24.
+// Few parts of few rows gain less than the second launch costs, whether the keys or the grid limit them.  One
+// sequence, 4 key heads of 64, unsplit and in as many parts as it has 512 keys: 1000 keys 12.1 us and 16.8,
+// 2500 (5 parts) 14.3 and 16.8, 3500 (6) 17.9 and 16.9.  B sequences of half to all of T tokens, 4 key heads,
+// unsplit and in the parts that the grid has room for (B 47: 5, 48: 4, 64: 3, 96: 2):
+//     D x T          B 47           48             64             96
+//     64 x 4096      21.5 and 22.8  21.1 and 21.5  25.8 and 28.5  28.8 and 33.6
+//     128 x 4096     32.2 and 35.9  32.4 and 37.3  41.0 and 45.6  58.5 and 63.2
+//     64 x 8192      35.6 and 33.3  35.5 and 32.5  40.5 and 45.6  54.9 and 60.6
+//     128 x 8192     57.6 and 59.2  58.1 and 62.6  79.8 and 81.8  110 and 113
+//     64 x 16384     64.5 and 61.1  64.3 and 58.3  79.5 and 79.5  113 and 114
+//     128 x 16384    109 and 109    111 and 112    167 and 150    219 and 212
+//     64 x 65536     (5.6 TB/s)     241 and 212    342 and 311    410 and 390
+//     128 x 65536    (6.2 TB/s)     421 and 420    590 and 545    794 and 766
+// (39 sequences of 8192, 5 parts: 34.5 and 29.1, 53.7 and 51.0.)
 constexpr int64_t FILL_FEW = 768, SPLIT_MIN = 512;
-constexpr int64_t SPLIT_LEAST = 5, SPLIT_MAX = NT;   // the join weighs one split a thread
+constexpr int64_t SPLIT_MAX = NT;   // the join weighs one split a thread
+constexpr int64_t SPLIT_FROM = 3000;   // keys
+int64_t least_room(int64_t keys) { return keys >= 16384 ? 2 : keys >= 8192 ? 5 : 6; }
 
 int splits(const AttnArgs& a, int sinks)
 {
     const int bm = tile_rows(a);
-    const int64_t wgs = (a.nrow + bm - 1) / bm * (int64_t)a.nbh, fill = a.nrow <= FEW ? FILL_FEW : FILL;
+    const bool few = a.nrow <= FEW;
+    const int64_t wgs = (a.nrow + bm - 1) / bm * (int64_t)a.nbh, fill = few ? FILL_FEW : FILL;
     const int64_t keys = std::min<int64_t>(a.Lk, (int64_t)a.window + sinks + std::min<int64_t>(a.Lq, bm));
     if (wgs <= 0 || 2 * wgs > fill) return 1;
-    const int64_t n = std::min<int64_t>({(fill + wgs - 1) / wgs, keys / SPLIT_MIN, SPLIT_MAX});
-    return n < (a.nrow <= FEW ? SPLIT_LEAST : 2) ? 1 : (int)n;
+    const int64_t room = (fill + wgs - 1) / wgs;   // parts that the grid has room for
+    if (few && (keys < SPLIT_FROM || room < least_room(keys))) return 1;
+    return (int)std::max<int64_t>(1, std::min<int64_t>({room, keys / SPLIT_MIN, SPLIT_MAX}));
 }
 
 template <class IO, Code CODE, int J, class S>

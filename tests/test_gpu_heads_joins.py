@@ -50,3 +50,22 @@ def test_a_row_of_nan_is_nan_and_alone(sc, dtype, code, Lq):
         assert torch.equal(o, want) and torch.equal(lse, wl)
         o, lse = sc.cached_attention(q, c, lengths(0), lse=True)
         assert torch.isneginf(lse).all() and o.eq(0).all()
+
+
+@pytest.mark.parametrize("Hkv,want", [(192, 4), (256, 3), (384, 2)])
+def test_parts_that_the_grid_limits(sc, Hkv, want):
+    # many key heads over a long cache: few parts each
+    print("case attn8 grid parts", Hkv, flush=True)
+    T, D = 16400, 16
+    gen = torch.Generator(device=DEV).manual_seed(Hkv)
+    c = sc.KVCache(1, T, Hkv, D, "int8", device=DEV)
+    k, v, q = (torch.randn(1, n, Hkv, D, generator=gen, device=DEV) for n in (T, T, 1))
+    sc.cache_write(c, k, v, lengths(T))
+    assert parts(sc, c, 1, Hkv, sc.KIND_F32) == want
+    for n in (T, 100, 9000):
+        o, lse = sc.cached_attention(q, c, lengths(n), lse=True)
+        heads = [0, 1, Hkv // 2, Hkv - 1]
+        kx, vx = (f64(t[:, :, heads]) for t in sc.cache_read(c, n, lengths(n), torch.float32))
+        (ro, rl), (bo, bl) = ref.cached_attention(f64(q[:, :, heads]), kx, vx, [n], 0.25)
+        check(o[:, :, heads], ro, bo, "f32", "o")
+        check(lse[:, heads], rl, bl, "f32", "lse")
