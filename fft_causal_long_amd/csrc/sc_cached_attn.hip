@@ -16,7 +16,8 @@
 // of the call (2048 tokens after 6144, 16 heads of 128 on 4: 214 us for 172; B 8, 1024 tokens over 4096, 16
 // heads of 64: 236 for 173; but one token over the caches of the first call below: 45.3 for 43.8).  A
 // block's vs goes into the weights' exponent, w = 2^(s + log2 vs - base), so that every weight is
-// relative to the row's largest contribution to o, whatever the scales; the sum takes w / vs.
+// relative to the row's largest contribution to o, whatever the scales, and off by 2^-32 of that at most
+// besides (half precision ends at 2^-24, the base stands for 2^HEAD); the sum takes w / vs.
 // The heads that share a key head are packed into one row axis, scores are made transposed (keys x
 // rows) and the blocks' byte order is that of the operands (sc_cache.h), so a score block, rounded, is
 // the operand of the second product and codes go from memory to the products without an exchange.

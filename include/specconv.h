@@ -604,8 +604,11 @@ sc_status sc_qk_norm_rotary_bwd(sc_kind kind, const sc_qk* a, const void* dq_out
  *      A row that sees nothing gives o = 0, lse = -infinity.  Products run on the codes in half precision
  *      with float32 sums: a query row enters scaled by a power of two (bfloat16 exact down to 2^-29 of
  *      its largest value, float32 as two halves), a weight as two halves, 22 bits, in float32 and where
- *      Lq H / Hkv <= 16, else as one, 11 bits.  Cached values of existing positions must be finite (an
- *      e4m3 NaN may reach other rows).  H a multiple of Hkv; ws as for sc_causal_attn,
+ *      Lq H / Hkv <= 16, else as one, 11 bits.  A weight is held with its block's v_scale, and no finer
+ *      than 2^-32 of the largest such product of the row: where one block's values are 2^20 times the
+ *      others', o's channels that are small in that block have fewer bits.  Cached values of existing
+ *      positions must be finite (an e4m3 NaN may reach other rows); a query row of NaN gives NaN in its
+ *      o and lse.  H a multiple of Hkv; ws as for sc_causal_attn,
  *      sc_cached_attn_workspace_bytes(kind, c, a) bytes.
  */
 #define SC_CACHE_BLOCK 64
