@@ -472,13 +472,14 @@ __global__ __launch_bounds__(NT) void qk_pairs(QkArgs a)
 }
 
 // dw = the workgroups' sums added: 4 columns a workgroup, 64 threads a column, whose loads are all in
-// flight at once (up to 1024 parts: 16 a thread).
+// flight at once (up to 1024 parts: 16 a thread).  In 64 bits: a part adds a few rows, but there are up to
+// 2048 parts, whose sum may be small beside them.
 template <class IO>
 __global__ __launch_bounds__(NT) void qk_sum(QkArgs a)
 {
-    __shared__ float sum[NT];
+    __shared__ double sum[NT];
     const int at = blockIdx.x * 4 + threadIdx.x % 4, s = at >= a.D;
-    float x = 0.f;
+    double x = 0.0;
     if (at < 2 * a.D) {
         const float* p = a.part + (s ? (int64_t)a.wgs[0] * a.D : 0) + (at - s * a.D);
         const int parts = (int)a.wgs[s];
@@ -494,7 +495,7 @@ __global__ __launch_bounds__(NT) void qk_sum(QkArgs a)
     }
     if (threadIdx.x >= 4 || at >= 2 * a.D) return;
     typename IO::T* out = (typename IO::T*)a.dw[at < a.D ? 0 : 1];
-    if (out) IO::store(out, at % a.D, sum[threadIdx.x]);
+    if (out) IO::store(out, at % a.D, (float)sum[threadIdx.x]);
 }
 
 // Tokens of a turn (of one sequence): so many that the turns fill the GPU several times over, up to what

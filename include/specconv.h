@@ -546,7 +546,8 @@ sc_status sc_causal_attn_bwd(sc_kind kind, const sc_attn* a, const void* dout, c
  *  sc_qk_norm_rotary_bwd -- for the output gradients dq_out, dk_out (strides q_out, k_out), from the
  *      inputs q, k: dq, dk, and the gradients of the weights dwq, dwk (D values, or null: not wanted; of
  *      a null weight: of ones).  ws: sc_qk_norm_rotary_workspace_bytes(kind, a) bytes with dwq or dwk,
- *      else 0.  Without tokens or heads dwq and dwk are set to zero.
+ *      else 0.  They are float32 sums of a workgroup's rows, added in 64 bits.  Without tokens or heads
+ *      dwq and dwk are set to zero.
  * Strides are in elements, {batch, token, head}; the D values are contiguous, D <= 512.  Rows that all
  * start 16-byte aligned, with D (and, for halves, R) a multiple of 32 bytes, are moved in vectors; any
  * others work, slower.  A row of NaN or infinity affects itself (and dw) only.
