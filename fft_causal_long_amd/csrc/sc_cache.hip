@@ -11,7 +11,8 @@
 //
 // Measured (MI355X): B 4, 8192 tokens, 4 heads of 128 bf16, int8: 20.5 us written (4.9 TB/s; a large copy
 // moves 5.4), 18 read back (5.6); B 8, 4096 tokens, 16 heads of 64 bf16, e4m3 49 (4.1) and 33 (6.1): rows
-// of 128 bytes a head.  k and v of a block in one workgroup took 53 for 49; the workgroups of a block's heads
+// of 128 bytes a head.  The first in float32: 39 (4.3) and 47 (3.5: each lane stores 64 bytes in four
+// pieces, so a wave's stores lie 64 bytes apart).  k and v of a block in one workgroup took 53 for 49; the workgroups of a block's heads
 // on one die 2 us less there and 2 more in the first; 20 was 30 with the codes of every value checked and
 // clamped, since the arithmetic bound it.
 

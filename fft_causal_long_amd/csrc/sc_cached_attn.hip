@@ -29,18 +29,25 @@
 //
 // Measured (MI355X; a large copy moves 5.4 TB/s, reads alone up to 6.3, a half-precision product of 8192^3
 // reaches 1200 TFLOP/s), whole calls:
-//  * 8 sequences over ragged caches of up to 65536, one token, 16 heads of 64 on 4, int8: 43 us, of it 38 the
-//    kernel (5.5 TB/s of the codes) and 4.6 the join: bound by the codes' bytes.  Loads past the caches took it
-//    there from 50 (44 the kernel).  The same in bfloat16 caches: 88.
-//  * 32 sequences, window 256 and 4 sinks, 16 heads of 64, e4m3 in a pool: 9 us of kernel, five blocks a
+//  * 8 sequences over ragged caches of up to 65536, one token, 16 heads of 64 on 4, int8: 45 us, of it 40 the
+//    kernel (5.3 TB/s of the codes) and 4.6 the join: bound by the codes' bytes.  Loads past the caches took
+//    the call from 50 to 44 (and the weights' second half to 45).  float32 45; the same in bfloat16 caches: 91.
+//  * 64 sequences of 2048 to 4096, one token, 16 heads of 128 on 4, e4m3: 43 us for 202 MB (4.7 TB/s): 256
+//    workgroups that each walk one row's blocks, one wave a SIMD.
+//  * 32 sequences, window 256 and 4 sinks, 16 heads of 64, e4m3 in a pool: 10 us of kernel, five blocks a
 //    workgroup: the chain length, table, codes, scores.
-//  * 4 sequences of up to 10007, 5 tokens, 12 heads of 64, float32, capped: 17 us and 4 of join for 50 MB:
+//  * 4 sequences of up to 10007, 5 tokens, 12 heads of 64, float32, capped: 18 us and 4 of join for 50 MB:
 //    the same chain before the bytes, three blocks a wave.
+//  * 5 and 16 tokens over the first call's caches (20 and 64 packed rows): 74 and 78 us, one block of codes
+//    ahead a workgroup where one row has one a wave, and at 20 rows two waves of four without rows.
 //  * 2048 tokens over 8192, 16 heads of 128 on 4, int8: 172 us, 700 TFLOP/s of the products that the mask
-//    leaves (sc_causal_attn on bfloat16: 228).  Vector instructions (176 for 16 x 64 scores, of them 64 the
-//    conversion, 16 exponentials) and the products share the issue: 46% and 26% of the cycles at 1.7 waves a
-//    SIMD.  Four waves a SIMD (the keys of a block in two halves) changed nothing, the next block's conversion
-//    placed beside the first product made it 198, each wave converting for itself 257.
+//    leaves (sc_causal_attn on bfloat16: 222 to 228); e4m3 178; float32, of two halves each, 237.  Three
+//    things take turns: vector instructions (176 for 16 x 64 scores, of them 64 the conversion, 16
+//    exponentials), 47% of the cycles; matrix instructions, 27%; and LDS, of which a wave of 16 rows reads an
+//    operand of 1 KB for each product, 32 a block, and writes 8: 29 and 7 MB a CU, 95 and 24 us of the 172
+//    at 128 bytes a clock.  At 1.7 waves a SIMD they do not overlap fully.  Four waves a SIMD (the keys of a
+//    block in two halves) changed nothing, the next block's conversion placed beside the first product made
+//    it 198, each wave converting for itself 257.
 
 #include <hip/hip_runtime.h>
 

@@ -19,7 +19,11 @@
 //
 // Measured (MI355X; a large copy moves 5.4 TB/s, two reads and a write 5.97; inputs past every cache), whole
 // calls: B 8, L 4096, 16 + 16 heads of 64 bf16, columns of one projection: forward 55 us (4.9 TB/s), backward
-// 84 (4.8), of it 5 the second kernel's; B 1, L 8192, 16 + 4 heads of 128 float32 backward 58 (4.3).  Steps,
+// 85 (4.8), of it 5 the second kernel's; B 1, L 8192, 16 + 4 heads of 128 float32 backward 58 (4.3), of it 7;
+// B 4, L 4096, 16 + 4 heads of 128 float32 forward 60 (5.6).  Short prompts are far from that: up to 8191
+// tokens a workgroup has one (the rule at the end of this file), which leaves most of its rows' places empty
+// where the heads are few: 4096 tokens of 16 + 4 heads of 64 bf16 17 us for 21 MB, 2002 of 12 + 12 float32
+// in pairs 10 for 25 MB.  The second kernel reads each 128-byte line of the parts from eight workgroups.  Steps,
 // with inputs partly in the last-level cache: a 64-bit division a row 54 / 103, walks without it and the
 // tensors' numbers taken out of the loop 51.6 / 98 (an index into the call's arguments is a load a row),
 // 8-byte vectors backward 89, the rest 50 / 85.

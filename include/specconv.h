@@ -549,8 +549,10 @@ sc_status sc_causal_attn_bwd(sc_kind kind, const sc_attn* a, const void* dout, c
  *      else 0.  They are float32 sums of a workgroup's rows, added in 64 bits.  Without tokens or heads
  *      dwq and dwk are set to zero.
  * Strides are in elements, {batch, token, head}; the D values are contiguous, D <= 512.  Rows that all
- * start 16-byte aligned, with D (and, for halves, R) a multiple of 32 bytes, are moved in vectors; any
- * others work, slower.  A row of NaN or infinity affects itself (and dw) only.
+ * start 16-byte aligned are moved in vectors of 16, 8 or 4 bytes (two elements at least, those up to D =
+ * 256), the longest of which D and, for halves, R hold an even number; any others value by value, slower.
+ * mean(x^2) is a float32: rows of values past 2^59 may give 0, and without eps those below 2^-60 lose bits.
+ * A row of NaN or infinity affects itself (and dw) only.
  */
 typedef struct sc_qk {
     int64_t B, L, H, Hkv, D, R;
@@ -576,8 +578,8 @@ sc_status sc_qk_norm_rotary_bwd(sc_kind kind, const sc_qk* a, const void* dq_out
  *     e = the smallest in -60 .. 60 with max |x| <= Q 2^e over the block,
  *     code = x / 2^e rounded once (ties to even) to an integer of -127 .. 127 (SC_CODE_I8, Q = 127) or
  *     to an e4m3 value (SC_CODE_E4M3, Q = 448: 4 exponent and 3 mantissa bits, subnormals down to 2^-9).
- * Infinities count as the largest code and not towards max |x| (as do values past Q 2^60); NaN is 0 in
- * int8 and stays NaN in e4m3.  When tokens are appended to a block that holds older ones, its exponent
+ * Infinities take the largest code and do not count towards max |x|; finite values past Q 2^60 do (e is 60
+ * then) and take the largest code.  NaN is 0 in int8 and stays NaN in e4m3.  When tokens are appended to a block that holds older ones, its exponent
  * is the larger of the one it has and the new tokens'; where it grows, the older codes are rounded again
  * at the new scale.
  *
