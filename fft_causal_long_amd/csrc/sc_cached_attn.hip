@@ -609,8 +609,8 @@ int tile_rows(const AttnArgs& a)
 //     128 x 8192     57.6 and 59.2  58.1 and 62.6  79.8 and 81.8  110 and 113
 //     64 x 16384     64.5 and 61.1  64.3 and 58.3  79.5 and 79.5  113 and 114
 //     128 x 16384    109 and 109    111 and 112    167 and 150    219 and 212
-//     64 x 65536     (5.6 TB/s)     241 and 212    342 and 311    410 and 390
-//     128 x 65536    (6.2 TB/s)     421 and 420    590 and 545    794 and 766
+//     64 x 65536     - and 213      241 and 212    342 and 311    410 and 390
+//     128 x 65536    - and 387      421 and 420    590 and 545    794 and 766
 // (39 sequences of 8192, 5 parts: 34.5 and 29.1, 53.7 and 51.0.)
 constexpr int64_t FILL_FEW = 768, SPLIT_MIN = 512;
 constexpr int64_t SPLIT_MAX = NT;   // the join weighs one split a thread
