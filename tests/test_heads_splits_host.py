@@ -23,7 +23,7 @@ def test_long_caches_are_split_whatever_the_number_of_sequences(sc):
 
 def test_short_caches_are_split_where_it_pays(sc):
     # a few parts of short caches cost a launch more than they save, whatever limits them
-    assert [parts(sc, 1, T, 4, 64, 16) for T in (64, 1000, 2500, 3000, 3072, 3584, 10240)] == [1, 1, 1, 5, 6, 7, 20]
+    assert [parts(sc, 1, T, 4, 64, 16) for T in (64, 1000, 2500, 3000, 3100, 3584, 10240)] == [1, 1, 1, 5, 6, 7, 20]
     for D in (64, 128):
         assert [parts(sc, B, 4096, 4, D, 16) for B in (8, 38, 39, 47, 48, 64, 96)] == [8, 6, 1, 1, 1, 1, 1]
         assert [parts(sc, B, 8192, 4, D, 16) for B in (8, 38, 39, 47, 48, 64, 96)] == [16, 6, 5, 5, 1, 1, 1]
